@@ -362,6 +362,120 @@ int w4a16_spec_verify(const void *p_target, const void *p_draft, const void *dra
                       void *workspace, size_t workspace_bytes, void *n_accepted, void *token,
                       void *stream);
 
+/* Fused linear layers.  The products of w4a16_gemm with what a layer does to
+ * them before they are stored, in the same kernels and on the same paths:
+ *   Z = X . W_hat^T + bias,   Y = residual + act(Z).
+ * The fp32 sums get bias, activation and residual in fp32 and Y is rounded to
+ * the activations' type once.  An epilogue belongs to each problem: */
+enum {
+  W4A16_ACT_NONE = 0,
+  W4A16_ACT_RELU = 1,      /* max(z, 0); derivative 0 at z = 0                   */
+  W4A16_ACT_SILU = 2,      /* z / (1 + exp(-z))                                  */
+  W4A16_ACT_GELU = 3,      /* z * erfc(-z / sqrt 2) / 2                          */
+  W4A16_ACT_GELU_TANH = 4  /* z * (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2  */
+};
+
+typedef struct w4a16_epilogue {
+  const void *bias;      /* [N] or NULL                                          */
+  const void *residual;  /* [M][N] or NULL; may be Y itself                      */
+  void *preact;          /* [M][N] or NULL: receives Z, rounded once             */
+  int32_t act;           /* W4A16_ACT_*, else EUNSUPPORTED                       */
+} w4a16_epilogue;
+
+/* Y of several independent problems, each with its epilogue (bias, residual and
+ * preact of the problem's activation type, 16-byte aligned).  problems and
+ * epilogues are host arrays of `count` entries; other arguments, the workspace,
+ * the sharing of launches and the errors are those of w4a16_gemm_grouped_ws.
+ * Outputs (Y, preact) must not overlap each other or any input, except that
+ * residual may be the same problem's Y.  Asynchronous on `stream`. */
+int w4a16_linear_workspace_size(const w4a16_problem *problems, const w4a16_epilogue *epilogues,
+                                int count, size_t *bytes);
+int w4a16_linear(const w4a16_problem *problems, const w4a16_epilogue *epilogues, int count,
+                 void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gated feed-forward block in one pass over X and both weights:
+ *   G = X . Wg_hat^T + bias_gate,  U = X . Wu_hat^T + bias_up,  H = act(G) * U.
+ * gate and up are the two products: same X, s, M, N, K, dtype and wbits (EINVAL
+ * otherwise).  Their Y receive G and U, each rounded once, for a backward pass:
+ * both set or both NULL.  H [M][N] is formed in fp32 from the unrounded sums
+ * and rounded once.  H, the Y and the biases ([N] or NULL) are of the
+ * activations' type and 16-byte aligned; outputs must not overlap each other
+ * or any input.  The workspace is optional, as for w4a16_gemm_grouped_ws.
+ * Asynchronous on `stream`. */
+int w4a16_gated_workspace_size(const w4a16_problem *gate, const w4a16_problem *up, size_t *bytes);
+int w4a16_gated(const w4a16_problem *gate, const w4a16_problem *up, const void *bias_gate,
+                const void *bias_up, int act, void *H, void *workspace, size_t workspace_bytes,
+                void *stream);
+
+/* Transposed copy of a packed weight, for the backward product dY . W_hat,
+ * whose sums run over N: made once and kept beside the packed weight.  The
+ * codes are the packed layout of the [K][Np] matrix q^T, Np = N rounded up to a
+ * multiple of 128 (columns N..Np-1 hold code 0): tile (b, g) covers the 16
+ * input features 16b..16b+15 and the 128 output rows of group g, at
+ * (g * K/16 + b) * 1024 (2048 for INT8 codes).  meta holds, for each group g of
+ * 128 output rows and each quantization group u of 128 input features, 512
+ * bytes at (g * K/128 + u) * 512: the 128 fp16 scales of rows 128g.. in input
+ * group u, then for each row j of them z + 1024 (INT4 codes: z + 64 where
+ * j % 4 is 2 or 3) as fp16, both exact; rows past N have scale 0.
+ * w4a16_transposed_sizes gives the byte sizes (wbits 4 or 8; N <= 2^22, else
+ * EINVAL).  w4a16_transpose writes both buffers (16-byte aligned, zero points
+ * integers of the packer's range 0..15 or 0..255); asynchronous on `stream`. */
+int w4a16_transposed_sizes(int64_t N, int64_t K, int wbits, size_t *wt_bytes, size_t *meta_bytes);
+int w4a16_transpose(const void *Wq, const void *scales, const void *zeros, int64_t N, int64_t K,
+                    int wbits, void *Wt, void *meta, void *stream);
+
+/* Backward of one linear layer with frozen (packed) weights:
+ *   dZ = dY * act'(Z),   dbias = sum over rows of dZ.
+ * dY [M][N]; Z = preact [M][N] as the forward kept it, and dZ [M][N] output
+ * (it may be dY or preact itself), both required unless act is
+ * W4A16_ACT_NONE, where dZ is dY and both must be NULL; dbias: fp32 [N], or
+ * NULL.  dZ is rounded once to the activations' type, and the product below
+ * reads the rounded values; dbias sums the unrounded ones in fp32, in a fixed
+ * order.  Wt, meta: the layer's transposed weight. */
+typedef struct w4a16_backward_term {
+  const void *dY;
+  const void *preact;
+  void *dZ;
+  void *dbias;
+  const void *Wt;
+  const void *meta;
+  int64_t N;
+  int32_t act;
+  int32_t wbits;         /* 0 or 4, or 8                                         */
+} w4a16_backward_term;
+
+/* dX [M][K] = add + s * (sum over terms of dZ . D), D[n][k] = (q - z) * scale:
+ * the gradient of the activations that all `count` layers (1 to 4, say q, k
+ * and v; one s, or NULL) read.  add [M][K] (a gradient from elsewhere, or NULL)
+ * may be dX itself.  Each D is rounded once to the activations' type (dtype,
+ * W4A16_DTYPE_*); sums are fp32, s and add are applied in fp32, and dX is
+ * rounded once.  Outlier weights have no transposed form.  All terms share
+ * wbits (EUNSUPPORTED otherwise).  M >= 0, dX may be NULL to get only dZ and
+ * dbias.  Outputs must not overlap each other or any input except as said.
+ * workspace: w4a16_backward_workspace_size() bytes (depends on M, K, dtype and
+ * the terms' N, act, dbias and whether dX is NULL; may be 0), 256-byte aligned;
+ * EINVAL if smaller.  Asynchronous on `stream`. */
+int w4a16_linear_backward_workspace_size(const w4a16_backward_term *terms, int count, int64_t M,
+                                         int64_t K, int dtype, size_t *bytes);
+int w4a16_linear_backward(const w4a16_backward_term *terms, int count, const void *s,
+                          const void *add, void *dX, int64_t M, int64_t K, int dtype,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
+/* Backward of the gated block, from dH and the G and U that its forward kept:
+ *   dG = dH * U * act'(G),  dU = dH * act(G),  dX = add + s * (dG . Dg + dU . Du),
+ * dbias_gate and dbias_up the fp32 row sums of dG and dU.  gate and up carry
+ * Wt, meta, N, wbits and dbias (or NULL) of the two weights, preact = G or U,
+ * and dZ = the output for dG or dU (each may be the same term's preact); the
+ * gate's act is the block's (act must be 0 in up) and both dY are ignored.
+ * Everything else as w4a16_linear_backward. */
+int w4a16_gated_backward_workspace_size(const w4a16_backward_term *gate,
+                                        const w4a16_backward_term *up, int64_t M, int64_t K,
+                                        int dtype, size_t *bytes);
+int w4a16_gated_backward(const void *dH, const w4a16_backward_term *gate,
+                         const w4a16_backward_term *up, const void *s, const void *add, void *dX,
+                         int64_t M, int64_t K, int dtype, void *workspace, size_t workspace_bytes,
+                         void *stream);
+
 /* Which path AUTO takes for this shape (host only; no GPU call). */
 int w4a16_select_path(int64_t M, int64_t N, int64_t K);
 

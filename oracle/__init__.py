@@ -53,6 +53,8 @@ readings Q1-Q5 are in that module.
 The outlier side path (``outliers``, [mhpq] sec.2.2) keeps the largest |W / s|
 in fp16 and quantizes the rest with those positions set to 0; its readings
 O1-O5 are in that module.
+``fused`` holds the fused linear layers (bias, activation, residual, gated pair), their
+gradients with the weights held fixed, and the transposed copy the backward reads.
 Pins: every function here is checked by tests against facts the pages or the
 mathematics fix (bound, grid reconstruction, byte counts, brute force in exact
 rationals, integer special case); see tests/test_oracle_*.py.
@@ -63,7 +65,7 @@ from .layout import (META_QUAD, TILE_BYTES, TILE_BYTES8, TILE_ROWS, byte_address
                      meta_index, nibble_address, pack_codes, pack_codes8, pack_meta, unpack_codes,
                      unpack_codes8, unpack_meta)
 from .matmul import dequantize, gemm
-from . import accounting, exact, gptq, outliers, spec
+from . import accounting, exact, fused, gptq, outliers, spec
 
 __all__ = [
     "GRANULARITIES", "GROUP", "QMAX", "NonFiniteInput", "OracleError", "QuantResult", "ScaleOverflow",
@@ -71,5 +73,5 @@ __all__ = [
     "meta_index", "nibble_address",
     "pack_codes", "pack_meta", "unpack_codes", "unpack_meta", "dequantize", "gemm",
     "TILE_BYTES8", "byte_address8", "pack_codes8", "unpack_codes8",
-    "accounting", "exact", "gptq", "outliers", "spec",
+    "accounting", "exact", "fused", "gptq", "outliers", "spec",
 ]

@@ -34,12 +34,17 @@ __all__ = [
     "w4a16_outlier_workspace_size", "page_outlier_count", "DTYPE_F16", "DTYPE_BF16",
     "w4a16_quantize_pack_gptq", "w4a16_gemm_grouped_static", "STATIC_SCRATCH_BYTES",
     "SHARED_SCRATCH_BYTES",
+    "ACT_NONE", "ACT_RELU", "ACT_SILU", "ACT_GELU", "ACT_GELU_TANH", "Epilogue", "LinearCall",
+    "w4a16_linear", "GatedCall", "w4a16_gated", "TransposedWeight", "w4a16_transpose",
+    "BackwardTerm", "LinearBackwardCall", "w4a16_linear_backward", "GatedBackwardCall",
+    "w4a16_gated_backward",
 ]
 
 GROUP = 128
 PATH_AUTO, PATH_SKINNY, PATH_TILED, PATH_SKINNY_WINDOW = 0, 1, 2, 3
 QUANT_ASYM, QUANT_SYM, QUANT_ASYM_CHANNEL, QUANT_ASYM_TENSOR, QUANT_ASYM8 = 0, 1, 2, 3, 4
 DTYPE_F16, DTYPE_BF16 = 0, 1
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2, 3, 4
 STATUS = {0: "W4A16_OK", -1: "W4A16_EINVAL", -2: "W4A16_EALIGN", -3: "W4A16_EUNSUPPORTED",
           -4: "W4A16_ENONFINITE", -5: "W4A16_ERANGE", -6: "W4A16_EHIP", -7: "W4A16_ESCRATCH"}
 STATIC_SCRATCH_BYTES = 64 << 20   # W4A16_STATIC_SCRATCH_BYTES
@@ -53,7 +58,11 @@ EXPORTED_SYMBOLS = ("w4a16_packed_sizes", "w4a16_packed_sizes_mode", "w4a16_quan
                     "w4a16_gptq_workspace_size", "w4a16_quantize_pack_gptq",
                     "w4a16_quantize_pack_outliers", "w4a16_spec_verify",
                     "w4a16_spec_verify_workspace_size", "w4a16_select_path",
-                    "w4a16_strerror", "w4a16_version")
+                    "w4a16_strerror", "w4a16_version",
+                    "w4a16_linear", "w4a16_linear_workspace_size", "w4a16_gated",
+                    "w4a16_gated_workspace_size", "w4a16_transposed_sizes", "w4a16_transpose",
+                    "w4a16_linear_backward", "w4a16_linear_backward_workspace_size",
+                    "w4a16_gated_backward", "w4a16_gated_backward_workspace_size")
 
 
 class Problem(ctypes.Structure):
@@ -63,6 +72,19 @@ class Problem(ctypes.Structure):
                 ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
                 ("o_row_ptr", ctypes.c_void_p), ("o_col", ctypes.c_void_p),
                 ("o_val", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("wbits", ctypes.c_int32)]
+
+
+class EpilogueStruct(ctypes.Structure):
+    """Mirror of the C struct w4a16_epilogue."""
+    _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+                ("preact", ctypes.c_void_p), ("act", ctypes.c_int32)]
+
+
+class BackwardTermStruct(ctypes.Structure):
+    """Mirror of the C struct w4a16_backward_term."""
+    _fields_ = [("dY", ctypes.c_void_p), ("preact", ctypes.c_void_p), ("dZ", ctypes.c_void_p),
+                ("dbias", ctypes.c_void_p), ("Wt", ctypes.c_void_p), ("meta", ctypes.c_void_p),
+                ("N", ctypes.c_int64), ("act", ctypes.c_int32), ("wbits", ctypes.c_int32)]
 
 
 class W4A16Error(RuntimeError):
@@ -104,6 +126,19 @@ def lib() -> ctypes.CDLL:
     L.w4a16_gptq_workspace_size.argtypes = [i64, i64, i64, sz]
     L.w4a16_quantize_pack_gptq.argtypes = [vp, vp, i64, i64, vp, i64, ctypes.c_double, vp, vp, vp,
                                            vp, ctypes.c_size_t, vp]
+    pp, ep, bp = (ctypes.POINTER(Problem), ctypes.POINTER(EpilogueStruct),
+                  ctypes.POINTER(BackwardTermStruct))
+    ci, cs = ctypes.c_int, ctypes.c_size_t
+    L.w4a16_linear_workspace_size.argtypes = [pp, ep, ci, sz]
+    L.w4a16_linear.argtypes = [pp, ep, ci, vp, cs, vp]
+    L.w4a16_gated_workspace_size.argtypes = [pp, pp, sz]
+    L.w4a16_gated.argtypes = [pp, pp, vp, vp, ci, vp, vp, cs, vp]
+    L.w4a16_transposed_sizes.argtypes = [i64, i64, ci, sz, sz]
+    L.w4a16_transpose.argtypes = [vp, vp, vp, i64, i64, ci, vp, vp, vp]
+    L.w4a16_linear_backward_workspace_size.argtypes = [bp, ci, i64, i64, ci, sz]
+    L.w4a16_linear_backward.argtypes = [bp, ci, vp, vp, vp, i64, i64, ci, vp, cs, vp]
+    L.w4a16_gated_backward_workspace_size.argtypes = [bp, bp, i64, i64, ci, sz]
+    L.w4a16_gated_backward.argtypes = [vp, bp, bp, vp, vp, vp, i64, i64, ci, vp, cs, vp]
     L.w4a16_select_path.argtypes = [i64, i64, i64]
     L.w4a16_strerror.argtypes = [ctypes.c_int]
     L.w4a16_strerror.restype = ctypes.c_char_p
@@ -116,6 +151,10 @@ def lib() -> ctypes.CDLL:
                  "w4a16_spec_verify", "w4a16_spec_verify_workspace_size", "w4a16_select_path",
                  "w4a16_outlier_workspace_size", "w4a16_quantize_pack_outliers",
                  "w4a16_gptq_workspace_size", "w4a16_quantize_pack_gptq",
+                 "w4a16_linear_workspace_size", "w4a16_linear", "w4a16_gated_workspace_size",
+                 "w4a16_gated", "w4a16_transposed_sizes", "w4a16_transpose",
+                 "w4a16_linear_backward_workspace_size", "w4a16_linear_backward",
+                 "w4a16_gated_backward_workspace_size", "w4a16_gated_backward",
                  "w4a16_version"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
@@ -495,3 +534,315 @@ def w4a16_spec_verify(p_target, p_draft, draft, u_accept, u_sample, out=None, wo
     """Speculative-sampling verification of B sequences on the current stream; returns
     (n_accepted, token).  Arguments as for SpecVerifyCall."""
     return SpecVerifyCall(p_target, p_draft, draft, u_accept, u_sample, out, workspace)()
+
+
+# ---- fused linear layers and their backward passes -------------------------------------
+
+def _act_dtype(t, name):
+    """The activations' type of tensor t: torch.float16 or torch.bfloat16."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or t.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"{name} must be a float16 or bfloat16 tensor")
+    return t.dtype
+
+
+def _dtype_code(dtype):
+    return DTYPE_BF16 if dtype == _torch().bfloat16 else DTYPE_F16
+
+
+def _shaped_ptr(t, name, dtype, shape, device):
+    """Device pointer of an optional tensor of this type, shape and device."""
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    p = _dev_ptr(t, name, dtype)
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return p
+
+
+def _problem(X, pw, s, y_ptr, device):
+    torch = _torch()
+    if X.dim() != 2 or X.shape[1] != pw.K:
+        raise ValueError("X must be [M][K] with K matching the packed weight")
+    meta = (pw.N * (-(-(pw.K // GROUP) // 4) * 4),)
+    return Problem(
+        _dev_ptr(X, "X", X.dtype),
+        _shaped_ptr(pw.wq, "wq", torch.uint8, (pw.N * pw.K * pw.wbits // 8,), device),
+        _shaped_ptr(pw.scales, "scales", torch.float16, meta, device),
+        _shaped_ptr(pw.zeros, "zeros", torch.float16, meta, device),
+        _shaped_ptr(s, "s", torch.float16, (pw.K,), device), y_ptr, X.shape[0], pw.N, pw.K,
+        *pw.outlier_ptrs(), _dtype_code(X.dtype), pw.wbits)
+
+
+class _PreparedCall:
+    """One C call over fixed buffers on one device, with a workspace of its own (or a
+    caller's uint8 device tensor).  Calls that share a workspace must not overlap in time,
+    nor may replays of captured calls that share one."""
+
+    def _prepare(self, device, nbytes, workspace, stream):
+        torch = _torch()
+        self.device = device
+        self.stream = None if stream is None else ctypes.c_void_p(stream)
+        self.ws, self.ws_ptr, self.ws_bytes = None, None, 0
+        if nbytes == 0:
+            return
+        if workspace is None:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        elif (not workspace.is_cuda or workspace.dtype != torch.uint8 or workspace.device != device
+              or not workspace.is_contiguous() or workspace.numel() < nbytes):
+            raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {nbytes} "
+                             f"bytes on {device}")
+        self.ws, self.ws_ptr, self.ws_bytes = workspace, workspace.data_ptr(), nbytes
+
+    def _run(self, name, *args):
+        torch = _torch()
+        st = self.stream if self.stream is not None else _stream_handle(self.device)
+        if torch.cuda.current_device() == self.device.index:
+            rc = getattr(lib(), name)(*args, self.ws_ptr, self.ws_bytes, st)
+        else:
+            with torch.cuda.device(self.device):
+                rc = getattr(lib(), name)(*args, self.ws_ptr, self.ws_bytes, st)
+        if rc:
+            raise W4A16Error(rc, name)
+
+    @staticmethod
+    def _size(name, *args):
+        n = ctypes.c_size_t()
+        rc = getattr(lib(), name)(*args, ctypes.byref(n))
+        if rc:
+            raise W4A16Error(rc, name)
+        return n.value
+
+
+@dataclass
+class Epilogue:
+    """What a linear layer does to its product Z = X . dequant(pw)^T + bias before it is
+    stored: Y = residual + act(Z).  bias [N], residual [M][N] (may be Y itself) and preact
+    [M][N] (receives Z) are of X's type; act is one of the ACT_* constants."""
+    bias: "object" = None
+    act: int = ACT_NONE
+    residual: "object" = None
+    preact: "object" = None
+
+
+class LinearCall(_PreparedCall):
+    """A prepared w4a16_linear call.  Items are (X, PackedWeight, s or None, Y, Epilogue);
+    problems of one call share launches as in GroupedCall.  All tensors are on one device;
+    each call runs on the current stream, or on ``stream`` (a HIP stream handle)."""
+
+    def __init__(self, items, stream=None, workspace=None):
+        self.items = list(items)  # keep the tensors alive
+        n = len(self.items)
+        self.problems, self.epilogues = (Problem * n)(), (EpilogueStruct * n)()
+        device = self.items[0][0].device if n else None
+        for i, (X, pw, s, Y, e) in enumerate(self.items):
+            dt = _act_dtype(X, f"problem {i}: X")
+            shape = (X.shape[0], pw.N)
+            if X.device != device:
+                raise ValueError(f"problem {i}: X must be on {device}")
+            self.problems[i] = _problem(X, pw, s, _shaped_ptr(Y, "Y", dt, shape, device), device)
+            self.epilogues[i] = EpilogueStruct(
+                _shaped_ptr(e.bias, "bias", dt, (pw.N,), device),
+                _shaped_ptr(e.residual, "residual", dt, shape, device),
+                _shaped_ptr(e.preact, "preact", dt, shape, device), e.act)
+        nbytes = self._size("w4a16_linear_workspace_size", self.problems, self.epilogues, n)
+        self._prepare(device, nbytes, workspace, stream)
+
+    def __call__(self):
+        if self.items:
+            self._run("w4a16_linear", self.problems, self.epilogues, len(self.items))
+
+
+def w4a16_linear(X, pw: PackedWeight, s=None, bias=None, act=ACT_NONE, residual=None, out=None,
+                 preact=None):
+    """Y = residual + act(X . dequant(pw)^T + bias) on the current stream; X fp16 or bf16
+    [M][K].  preact, when given, receives the pre-activation for a backward pass."""
+    if out is None:
+        out = _torch().empty((X.shape[0], pw.N), dtype=X.dtype, device=X.device)
+    LinearCall([(X, pw, s, out, Epilogue(bias, act, residual, preact))])()
+    return out
+
+
+class GatedCall(_PreparedCall):
+    """A prepared w4a16_gated call: H = act(G) * U with G = X . dequant(gate)^T + bias_gate
+    and U = X . dequant(up)^T + bias_up, both products in one pass over X.  preact: a pair
+    of [M][N] tensors that receive G and U, or None."""
+
+    def __init__(self, X, gate, up, s, H, act=ACT_SILU, bias_gate=None, bias_up=None, preact=None,
+                 stream=None, workspace=None):
+        dt, device = _act_dtype(X, "X"), X.device
+        if (gate.N, gate.K, gate.wbits) != (up.N, up.K, up.wbits):
+            raise ValueError("gate and up must have the same shape and code width")
+        shape = (X.shape[0], gate.N)
+        G, U = preact if preact is not None else (None, None)
+        self.keep = (X, gate, up, s, H, bias_gate, bias_up, G, U)
+        self.gate = _problem(X, gate, s, _shaped_ptr(G, "preact[0]", dt, shape, device), device)
+        self.up = _problem(X, up, s, _shaped_ptr(U, "preact[1]", dt, shape, device), device)
+        self.args = (ctypes.byref(self.gate), ctypes.byref(self.up),
+                     _shaped_ptr(bias_gate, "bias_gate", dt, (gate.N,), device),
+                     _shaped_ptr(bias_up, "bias_up", dt, (gate.N,), device), act,
+                     _shaped_ptr(H, "H", dt, shape, device))
+        nbytes = self._size("w4a16_gated_workspace_size", *self.args[:2])
+        self._prepare(device, nbytes, workspace, stream)
+
+    def __call__(self):
+        self._run("w4a16_gated", *self.args)
+
+
+def w4a16_gated(X, gate: PackedWeight, up: PackedWeight, s=None, act=ACT_SILU, bias_gate=None,
+                bias_up=None, out=None, preact=None):
+    """H = act(X . dequant(gate)^T + bias_gate) * (X . dequant(up)^T + bias_up) on the
+    current stream.  preact: a pair of tensors that receive the two pre-activations."""
+    if out is None:
+        out = _torch().empty((X.shape[0], gate.N), dtype=X.dtype, device=X.device)
+    GatedCall(X, gate, up, s, out, act, bias_gate, bias_up, preact)()
+    return out
+
+
+@dataclass
+class TransposedWeight:
+    """Transposed copy of a PackedWeight for the backward passes (layout: w4a16_transpose in
+    include/w4a16.h)."""
+    wt: "object"
+    meta: "object"
+    N: int
+    K: int
+    wbits: int = 4
+
+
+def w4a16_transpose(pw: PackedWeight) -> TransposedWeight:
+    """The transposed copy that the backward passes read, made once per weight (on the
+    current stream).  Weights with fp16 outliers have none."""
+    torch = _torch()
+    if pw.outlier_ptrs()[0] is not None:
+        raise ValueError("weights with fp16 outliers have no transposed form")
+    a, b = ctypes.c_size_t(), ctypes.c_size_t()
+    rc = lib().w4a16_transposed_sizes(pw.N, pw.K, pw.wbits, ctypes.byref(a), ctypes.byref(b))
+    if rc:
+        raise W4A16Error(rc, "w4a16_transposed_sizes")
+    dev = pw.wq.device
+    meta = (pw.N * (-(-(pw.K // GROUP) // 4) * 4),)
+    src = (_shaped_ptr(pw.wq, "wq", torch.uint8, (pw.N * pw.K * pw.wbits // 8,), dev),
+           _shaped_ptr(pw.scales, "scales", torch.float16, meta, dev),
+           _shaped_ptr(pw.zeros, "zeros", torch.float16, meta, dev))
+    out = TransposedWeight(torch.empty(a.value, dtype=torch.uint8, device=dev),
+                           torch.empty(b.value, dtype=torch.uint8, device=dev), pw.N, pw.K,
+                           pw.wbits)
+    with torch.cuda.device(dev):
+        rc = lib().w4a16_transpose(*src, pw.N, pw.K, pw.wbits, _dev_ptr(out.wt, "wt"),
+                                   _dev_ptr(out.meta, "meta"), _stream_handle(dev))
+    if rc:
+        raise W4A16Error(rc, "w4a16_transpose")
+    return out
+
+
+@dataclass
+class BackwardTerm:
+    """One layer of a backward call: dZ = dY * act'(preact), dbias = column sums of dZ.
+    With ACT_NONE dZ is dY itself, and preact and dZ must be None.  dbias: fp32 [N] output
+    or None."""
+    dY: "object"
+    wt: TransposedWeight
+    act: int = ACT_NONE
+    preact: "object" = None
+    dZ: "object" = None
+    dbias: "object" = None
+
+    def struct(self, dt, shape, device):
+        torch = _torch()
+        w = self.wt
+        ng = -(-w.N // GROUP)
+        return BackwardTermStruct(
+            _shaped_ptr(self.dY, "dY", dt, shape, device),
+            _shaped_ptr(self.preact, "preact", dt, shape, device),
+            _shaped_ptr(self.dZ, "dZ", dt, shape, device),
+            _shaped_ptr(self.dbias, "dbias", torch.float32, (w.N,), device),
+            _shaped_ptr(w.wt, "wt", torch.uint8, (ng * GROUP * w.K * w.wbits // 8,), device),
+            _shaped_ptr(w.meta, "meta", torch.uint8, (ng * (w.K // GROUP) * 512,), device),
+            w.N, self.act, w.wbits)
+
+
+class LinearBackwardCall(_PreparedCall):
+    """A prepared w4a16_linear_backward call: dX = add + s * sum over the terms of dZ . D,
+    and each term's dZ and dbias.  The terms (1 to 4 BackwardTerm) are the layers that read
+    the same X with the same s.  dX None: only dZ and dbias; add may be dX itself."""
+
+    def __init__(self, terms, s, dX, add=None, stream=None, workspace=None):
+        torch = _torch()
+        self.keep = (list(terms), s, dX, add)
+        terms = self.keep[0]
+        if not terms:
+            raise ValueError("at least one term")
+        dt, device = _act_dtype(terms[0].dY, "dY"), terms[0].dY.device
+        M, K = terms[0].dY.shape[0], terms[0].wt.K
+        if any(t.wt.K != K for t in terms):
+            raise ValueError("the terms' weights must have the same K")
+        self.terms = (BackwardTermStruct * len(terms))()
+        for i, t in enumerate(terms):
+            self.terms[i] = t.struct(dt, (M, t.wt.N), device)
+        self.args = (self.terms, len(terms), _shaped_ptr(s, "s", torch.float16, (K,), device),
+                     _shaped_ptr(add, "add", dt, (M, K), device),
+                     _shaped_ptr(dX, "dX", dt, (M, K), device), M, K, _dtype_code(dt))
+        nbytes = self._size("w4a16_linear_backward_workspace_size", self.terms, len(terms), M, K,
+                            _dtype_code(dt))
+        self._prepare(device, nbytes, workspace, stream)
+
+    def __call__(self):
+        self._run("w4a16_linear_backward", *self.args)
+
+
+def w4a16_linear_backward(dY, wt: TransposedWeight, s=None, act=ACT_NONE, preact=None, add=None,
+                          bias_grad=False):
+    """Backward of w4a16_linear on the current stream: (dX, dZ, dbias).  dZ is dY itself for
+    ACT_NONE; dbias (fp32) is None unless bias_grad.  The residual's gradient is dY."""
+    torch = _torch()
+    M = dY.shape[0]
+    dX = torch.empty((M, wt.K), dtype=dY.dtype, device=dY.device)
+    dZ = torch.empty_like(dY) if act != ACT_NONE else None
+    db = torch.empty(wt.N, dtype=torch.float32, device=dY.device) if bias_grad else None
+    LinearBackwardCall([BackwardTerm(dY, wt, act, preact, dZ, db)], s, dX, add)()
+    return dX, dY if dZ is None else dZ, db
+
+
+class GatedBackwardCall(_PreparedCall):
+    """A prepared w4a16_gated_backward call: dG = dH * U * act'(G), dU = dH * act(G),
+    dX = add + s * (dG . Dg + dU . Du), and the fp32 column sums of dG and dU.  dG may be G
+    and dU may be U; dX None: only dG, dU and the sums."""
+
+    def __init__(self, dH, G, U, gate: TransposedWeight, up: TransposedWeight, s, dX, dG, dU,
+                 act=ACT_SILU, add=None, dbias_gate=None, dbias_up=None, stream=None,
+                 workspace=None):
+        torch = _torch()
+        dt, device = _act_dtype(dH, "dH"), dH.device
+        if (gate.N, gate.K, gate.wbits) != (up.N, up.K, up.wbits):
+            raise ValueError("gate and up must have the same shape and code width")
+        M, K = dH.shape[0], gate.K
+        shape = (M, gate.N)
+        self.keep = (dH, G, U, gate, up, s, dX, dG, dU, add, dbias_gate, dbias_up)
+        self.gate = BackwardTerm(None, gate, act, G, dG, dbias_gate).struct(dt, shape, device)
+        self.up = BackwardTerm(None, up, ACT_NONE, U, dU, dbias_up).struct(dt, shape, device)
+        refs = (ctypes.byref(self.gate), ctypes.byref(self.up))
+        self.args = (_shaped_ptr(dH, "dH", dt, shape, device), *refs,
+                     _shaped_ptr(s, "s", torch.float16, (K,), device),
+                     _shaped_ptr(add, "add", dt, (M, K), device),
+                     _shaped_ptr(dX, "dX", dt, (M, K), device), M, K, _dtype_code(dt))
+        nbytes = self._size("w4a16_gated_backward_workspace_size", *refs, M, K, _dtype_code(dt))
+        self._prepare(device, nbytes, workspace, stream)
+
+    def __call__(self):
+        self._run("w4a16_gated_backward", *self.args)
+
+
+def w4a16_gated_backward(dH, G, U, gate: TransposedWeight, up: TransposedWeight, s=None,
+                         act=ACT_SILU, add=None, bias_grad=False):
+    """Backward of w4a16_gated on the current stream, from dH and the saved pre-activations:
+    (dX, dG, dU, dbias_gate, dbias_up); the bias gradients (fp32) are None unless bias_grad."""
+    torch = _torch()
+    dX = torch.empty((dH.shape[0], gate.K), dtype=dH.dtype, device=dH.device)
+    dG, dU = torch.empty_like(dH), torch.empty_like(dH)
+    db = [torch.empty(gate.N, dtype=torch.float32, device=dH.device) if bias_grad else None
+          for _ in range(2)]
+    GatedBackwardCall(dH, G, U, gate, up, s, dX, dG, dU, act, add, *db)()
+    return dX, dG, dU, db[0], db[1]

@@ -14,7 +14,7 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 LIB_NAME = "libw4a16.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ("api.hip", "pack.hip", "skinny.hip", "tiled.hip", "spec.hip", "outliers.hip",
-           "gptq.hip")
+           "gptq.hip", "backward.hip")
 # the plain streaming-read and MFMA-only kernels the benchmark times as its
 # bandwidth and matrix-core ceilings:
 # its own small library, not part of the W4A16 ABI

@@ -359,20 +359,25 @@ int check_problems(const w4a16_problem *problems, int count) {
   return W4A16_OK;
 }
 
-w4a16::GemmDesc desc_of(const w4a16_problem &p) {
-  return {p.X,      p.Wq,        p.scales, p.zeros, p.s,  p.Y, (int)p.M, (int)p.N,
-          (int)p.K, p.o_row_ptr, p.o_col,  p.o_val, p.dtype == W4A16_DTYPE_BF16, p.wbits == 8};
+// A problem with the fused epilogue of its call (null: none).
+w4a16::GemmDesc desc_of(const w4a16_problem &p, const w4a16::Fused *fused) {
+  w4a16::GemmDesc d = {p.X,      p.Wq,        p.scales, p.zeros, p.s,  p.Y, (int)p.M, (int)p.N,
+                       (int)p.K, p.o_row_ptr, p.o_col,  p.o_val, p.dtype == W4A16_DTYPE_BF16, p.wbits == 8};
+  d.fused = fused;
+  return d;
 }
 
 // The tiled-path problems of a grouped call, in call order, in launches of up
 // to tiled_max_problems(): the same batches for the size query and the call.
-std::vector<std::vector<w4a16::GemmDesc>> tiled_batches(const w4a16_problem *problems, int count) {
+// fused: one epilogue per problem, or null for a plain call.
+std::vector<std::vector<w4a16::GemmDesc>> tiled_batches(const w4a16_problem *problems, int count,
+                                                        const w4a16::Fused *fused) {
   std::vector<std::vector<w4a16::GemmDesc>> out;
   const size_t cap = (size_t)w4a16::tiled_max_problems();
   for (int i = 0; i < count; ++i) {
     const w4a16_problem &p = problems[i];
     if (p.M == 0 || w4a16_select_path(p.M, p.N, p.K) != W4A16_PATH_TILED) continue;
-    const w4a16::GemmDesc d = desc_of(p);
+    const w4a16::GemmDesc d = desc_of(p, fused ? fused + i : nullptr);
     // a launch is one kernel instance: one activation type
     if (out.empty() || out.back().size() == cap || out.back().back().bf16 != d.bf16 ||
         out.back().back().w8 != d.w8)
@@ -380,6 +385,44 @@ std::vector<std::vector<w4a16::GemmDesc>> tiled_batches(const w4a16_problem *pro
     out.back().push_back(d);
   }
   return out;
+}
+
+// The streaming-path problems of a grouped call (M <= 16: one piece each).
+std::vector<w4a16::GemmDesc> streaming_pieces(const w4a16_problem *problems, int count,
+                                              const w4a16::Fused *fused) {
+  std::vector<w4a16::GemmDesc> pieces;
+  for (int i = 0; i < count; ++i) {
+    const w4a16_problem &p = problems[i];
+    if (p.M == 0 || w4a16_select_path(p.M, p.N, p.K) != W4A16_PATH_SKINNY) continue;
+    pieces.push_back(desc_of(p, fused ? fused + i : nullptr));
+  }
+  return pieces;
+}
+
+// Workspace and launches of a validated call.
+size_t grouped_bytes(const w4a16_problem *problems, int count, const w4a16::Fused *fused) {
+  // launches run in order on one stream, so they share the workspace
+  size_t need = 0;
+  for (const auto &b : tiled_batches(problems, count, fused)) {
+    const size_t n = w4a16::tiled_workspace_bytes(b.data(), (int)b.size());
+    need = n > need ? n : need;
+  }
+  const size_t sk = pieces_workspace_bytes(streaming_pieces(problems, count, fused));
+  return sk > need ? sk : need;
+}
+
+int launch_grouped(const w4a16_problem *problems, int count, const w4a16::Fused *fused,
+                   void *workspace, size_t workspace_bytes, void *stream) {
+  if (workspace && !aligned16(workspace)) return W4A16_EALIGN;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  for (const auto &b : tiled_batches(problems, count, fused))
+    if (w4a16::launch_tiled_set(b.data(), (int)b.size(), workspace, workspace_bytes, st) !=
+        hipSuccess)
+      return W4A16_EHIP;
+  return launch_pieces(streaming_pieces(problems, count, fused), st, false, workspace,
+                       workspace_bytes) == hipSuccess
+             ? W4A16_OK
+             : W4A16_EHIP;
 }
 
 }  // namespace
@@ -390,19 +433,7 @@ int w4a16_gemm_workspace_size(const w4a16_problem *problems, int count, size_t *
   if (!bytes) return W4A16_EINVAL;
   const int rc = check_problems(problems, count);
   if (rc) return rc;
-  // launches run in order on one stream, so they share the workspace
-  size_t need = 0;
-  for (const auto &b : tiled_batches(problems, count)) {
-    const size_t n = w4a16::tiled_workspace_bytes(b.data(), (int)b.size());
-    need = n > need ? n : need;
-  }
-  std::vector<w4a16::GemmDesc> pieces;
-  for (int i = 0; i < count; ++i) {
-    const w4a16_problem &p = problems[i];
-    if (p.M > 0 && w4a16_select_path(p.M, p.N, p.K) == W4A16_PATH_SKINNY) skinny_pieces(p, pieces);
-  }
-  const size_t sk = pieces_workspace_bytes(pieces);
-  *bytes = sk > need ? sk : need;
+  *bytes = grouped_bytes(problems, count, nullptr);
   return W4A16_OK;
 }
 
@@ -410,19 +441,111 @@ int w4a16_gemm_grouped_ws(const w4a16_problem *problems, int count, void *worksp
                           size_t workspace_bytes, void *stream) {
   const int rc = check_problems(problems, count);
   if (rc) return rc;
-  if (workspace && !aligned16(workspace)) return W4A16_EALIGN;
-  hipStream_t st = static_cast<hipStream_t>(stream);
-  std::vector<w4a16::GemmDesc> pieces;
+  return launch_grouped(problems, count, nullptr, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+bool known_act(int act) { return act >= W4A16_ACT_NONE && act <= W4A16_ACT_GELU_TANH; }
+static_assert(W4A16_ACT_RELU == (int)w4a16::kActRelu && W4A16_ACT_SILU == (int)w4a16::kActSilu &&
+                  W4A16_ACT_GELU == (int)w4a16::kActGelu &&
+                  W4A16_ACT_GELU_TANH == (int)w4a16::kActGeluTanh,
+              "the kernels' activation numbers");
+
+// Validates the epilogues of a linear call and puts them into the kernels' form.
+int fuse_linear(const w4a16_problem *problems, const w4a16_epilogue *epilogues, int count,
+                std::vector<w4a16::Fused> &out) {
+  int rc = check_problems(problems, count);
+  if (rc) return rc;
+  if (count > 0 && !epilogues) return W4A16_EINVAL;
   for (int i = 0; i < count; ++i) {
-    const w4a16_problem &p = problems[i];
-    if (p.M > 0 && w4a16_select_path(p.M, p.N, p.K) == W4A16_PATH_SKINNY) skinny_pieces(p, pieces);
+    const w4a16_epilogue &e = epilogues[i];
+    if (!known_act(e.act)) return W4A16_EUNSUPPORTED;
+    if (!aligned16(e.bias) || !aligned16(e.residual) || !aligned16(e.preact)) return W4A16_EALIGN;
+    w4a16::Fused f = {};
+    f.bias = e.bias;
+    f.residual = e.residual;
+    f.pre = e.preact;
+    f.act = e.act;
+    out.push_back(f);
   }
-  for (const auto &b : tiled_batches(problems, count))
-    if (w4a16::launch_tiled_set(b.data(), (int)b.size(), workspace, workspace_bytes, st) !=
-        hipSuccess)
-      return W4A16_EHIP;
-  return launch_pieces(pieces, st, false, workspace, workspace_bytes) == hipSuccess ? W4A16_OK
-                                                                                   : W4A16_EHIP;
+  return W4A16_OK;
+}
+
+// Validates a gated call; *p is the gate's problem with Y = H.
+int fuse_gated(const w4a16_problem *gate, const w4a16_problem *up, const void *bias_gate,
+               const void *bias_up, int act, const void *H, w4a16_problem *p, w4a16::Fused *f) {
+  if (!gate || !up) return W4A16_EINVAL;
+  if (gate->X != up->X || gate->s != up->s || gate->M != up->M || gate->N != up->N ||
+      gate->K != up->K || gate->dtype != up->dtype ||
+      (gate->wbits == 8) != (up->wbits == 8) || !gate->Y != !up->Y)
+    return W4A16_EINVAL;
+  w4a16_problem q[2] = {*gate, *up};
+  q[0].Y = q[1].Y = const_cast<void *>(H);
+  const int rc = check_problems(q, 2);
+  if (rc) return rc;
+  if (!known_act(act)) return W4A16_EUNSUPPORTED;
+  if (!aligned16(bias_gate) || !aligned16(bias_up) || !aligned16(gate->Y) || !aligned16(up->Y))
+    return W4A16_EALIGN;
+  *p = q[0];
+  *f = {};
+  f->gated = 1;
+  f->act = act;
+  f->bias = bias_gate;
+  f->bias2 = bias_up;
+  f->pre = gate->Y;
+  f->pre2 = up->Y;
+  f->Wq2 = static_cast<const uint8_t *>(up->Wq);
+  f->scales2 = static_cast<const _Float16 *>(up->scales);
+  f->zeros2 = static_cast<const _Float16 *>(up->zeros);
+  f->orp2 = static_cast<const int32_t *>(up->o_row_ptr);
+  f->ocol2 = static_cast<const int32_t *>(up->o_col);
+  f->oval2 = static_cast<const _Float16 *>(up->o_val);
+  return W4A16_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int w4a16_linear_workspace_size(const w4a16_problem *problems, const w4a16_epilogue *epilogues,
+                                int count, size_t *bytes) {
+  if (!bytes) return W4A16_EINVAL;
+  std::vector<w4a16::Fused> f;
+  const int rc = fuse_linear(problems, epilogues, count, f);
+  if (rc) return rc;
+  *bytes = grouped_bytes(problems, count, f.data());
+  return W4A16_OK;
+}
+
+int w4a16_linear(const w4a16_problem *problems, const w4a16_epilogue *epilogues, int count,
+                 void *workspace, size_t workspace_bytes, void *stream) {
+  std::vector<w4a16::Fused> f;
+  const int rc = fuse_linear(problems, epilogues, count, f);
+  if (rc) return rc;
+  return launch_grouped(problems, count, f.data(), workspace, workspace_bytes, stream);
+}
+
+int w4a16_gated_workspace_size(const w4a16_problem *gate, const w4a16_problem *up, size_t *bytes) {
+  if (!bytes) return W4A16_EINVAL;
+  w4a16_problem p;
+  w4a16::Fused f;
+  const int rc = fuse_gated(gate, up, nullptr, nullptr, W4A16_ACT_NONE, gate ? gate->X : nullptr, &p, &f);
+  if (rc) return rc;
+  *bytes = grouped_bytes(&p, 1, &f);
+  return W4A16_OK;
+}
+
+int w4a16_gated(const w4a16_problem *gate, const w4a16_problem *up, const void *bias_gate,
+                const void *bias_up, int act, void *H, void *workspace, size_t workspace_bytes,
+                void *stream) {
+  w4a16_problem p;
+  w4a16::Fused f;
+  const int rc = fuse_gated(gate, up, bias_gate, bias_up, act, H, &p, &f);
+  if (rc) return rc;
+  return launch_grouped(&p, 1, &f, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"
@@ -586,6 +709,206 @@ int w4a16_gemm(const void *X, const void *Wq, const void *scales, const void *ze
   p.N = N;
   p.K = K;
   return grouped_shared(&p, 1, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+bool aligned256(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
+
+// Rows of a transposed weight are addressed from a block's first row with
+// 32-bit byte offsets (128 rows of dZ).
+constexpr int64_t kMaxBackwardN = int64_t(1) << 22;
+
+int check_transposed(int64_t N, int64_t K, int wbits) {
+  if (wbits != 0 && wbits != 4 && wbits != 8) return W4A16_EUNSUPPORTED;
+  const int rc = check_shape_mode(N, K, wbits == 8 ? W4A16_QUANT_ASYM8 : W4A16_QUANT_ASYM);
+  if (rc) return rc;
+  if (N > kMaxBackwardN) return W4A16_EINVAL;
+  const int64_t Np = (N + W4A16_GROUP - 1) / W4A16_GROUP * W4A16_GROUP;
+  return Np * K / (wbits == 8 ? 1 : 2) > kMaxPackedBytes ? W4A16_EINVAL : W4A16_OK;
+}
+
+// Shape checks of a backward call, shared by the size query (which looks at no
+// pointer but which of dbias are set) and the call.
+int check_backward_shape(const w4a16_backward_term *terms, int count, int64_t M, int64_t K,
+                         int dtype) {
+  if (!terms || count < 1 || count > w4a16::kMaxDxTerms) return W4A16_EINVAL;
+  if (M < 0 || M > kMaxM) return W4A16_EINVAL;
+  if (dtype != W4A16_DTYPE_F16 && dtype != W4A16_DTYPE_BF16) return W4A16_EUNSUPPORTED;
+  for (int i = 0; i < count; ++i) {
+    if (!known_act(terms[i].act)) return W4A16_EUNSUPPORTED;
+    const int rc = check_transposed(terms[i].N, K, terms[i].wbits);
+    if (rc) return rc;
+    if ((terms[i].wbits == 8) != (terms[0].wbits == 8)) return W4A16_EUNSUPPORTED;
+  }
+  return W4A16_OK;
+}
+
+w4a16::DxDesc dx_desc(const w4a16_backward_term *terms, int count, const void *const *dZ,
+                      const void *s, const void *add, void *dX, int64_t M, int64_t K, int dtype) {
+  w4a16::DxDesc d = {};
+  d.count = count;
+  for (int i = 0; i < count; ++i) {
+    d.dZ[i] = dZ ? dZ[i] : nullptr;
+    d.Wt[i] = terms[i].Wt;
+    d.meta[i] = terms[i].meta;
+    d.N[i] = (int)terms[i].N;
+  }
+  d.s = s;
+  d.add = add;
+  d.dX = dX;
+  d.M = (int)M;
+  d.K = (int)K;
+  d.bf16 = dtype == W4A16_DTYPE_BF16;
+  d.w8 = terms[0].wbits == 8;
+  return d;
+}
+
+// The epilogue gradients of all terms, then the product, run in order on one
+// stream, so they share the workspace.
+size_t backward_bytes(const w4a16_backward_term *terms, int count, bool gated, bool dx, int64_t M,
+                      int64_t K, int dtype) {
+  if (M == 0) return 0;
+  size_t need = dx ? w4a16::dx_workspace_bytes(
+                         dx_desc(terms, count, nullptr, nullptr, nullptr, nullptr, M, K, dtype))
+                   : 0;
+  for (int i = 0; i < count; ++i) {
+    const int sums = gated ? (terms[0].dbias ? 1 : 0) + (terms[1].dbias ? 1 : 0)
+                           : (terms[i].dbias ? 1 : 0);
+    const size_t n = w4a16::grad_workspace_bytes((int)M, (int)terms[i].N, sums);
+    need = n > need ? n : need;
+  }
+  return need;
+}
+
+int check_backward_pointers(const w4a16_backward_term &t, bool gated, bool dx, int64_t M) {
+  if (!aligned16(t.dbias)) return W4A16_EALIGN;
+  if (M == 0) return W4A16_OK;  // nothing to read
+  if (gated || t.act != W4A16_ACT_NONE) {
+    if (!t.preact || !t.dZ) return W4A16_EINVAL;
+  } else if (t.preact || t.dZ) {
+    return W4A16_EINVAL;
+  }
+  if (!gated && !t.dY) return W4A16_EINVAL;
+  if (dx && (!t.Wt || !t.meta)) return W4A16_EINVAL;
+  if ((!gated && !aligned16(t.dY)) || !aligned16(t.preact) || !aligned16(t.dZ) ||
+      !aligned16(t.Wt) || !aligned16(t.meta))
+    return W4A16_EALIGN;
+  return W4A16_OK;
+}
+
+int check_backward_common(const w4a16_backward_term *terms, int count, bool gated, const void *s,
+                          const void *add, const void *dX, int64_t M, int64_t K, int dtype,
+                          const void *workspace, size_t workspace_bytes) {
+  for (int i = 0; i < count; ++i) {
+    const int rc = check_backward_pointers(terms[i], gated, dX != nullptr, M);
+    if (rc) return rc;
+  }
+  if (add && !dX && M > 0) return W4A16_EINVAL;
+  if (!aligned16(s) || !aligned16(add) || !aligned16(dX)) return W4A16_EALIGN;
+  const size_t need = backward_bytes(terms, count, gated, dX != nullptr, M, K, dtype);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return W4A16_EINVAL;
+  return workspace && !aligned256(workspace) ? W4A16_EALIGN : W4A16_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int w4a16_transposed_sizes(int64_t N, int64_t K, int wbits, size_t *wt_bytes, size_t *meta_bytes) {
+  if (!wt_bytes || !meta_bytes) return W4A16_EINVAL;
+  const int rc = check_transposed(N, K, wbits);
+  if (rc) return rc;
+  const int64_t NG = (N + W4A16_GROUP - 1) / W4A16_GROUP;
+  *wt_bytes = (size_t)(NG * W4A16_GROUP * K / (wbits == 8 ? 1 : 2));
+  *meta_bytes = (size_t)(NG * (K / W4A16_GROUP) * 512);
+  return W4A16_OK;
+}
+
+int w4a16_transpose(const void *Wq, const void *scales, const void *zeros, int64_t N, int64_t K,
+                    int wbits, void *Wt, void *meta, void *stream) {
+  const int rc = check_transposed(N, K, wbits);
+  if (rc) return rc;
+  if (!Wq || !scales || !zeros || !Wt || !meta) return W4A16_EINVAL;
+  if (!aligned16(Wq) || !aligned16(scales) || !aligned16(zeros) || !aligned16(Wt) || !aligned16(meta))
+    return W4A16_EALIGN;
+  return w4a16::launch_transpose(Wq, scales, zeros, (int)N, (int)K, wbits == 8, Wt, meta,
+                                 static_cast<hipStream_t>(stream)) == hipSuccess
+             ? W4A16_OK
+             : W4A16_EHIP;
+}
+
+int w4a16_linear_backward_workspace_size(const w4a16_backward_term *terms, int count, int64_t M,
+                                         int64_t K, int dtype, size_t *bytes) {
+  if (!bytes) return W4A16_EINVAL;
+  const int rc = check_backward_shape(terms, count, M, K, dtype);
+  if (rc) return rc;
+  *bytes = backward_bytes(terms, count, false, true, M, K, dtype);
+  return W4A16_OK;
+}
+
+int w4a16_linear_backward(const w4a16_backward_term *terms, int count, const void *s,
+                          const void *add, void *dX, int64_t M, int64_t K, int dtype,
+                          void *workspace, size_t workspace_bytes, void *stream) {
+  int rc = check_backward_shape(terms, count, M, K, dtype);
+  if (rc) return rc;
+  rc = check_backward_common(terms, count, false, s, add, dX, M, K, dtype, workspace, workspace_bytes);
+  if (rc) return rc;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const void *dZ[w4a16::kMaxDxTerms] = {};
+  for (int i = 0; i < count; ++i) {
+    const w4a16_backward_term &t = terms[i];
+    dZ[i] = t.dZ ? t.dZ : t.dY;
+    if (!t.dbias && (!t.dZ || M == 0)) continue;  // dZ is dY, and no column sums
+    w4a16::GradDesc g = {t.dY,    t.preact, nullptr, t.dZ,     nullptr, t.dbias, nullptr,
+                         (int)M, (int)t.N, t.act,   dtype == W4A16_DTYPE_BF16};
+    if (w4a16::launch_grad(g, workspace, st) != hipSuccess) return W4A16_EHIP;
+  }
+  if (!dX || M == 0) return W4A16_OK;
+  return w4a16::launch_dx(dx_desc(terms, count, dZ, s, add, dX, M, K, dtype), workspace, st) ==
+                 hipSuccess
+             ? W4A16_OK
+             : W4A16_EHIP;
+}
+
+int w4a16_gated_backward_workspace_size(const w4a16_backward_term *gate,
+                                        const w4a16_backward_term *up, int64_t M, int64_t K,
+                                        int dtype, size_t *bytes) {
+  if (!bytes || !gate || !up || gate->N != up->N) return W4A16_EINVAL;
+  const w4a16_backward_term terms[2] = {*gate, *up};
+  const int rc = check_backward_shape(terms, 2, M, K, dtype);
+  if (rc) return rc;
+  *bytes = backward_bytes(terms, 2, true, true, M, K, dtype);
+  return W4A16_OK;
+}
+
+int w4a16_gated_backward(const void *dH, const w4a16_backward_term *gate,
+                         const w4a16_backward_term *up, const void *s, const void *add, void *dX,
+                         int64_t M, int64_t K, int dtype, void *workspace, size_t workspace_bytes,
+                         void *stream) {
+  if (!gate || !up || gate->N != up->N) return W4A16_EINVAL;
+  const w4a16_backward_term terms[2] = {*gate, *up};
+  int rc = check_backward_shape(terms, 2, M, K, dtype);
+  if (rc) return rc;
+  if (up->act != W4A16_ACT_NONE) return W4A16_EINVAL;
+  if (!dH && M > 0) return W4A16_EINVAL;
+  if (!aligned16(dH)) return W4A16_EALIGN;
+  rc = check_backward_common(terms, 2, true, s, add, dX, M, K, dtype, workspace, workspace_bytes);
+  if (rc) return rc;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (M > 0 || gate->dbias || up->dbias) {
+    w4a16::GradDesc g = {dH,       gate->preact, up->preact, gate->dZ,  up->dZ, gate->dbias,
+                         up->dbias, (int)M,       (int)gate->N, gate->act, dtype == W4A16_DTYPE_BF16};
+    if (w4a16::launch_grad(g, workspace, st) != hipSuccess) return W4A16_EHIP;
+  }
+  if (!dX || M == 0) return W4A16_OK;
+  const void *dZ[2] = {gate->dZ, up->dZ};
+  return w4a16::launch_dx(dx_desc(terms, 2, dZ, s, add, dX, M, K, dtype), workspace, st) ==
+                 hipSuccess
+             ? W4A16_OK
+             : W4A16_EHIP;
 }
 
 }  // extern "C"

@@ -1,0 +1,644 @@
+// Backward passes of the fused linear layers (frozen packed weights):
+//   dZ = dY * act'(Z)                          (gated: dG and dU from dH, G, U)
+//   dbias = sum over rows of dZ
+//   dX = add + s * sum over layers of dZ . D,  D[n][k] = (q - z) * scale
+//
+// The product contracts over N, the packed layout is made for contracting over
+// K: a lane's code word is 8 columns of one row, but the B operand of dZ . D
+// needs 8 rows of one column.  Transposing in the kernel costs either LDS
+// traffic for the dequantized tile (as much again as the A operand's, which
+// would bound the kernel by LDS) or byte shuffles in every workgroup that reads
+// the weight.  The weights never change in training, so they are transposed
+// once (transpose_codes_kernel): tiles of 16 input features x 128 output rows,
+// whose words are B operands again.  The scale and zero point now vary along the
+// contraction; they are the same for the 128 input features of a quantization
+// group, so a workgroup's share is 4 bytes per row and group, staged in LDS.
+#include <algorithm>
+
+#include "epilogue.h"
+#include "w4a16_device.h"
+#include "w4a16_internal.h"
+
+namespace w4a16 {
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kRsrcWord3 = 0x00020000;  // raw buffer resource, 32-bit data format
+constexpr int kMetaBytes = 512;         // metadata of 128 rows and one quantization group
+constexpr int kOutOfRange = 0x7ffffff0; // a buffer offset past every resource: loads read 0
+
+__device__ __forceinline__ int uniform_int(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t bits) {
+  uint32_t r;
+  asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(mask), "v"(bits));
+  return r;
+}
+
+// ---- transposed weights -----------------------------------------------------------
+
+// One thread per 8 codes of the transposed layout: rows n0 .. n0 + 7 of input
+// feature k.  Offline, so the 8 gathered bytes per thread are left to the caches.
+template <bool W8>
+__global__ __launch_bounds__(256) void transpose_codes_kernel(const uint8_t *Wq, int N, int K,
+                                                              long long octets, uint8_t *Wt) {
+  const long long o = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (o >= octets) return;
+  const int t = (int)(o & 3), lane = (int)(o >> 2) & 63, c = lane >> 4, r = lane & 15;
+  const int KB = K / kTileRows, NB = N / kTileRows;
+  const int tile = (int)(o >> 8), g = tile / KB, b = tile - g * KB;
+  const int k = b * kTileRows + r, n0 = g * kGroup + 32 * t + 8 * c;
+  const int gk = k / kGroup, kk = k % kGroup, ts = kk / 32, cs = kk % 32 / 8, js = kk % 8;
+  const int slot = js / 2 + 4 * (js % 2);
+  uint32_t code[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (n0 < N) {  // N is a multiple of 16: all 8 rows or none
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int n = n0 + j;
+      const size_t lane16 = ((size_t)gk * NB + n / kTileRows) * kWave + 16 * cs + n % kTileRows;
+      code[j] = W8 ? Wq[lane16 * 32 + 8 * ts + js]
+                   : (Wq[lane16 * 16 + 4 * ts + slot / 2] >> (4 * (slot & 1))) & 15u;
+    }
+  }
+  if (W8) {
+    uint32_t *dst = reinterpret_cast<uint32_t *>(Wt) + 2 * o;
+    dst[0] = code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24;
+    dst[1] = code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24;
+  } else {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w |= code[2 * (i % 4) + i / 4] << (4 * i);
+    reinterpret_cast<uint32_t *>(Wt)[o] = w;
+  }
+}
+
+// One thread per (128-row group g, quantization group u, row j): its scale and
+// its zero point plus the bias of the code's decoding, 1024 (or 64 for the codes
+// that are decoded from the upper 4 bits of a byte), both exact in fp16.
+template <bool W8>
+__global__ __launch_bounds__(256) void transpose_meta_kernel(const _Float16 *scales,
+                                                             const _Float16 *zeros, int N, int G,
+                                                             long long count, uint8_t *meta) {
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= count) return;
+  const int j = (int)(i & (kGroup - 1));
+  const long long gu = i / kGroup;
+  const int g = (int)(gu / G), u = (int)(gu - (long long)g * G), n = g * kGroup + j;
+  _Float16 sc = (_Float16)0.f, z = (_Float16)0.f;
+  if (n < N) {
+    const size_t at = meta_index(n, u, N / kTileRows);
+    sc = scales[at];
+    z = zeros[at];
+  }
+  _Float16 *dst = reinterpret_cast<_Float16 *>(meta + gu * kMetaBytes);
+  dst[j] = sc;
+  dst[kGroup + j] = z + (_Float16)(!W8 && (j & 2) ? 64.f : 1024.f);
+}
+
+// ---- gradients of the epilogues -----------------------------------------------------
+
+// dZ (gated: dG and dU) of a strip of rows, 8 columns per thread, 4 rows at a
+// time, and the strip's column sums: each thread sums its rows in order, then
+// the 4 row lanes meet in LDS, so the sums do not depend on scheduling.
+// Bound by HBM: one read of dY and the pre-activations, one write of dZ.
+constexpr int kGradCols = 512;  // columns per workgroup
+struct GradArgs {
+  const void *dY, *z, *u;      // z, u: pre-activations (null: dZ = dY, not written)
+  void *dz, *du;
+  float *part, *part2;         // column sums [strips][N] (null: not wanted)
+  int M, N, rows, col_blocks;  // rows per strip
+  int act;
+};
+
+template <bool BF, bool GATED>
+__global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
+  const int strip = (int)blockIdx.x / a.col_blocks;
+  const int n = ((int)blockIdx.x - strip * a.col_blocks) * kGradCols + (int)(threadIdx.x & 63) * 8;
+  const int lane_row = threadIdx.x >> 6;
+  const int m1 = min(a.M, (strip + 1) * a.rows);
+  float s0[8] = {0, 0, 0, 0, 0, 0, 0, 0}, s1[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (n < a.N) {
+#pragma unroll 2
+    for (int m = strip * a.rows + lane_row; m < m1; m += 4) {
+      const size_t at = (size_t)m * a.N + n;
+      const u32x4 d = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.dY) + at);
+      u32x4 z = d, u = d, oz, ou;
+      if (a.z) z = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.z) + at);
+      if (GATED) u = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.u) + at);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t wz = 0, wu = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float dy = act_to_f32<BF>((uint16_t)(d[q] >> (16 * h)));
+          const float zv = act_to_f32<BF>((uint16_t)(z[q] >> (16 * h)));
+          float dz = a.z ? dy * act_grad(zv, a.act) : dy;
+          if (GATED) {
+            const float du = dy * act_value(zv, a.act);
+            dz *= act_to_f32<BF>((uint16_t)(u[q] >> (16 * h)));
+            s1[2 * q + h] += du;
+            wu |= (uint32_t)f32_to_act<BF>(du) << (16 * h);
+          }
+          s0[2 * q + h] += dz;
+          wz |= (uint32_t)f32_to_act<BF>(dz) << (16 * h);
+        }
+        oz[q] = wz;
+        ou[q] = wu;
+      }
+      if (a.dz) *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(a.dz) + at) = oz;
+      if (GATED) *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(a.du) + at) = ou;
+    }
+  }
+  __shared__ float red[4][kGradCols];
+  auto column_sums = [&](const float (&s)[8], float *part) {
+    if (!part) return;  // uniform
+#pragma unroll
+    for (int j = 0; j < 8; ++j) red[lane_row][(threadIdx.x & 63) * 8 + j] = s[j];
+    __syncthreads();
+    for (int x = threadIdx.x; x < kGradCols; x += 256) {
+      const int col = ((int)blockIdx.x - strip * a.col_blocks) * kGradCols + x;
+      if (col < a.N) part[(size_t)strip * a.N + col] = (red[0][x] + red[1][x]) + (red[2][x] + red[3][x]);
+    }
+    __syncthreads();
+  };
+  column_sums(s0, a.part);
+  if (GATED) column_sums(s1, a.part2);
+}
+
+// out[n] = the strips' sums, in order (0 without strips).
+__global__ __launch_bounds__(256) void bias_kernel(const float *part, int strips, int N, float *out) {
+  const int n = (int)blockIdx.x * 256 + (int)threadIdx.x;
+  if (n >= N) return;
+  float s = 0.f;
+  for (int k = 0; k < strips; ++k) s += part[(size_t)k * N + n];
+  out[n] = s;
+}
+
+// ---- dX ------------------------------------------------------------------------------
+
+struct DxTerm {
+  const void *dZ;       // [M][N]
+  const uint8_t *Wt, *meta;
+  int N, stage0;        // stage0: stages (128 rows of N each) of the terms before
+};
+struct DxArgs {
+  DxTerm t[kMaxDxTerms];
+  int count;
+  const _Float16 *s;
+  const void *add;
+  void *dX;
+  float *part;          // split > 1: split fp32 [M][K] partial slabs
+  int M, K;
+  int tiles_k, tiles;   // output blocks along K, and in all
+  int split, stages;
+};
+
+// dX block of 16 TM x 64 TN, four waves of 16 TM x 16 TN, in stages of 128 rows
+// of one term's N:
+//   * dZ's rows go from memory into LDS with DMA loads, double-buffered, one
+//     barrier per stage, 16-byte chunks XOR-swizzled by the row so that the A
+//     operand reads of 16 rows hit distinct banks; chunks past N read zeros;
+//   * the stage's scales and zero points (1 KB for 256 columns) follow the same
+//     way; a k step's 8 rows are one 16-byte read each, shared by the 16 lanes;
+//   * the wave's code tiles (its B operands) are loaded into registers one
+//     stage ahead, in two register sets that alternate.
+// A weight's dequantization: (q - z) exact in fp16, times the scale, rounded
+// once to fp16; bf16 takes the product in fp32 (v_fma_mix, exact: 8 + 11 bits)
+// and rounds it once: 5 instructions for two weights, where converting code
+// and scale to fp32 first would take 7.
+// N is split across workgroups when the output blocks leave CUs idle: fp32
+// partials, added in a fixed order by dx_reduce_kernel.
+template <int TM, int TN, bool BF, bool W8>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TN == 2 ? 4 : 2, TN == 2 ? 4 : 2))) void dx_kernel(
+    DxArgs P) {
+  constexpr int kCW = W8 ? 2 : 1;  // 16-byte code pieces per lane per tile
+  constexpr int BM = TM * 16, BN = 64 * TN;
+  constexpr int kRowChunks = kGroup / 8;  // 16-byte chunks per row per stage
+  constexpr int kDma = TM;                // DMA loads per wave per stage
+  static_assert(kDma * 4 * 64 == BM * kRowChunks, "a stage is whole DMA loads");
+  __shared__ __attribute__((aligned(16))) _Float16 As[2][BM * kGroup];
+  __shared__ __attribute__((aligned(16))) unsigned char Ms[2][1024];
+
+  const int M = P.M, K = P.K;
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform_int(tid >> 6);
+  const int c = lane >> 4, r = lane & 15;
+  // Workgroups go to the eight XCDs round robin: a split launch is renumbered
+  // so that each XCD takes a contiguous run of (split, block) pairs, which
+  // share dZ rows and code panels in its L2.
+  const int L = P.split * P.tiles, q8 = L >> 3, block = (int)blockIdx.x;
+  const int local = (P.split > 1 && block < 8 * q8) ? (block & 7) * q8 + (block >> 3) : block;
+  const int sp = local / P.tiles, t = local - sp * P.tiles;
+  const int mt = t / P.tiles_k;
+  const int k0 = (t - mt * P.tiles_k) * BN, m0 = mt * BM;
+  const int KB = K / kTileRows, G = K / kGroup;
+  const int sb = (int)((long long)P.stages * sp / P.split);
+  const int se = (int)((long long)P.stages * (sp + 1) / P.split);
+  const int rows = min(BM, M - m0);
+
+  float4v acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = float4v{0.f, 0.f, 0.f, 0.f};
+
+  for (int ti = 0; ti < P.count; ++ti) {
+    const DxTerm &T = P.t[ti];
+    const int N = T.N, NG = (N + kGroup - 1) / kGroup;
+    const int gb = max(sb - T.stage0, 0), ge = min(se - T.stage0, NG);
+    if (gb >= ge) continue;
+
+    // dZ: wave load u fills LDS chunks p = (u * 4 + wave) * 64 + lane; chunk p is
+    // row p / 16 = 16 u + 4 wave + lane / 16, physical chunk p % 16, holding
+    // logical chunk lc = (p % 16) ^ (row % 16), the same for every u.  Rows past
+    // M lie past the resource and read zeros, as do chunks past N.
+    const __amdgpu_buffer_rsrc_t xrs = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)(static_cast<const uint16_t *>(T.dZ) + (size_t)m0 * N), (short)0, rows * N * 2, kRsrcWord3);
+    const __amdgpu_buffer_rsrc_t wrs = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)T.Wt, (short)0, (int)min((size_t)0x7fffffff, (size_t)KB * NG * kTileBytes * kCW), kRsrcWord3);
+    const __amdgpu_buffer_rsrc_t mrs = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)T.meta, (short)0, (int)min((size_t)0x7fffffff, (size_t)NG * G * kMetaBytes), kRsrcWord3);
+    const int row0 = 4 * wave + (lane >> 4), lc = (lane & 15) ^ row0;
+    const int xoff = (row0 * N + 8 * lc) * 2;
+    auto load_x = [&](int g, int buf) {
+      const int vo = 8 * lc < N - g * kGroup ? xoff : kOutOfRange;
+#pragma unroll
+      for (int u = 0; u < kDma; ++u) {
+        const int vu = (int)((unsigned)vo + 32u * u * N);  // still out of range where vo is
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            xrs, (__attribute__((address_space(3))) void *)(&As[buf][(u * 4 + wave) * 64 * 8]), 16,
+            vu, g * kGroup * 2, 0, 0);
+      }
+      // scales and zero points of the block's quantization groups: 256 bytes a wave
+      const int mo = (wave * 64 + lane) * 4;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          mrs, (__attribute__((address_space(3))) void *)(&Ms[buf][wave * 256]), 4, mo,
+          (g * G + k0 / kGroup) * kMetaBytes, 0, 0);
+    };
+    const int kb0 = k0 / kTileRows + wave * TN;
+    const int tile_stride = KB * kTileBytes * kCW;
+    struct BStage {
+      u32x4 code[TN][kCW];
+    };
+    // column blocks past K re-read the last one (never stored)
+    auto load_b = [&](int g, BStage &b) {
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        const int kb = min(kb0 + j, KB - 1);
+#pragma unroll
+        for (int h = 0; h < kCW; ++h)
+          b.code[j][h] = __builtin_bit_cast(
+              u32x4, __builtin_amdgcn_raw_buffer_load_b128(wrs, (kb * 64 + lane) * 16 * kCW + 16 * h,
+                                                           g * tile_stride, 0));
+      }
+    };
+    // the wave's quantization group among the block's
+    const int ul = (wave * TN * kTileRows) / kGroup;
+
+    auto compute = [&](const BStage &b, int buf) {
+      const _Float16 *ms = reinterpret_cast<const _Float16 *>(&Ms[buf][ul * kMetaBytes]) + 8 * c;
+      struct Meta {
+        half8 scale, bias;
+      };
+      auto meta_at = [&](int tt) -> Meta {
+        return {*reinterpret_cast<const half8 *>(ms + 32 * tt),
+                *reinterpret_cast<const half8 *>(ms + kGroup + 32 * tt)};
+      };
+      auto dequant = [&](int j, int tt, const Meta &mt8) -> u32x4 {
+        half2v e[4];
+        if constexpr (W8) {
+          const uint32_t wa = b.code[j][tt >> 1][2 * (tt & 1)], wb = b.code[j][tt >> 1][2 * (tt & 1) + 1];
+          const uint32_t magic = 0x64646464u;
+          e[0] = as_half2(__builtin_amdgcn_perm(magic, wa, 0x05010400u));
+          e[1] = as_half2(__builtin_amdgcn_perm(magic, wa, 0x05030402u));
+          e[2] = as_half2(__builtin_amdgcn_perm(magic, wb, 0x05010400u));
+          e[3] = as_half2(__builtin_amdgcn_perm(magic, wb, 0x05030402u));
+        } else {
+          const uint32_t w = b.code[j][0][tt], w8 = w >> 8;
+          const half2v sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
+          e[0] = as_half2(and_or(w, 0x000F000Fu, kMagic2));
+          e[1] = as_half2(and_or(w, 0x00F000F0u, kMagic2)) * sixteenth;
+          e[2] = as_half2(and_or(w8, 0x000F000Fu, kMagic2));
+          e[3] = as_half2(and_or(w8, 0x00F000F0u, kMagic2)) * sixteenth;
+        }
+        u32x4 out;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const half2v bias = {mt8.bias[2 * p], mt8.bias[2 * p + 1]};
+          const half2v scale = {mt8.scale[2 * p], mt8.scale[2 * p + 1]};
+          const half2v v = e[p] - bias;  // q - z, exact
+          if constexpr (BF)
+            out[p] = pack_bf16x2(__builtin_fmaf((float)v[0], (float)scale[0], 0.f),
+                                 __builtin_fmaf((float)v[1], (float)scale[1], 0.f));
+          else
+            out[p] = __builtin_bit_cast(uint32_t, v * scale);
+        }
+        return out;
+      };
+      const _Float16 *abuf = As[buf];
+      // software pipeline: k step tt + 1's B operands are dequantized while k
+      // step tt's MFMAs run
+      u32x4 bop[TN];
+      Meta m = meta_at(0);
+#pragma unroll
+      for (int j = 0; j < TN; ++j) bop[j] = dequant(j, 0, m);
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) {
+        u32x4 bnx[TN];
+        if (tt < 3) {
+          m = meta_at(tt + 1);
+#pragma unroll
+          for (int j = 0; j < TN; ++j) bnx[j] = dequant(j, tt + 1, m);
+        }
+        const int pc = (4 * tt + c) ^ r;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+          const u32x4 aop = *reinterpret_cast<const u32x4 *>(abuf + (16 * i + r) * kGroup + 8 * pc);
+#pragma unroll
+          for (int j = 0; j < TN; ++j)
+            acc[i][j] = BF ? mfma16_bf16(aop, bop[j], acc[i][j])
+                           : mfma16(__builtin_bit_cast(half8, aop), __builtin_bit_cast(half8, bop[j]),
+                                    acc[i][j]);
+        }
+        if (tt < 3) {
+#pragma unroll
+          for (int j = 0; j < TN; ++j) bop[j] = bnx[j];
+        }
+      }
+    };
+
+    // one stage per step, as in the forward kernel: wait for this stage's loads
+    // (issued a step ago) and for every wave to be past the step before, issue
+    // the next stage's, compute.  Past the range the loads re-read its last
+    // stage into buffers and registers that nobody reads.
+    BStage b0, b1;
+    auto step = [&](int g, BStage &cur, BStage &nxt, int buf) {
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      const int gn = min(g + 1, ge - 1);
+      load_x(gn, buf ^ 1);
+      load_b(gn, nxt);
+      compute(cur, buf);
+    };
+    // the term before may still be read, and its last loads still land, in LDS
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    load_x(gb, 0);
+    load_b(gb, b0);
+    for (int g = gb; g < ge; g += 2) {
+      step(g, b0, b1, 0);
+      if (g + 1 < ge) step(g + 1, b1, b0, 1);
+    }
+  }
+  // the last step's DMA must land before the workgroup's LDS is released
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+
+  // lane holds D[4c + v][r] of each 16x16 sub-block.  Buffer resources that
+  // start at the sub-block's first row and end at row M drop rows past M; a
+  // 16-column block lies inside K as a whole or not at all.
+  const int kb0 = k0 / kTileRows + wave * TN;
+  float sv[TN];
+#pragma unroll
+  for (int j = 0; j < TN; ++j)
+    sv[j] = P.s && kb0 + j < KB ? (float)P.s[(kb0 + j) * kTileRows + r] : 1.f;
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int mi = m0 + 16 * i;
+    if (mi >= M) break;
+    const int n16 = min(M - mi, 16);
+    auto rsrc = [&](const void *p, size_t row0, int esize) {
+      return __builtin_amdgcn_make_buffer_rsrc(
+          (void *)(static_cast<const char *>(p) + row0 * K * esize), (short)0, n16 * K * esize, kRsrcWord3);
+    };
+    auto at = [&](int j, int v) { return (4 * c + v) * K + (kb0 + j) * kTileRows + r; };
+    if (P.split > 1) {
+      const __amdgpu_buffer_rsrc_t prs = rsrc(P.part, (size_t)sp * M + mi, 4);
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        if (kb0 + j >= KB) continue;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const float x = acc[i][j][v];  // (a bit cast of the vector element itself takes element 0)
+          __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, x), prs, at(j, v) * 4, 0, 0);
+        }
+      }
+      continue;
+    }
+    uint16_t add[TN][4];
+    if (P.add) {
+      const __amdgpu_buffer_rsrc_t ars = rsrc(P.add, mi, 2);
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          add[j][v] = __builtin_amdgcn_raw_buffer_load_b16(ars, kb0 + j < KB ? at(j, v) * 2 : 0, 0, 0);
+    }
+    const __amdgpu_buffer_rsrc_t yrs = rsrc(P.dX, mi, 2);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      if (kb0 + j >= KB) continue;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        float x = acc[i][j][v] * sv[j];
+        if (P.add) x += act_to_f32<BF>(add[j][v]);
+        __builtin_amdgcn_raw_buffer_store_b16(f32_to_act<BF>(x), yrs, at(j, v) * 2, 0, 0);
+      }
+    }
+  }
+}
+
+// dX from the split partials, in split order; four outputs of one row per thread.
+template <bool BF>
+__global__ __launch_bounds__(256) void dx_reduce_kernel(DxArgs P) {
+  const long long quads = (long long)P.M * P.K / 4;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= quads) return;
+  const float4v *src = reinterpret_cast<const float4v *>(P.part) + i;
+  float4v x = src[0];
+  for (int k = 1; k < P.split; ++k) x += src[(size_t)k * quads];
+  typedef _Float16 half4 __attribute__((ext_vector_type(4)));
+  if (P.s) {
+    const half4 s = *reinterpret_cast<const half4 *>(P.s + (i * 4) % P.K);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) x[v] *= (float)s[v];
+  }
+  u16x4 out;
+  if (P.add) {
+    const u16x4 a = reinterpret_cast<const u16x4 *>(P.add)[i];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) x[v] += act_to_f32<BF>(a[v]);
+  }
+#pragma unroll
+  for (int v = 0; v < 4; ++v) out[v] = f32_to_act<BF>(x[v]);
+  reinterpret_cast<u16x4 *>(P.dX)[i] = out;
+}
+
+// ---- plans and launches ----------------------------------------------------------------
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Rows per strip of grad_kernel: 32, fewer while the launch has under 512
+// workgroups (each is 256 threads: two per CU), more where column sums are
+// wanted and 256 strips would not cover M (their partials stay below 1/128 of
+// what the kernel reads).
+int strip_rows(int M, int N, bool sums) {
+  const long long cols = (N + kGradCols - 1) / kGradCols;
+  int rows = 32;
+  while (rows > 4 && cols * ((M + rows - 1) / rows) < 512) rows /= 2;
+  if (sums) rows = std::max(rows, ((M + 255) / 256 + 3) / 4 * 4);
+  return rows;
+}
+int strips_of(int M, int N, bool sums) {
+  const int rows = strip_rows(M, N, sums);
+  return (M + rows - 1) / rows;
+}
+
+struct DxPlan {
+  int tm, tn, split, stages;
+  long long tiles;
+};
+constexpr int kDxMaxSplit = 16;
+constexpr int kDxMinStages = 8;  // stages per split at the shortest
+
+// The block shape goes by M, as few 16-row tiles as cover it (128 x 256 blocks
+// above 64 rows), the split of the stages by a model of the launch: rounds of
+// workgroups that fill the GPU, each as long as its stages plus a fixed cost,
+// plus the partials' traffic.
+DxPlan plan_dx(const DxDesc &d) {
+  DxPlan p;
+  p.tm = d.M > 64 ? (d.w8 ? 6 : 8) : d.M > 32 ? 4 : d.M > 16 ? 2 : 1;
+  p.tn = p.tm >= 6 ? 4 : 2;
+  p.stages = 0;
+  for (int i = 0; i < d.count; ++i) p.stages += (d.N[i] + kGroup - 1) / kGroup;
+  p.tiles = (long long)((d.K + 64 * p.tn - 1) / (64 * p.tn)) * ((d.M + 16 * p.tm - 1) / (16 * p.tm));
+  const long long slots = p.tn == 4 ? 512 : 1024;
+  double best = 0.0;
+  p.split = 1;
+  for (int s = 1; s <= kDxMaxSplit && (s == 1 || p.stages / s >= kDxMinStages); ++s) {
+    const long long rounds = (p.tiles * s + slots - 1) / slots;
+    const double us = (double)rounds * ((p.stages + s - 1) / s + 2.0) * 2.3 +
+                      (s > 1 ? (double)(4 * s + 2) * d.M * d.K / 4.0e6 : 0.0);
+    if (s == 1 || us < best) {
+      best = us;
+      p.split = s;
+    }
+  }
+  return p;
+}
+
+template <bool BF, bool W8>
+void launch_dx_tile(int tm, dim3 grid, hipStream_t stream, const DxArgs &a) {
+  constexpr int kLarge = W8 ? 6 : 8;
+  if (tm == kLarge)
+    hipLaunchKernelGGL((dx_kernel<kLarge, 4, BF, W8>), grid, dim3(256), 0, stream, a);
+  else if (tm == 4)
+    hipLaunchKernelGGL((dx_kernel<4, 2, BF, W8>), grid, dim3(256), 0, stream, a);
+  else if (tm == 2)
+    hipLaunchKernelGGL((dx_kernel<2, 2, BF, W8>), grid, dim3(256), 0, stream, a);
+  else
+    hipLaunchKernelGGL((dx_kernel<1, 2, BF, W8>), grid, dim3(256), 0, stream, a);
+}
+
+}  // namespace
+
+hipError_t launch_transpose(const void *Wq, const void *scales, const void *zeros, int N, int K,
+                            bool w8, void *Wt, void *meta, hipStream_t stream) {
+  const int NG = (N + kGroup - 1) / kGroup, G = K / kGroup;
+  const long long octets = (long long)K * NG * (kGroup / 8), rows = (long long)NG * G * kGroup;
+  const dim3 cg((unsigned)((octets + 255) / 256)), mg((unsigned)((rows + 255) / 256)), th(256);
+  const uint8_t *q = static_cast<const uint8_t *>(Wq);
+  const _Float16 *s = static_cast<const _Float16 *>(scales), *z = static_cast<const _Float16 *>(zeros);
+  if (w8) {
+    hipLaunchKernelGGL(transpose_codes_kernel<true>, cg, th, 0, stream, q, N, K, octets, static_cast<uint8_t *>(Wt));
+    hipLaunchKernelGGL(transpose_meta_kernel<true>, mg, th, 0, stream, s, z, N, G, rows, static_cast<uint8_t *>(meta));
+  } else {
+    hipLaunchKernelGGL(transpose_codes_kernel<false>, cg, th, 0, stream, q, N, K, octets, static_cast<uint8_t *>(Wt));
+    hipLaunchKernelGGL(transpose_meta_kernel<false>, mg, th, 0, stream, s, z, N, G, rows, static_cast<uint8_t *>(meta));
+  }
+  return hipGetLastError();
+}
+
+size_t grad_workspace_bytes(int M, int N, int sums) {
+  return sums ? sums * align256((size_t)strips_of(M, N, true) * N * sizeof(float)) : 0;
+}
+
+hipError_t launch_grad(const GradDesc &d, void *workspace, hipStream_t stream) {
+  const bool gated = d.u != nullptr, sums = d.db || d.db2;
+  const int strips = d.M > 0 ? strips_of(d.M, d.N, sums) : 0;
+  GradArgs a = {d.dY, d.z, d.u, d.dz, d.du, nullptr, nullptr, d.M, d.N, 0, 0, d.act};
+  char *ws = static_cast<char *>(workspace);
+  const size_t slab = align256((size_t)strips * d.N * sizeof(float));
+  if (d.db) {
+    a.part = reinterpret_cast<float *>(ws);
+    ws += slab;
+  }
+  if (d.db2) a.part2 = reinterpret_cast<float *>(ws);
+  if (strips > 0) {
+    a.rows = strip_rows(d.M, d.N, sums);
+    a.col_blocks = (d.N + kGradCols - 1) / kGradCols;
+    const dim3 grid((unsigned)(strips * (long long)a.col_blocks)), th(256);
+    if (d.bf16 && gated)
+      hipLaunchKernelGGL((grad_kernel<true, true>), grid, th, 0, stream, a);
+    else if (d.bf16)
+      hipLaunchKernelGGL((grad_kernel<true, false>), grid, th, 0, stream, a);
+    else if (gated)
+      hipLaunchKernelGGL((grad_kernel<false, true>), grid, th, 0, stream, a);
+    else
+      hipLaunchKernelGGL((grad_kernel<false, false>), grid, th, 0, stream, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  const dim3 bg((unsigned)((d.N + 255) / 256)), th(256);
+  if (d.db) hipLaunchKernelGGL(bias_kernel, bg, th, 0, stream, a.part, strips, d.N, static_cast<float *>(d.db));
+  if (d.db2) hipLaunchKernelGGL(bias_kernel, bg, th, 0, stream, a.part2, strips, d.N, static_cast<float *>(d.db2));
+  return hipGetLastError();
+}
+
+size_t dx_workspace_bytes(const DxDesc &d) {
+  const DxPlan p = plan_dx(d);
+  return p.split > 1 ? (size_t)p.split * d.M * d.K * sizeof(float) : 0;
+}
+
+hipError_t launch_dx(const DxDesc &d, void *workspace, hipStream_t stream) {
+  if (d.count < 1 || d.count > kMaxDxTerms || d.M < 1) return hipErrorInvalidValue;
+  const DxPlan p = plan_dx(d);
+  if (p.tiles * p.split > INT32_MAX) return hipErrorInvalidValue;
+  DxArgs a = {};
+  int stage0 = 0;
+  for (int i = 0; i < d.count; ++i) {
+    a.t[i] = {d.dZ[i], static_cast<const uint8_t *>(d.Wt[i]), static_cast<const uint8_t *>(d.meta[i]),
+              d.N[i], stage0};
+    stage0 += (d.N[i] + kGroup - 1) / kGroup;
+  }
+  a.count = d.count;
+  a.s = static_cast<const _Float16 *>(d.s);
+  a.add = d.add;
+  a.dX = d.dX;
+  a.part = p.split > 1 ? static_cast<float *>(workspace) : nullptr;
+  a.M = d.M;
+  a.K = d.K;
+  a.tiles_k = (d.K + 64 * p.tn - 1) / (64 * p.tn);
+  a.tiles = (int)p.tiles;
+  a.split = p.split;
+  a.stages = p.stages;
+  const dim3 grid((unsigned)(p.tiles * p.split));
+  if (d.bf16 && d.w8)
+    launch_dx_tile<true, true>(p.tm, grid, stream, a);
+  else if (d.bf16)
+    launch_dx_tile<true, false>(p.tm, grid, stream, a);
+  else if (d.w8)
+    launch_dx_tile<false, true>(p.tm, grid, stream, a);
+  else
+    launch_dx_tile<false, false>(p.tm, grid, stream, a);
+  hipError_t err = hipGetLastError();
+  if (err == hipSuccess && p.split > 1) {
+    const dim3 rg((unsigned)(((long long)d.M * d.K / 4 + 255) / 256));
+    if (d.bf16)
+      hipLaunchKernelGGL(dx_reduce_kernel<true>, rg, dim3(256), 0, stream, a);
+    else
+      hipLaunchKernelGGL(dx_reduce_kernel<false>, rg, dim3(256), 0, stream, a);
+    err = hipGetLastError();
+  }
+  return err;
+}
+
+}  // namespace w4a16

@@ -43,6 +43,7 @@
 // per CU, instead of windows.  Whole-row launches without outliers keep each
 // wave's scales and zero points in an LDS slab when that costs no workgroup
 // per CU.
+#include "epilogue.h"
 #include "w4a16_device.h"
 #include "w4a16_internal.h"
 
@@ -243,6 +244,79 @@ __device__ __forceinline__ Problem find_problem(const ProblemSet &ps) {
   return P;
 }
 
+// The epilogues of a fused launch, one per problem; plain launches carry none.
+struct FusedSet {
+  Fused f[kMaxProblems];
+};
+struct NoFused {};
+
+// This workgroup's epilogue, read after the weights have been streamed (the
+// index is hidden from the compiler): its dozen scalars would otherwise stay in
+// registers, or spill, through the whole K loop.
+__device__ __forceinline__ Fused find_fused(const ProblemSet &ps, const FusedSet &fs) {
+  int pi = 0;
+#pragma unroll
+  for (int i = 1; i < kMaxProblems; ++i)
+    if (i < ps.count && (int)blockIdx.x >= ps.p[i].block0) pi = i;
+  pi = uniform_int(pi);
+  asm volatile("" : "+s"(pi));
+  const Fused &q = fs.f[pi];
+  Fused F = {};
+  F.bias = uniform_ptr(q.bias);
+  F.residual = uniform_ptr(q.residual);
+  F.pre = uniform_ptr(q.pre);
+  F.act = uniform_int(q.act);
+  F.gated = uniform_int(q.gated);
+  F.bias2 = uniform_ptr(q.bias2);
+  F.pre2 = uniform_ptr(q.pre2);
+  return F;
+}
+__device__ __forceinline__ NoFused find_fused(const ProblemSet &, const NoFused &) { return {}; }
+
+// Row block of slot v (the slots of a problem are given to the waves in order).
+// Plain and linear problems have one slot per row block.  A gated problem (the
+// only one of its call) has two, gate then up, so that the two waves (or groups
+// of S waves) whose sums meet in act(G) * U are neighbours in one workgroup and
+// both read the X * s staged there; P becomes the slot's own matrix.
+__device__ __forceinline__ int slot_block(Problem &, const NoFused &, int v) { return v; }
+__device__ __forceinline__ int slot_block(Problem &P, const FusedSet &fs, int v) {
+  const Fused &q = fs.f[0];
+  if (!q.gated) return v;
+  if (v & 1) {
+    P.Wq = uniform_ptr(q.Wq2);
+    P.scales = uniform_ptr(q.scales2);
+    P.zeros = uniform_ptr(q.zeros2);
+    P.orp = uniform_ptr(q.orp2);
+    P.ocol = uniform_ptr(q.ocol2);
+    P.oval = uniform_ptr(q.oval2);
+  }
+  return v >> 1;
+}
+
+// The bias and residual of the outputs that this lane stores, fetched before
+// the sums meet in LDS.  Rows past M read row M - 1.
+struct EpiloguePrefetch {
+  uint16_t bias, bias2, res[4];
+};
+__device__ __forceinline__ NoFused prefetch_epilogue(const Problem &, const NoFused &, int, int,
+                                                     int, int, int) {
+  return {};
+}
+__device__ __forceinline__ EpiloguePrefetch prefetch_epilogue(const Problem &P, const Fused &F,
+                                                              int slot, int b, int ks, int c, int r) {
+  EpiloguePrefetch e = {};
+  if (ks != 0 || (F.gated && (slot & 1))) return e;  // another wave stores
+  const int n = b * kTileRows + r;
+  if (F.bias) e.bias = static_cast<const uint16_t *>(F.bias)[n];
+  if (F.bias2) e.bias2 = static_cast<const uint16_t *>(F.bias2)[n];
+  if (F.residual) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      e.res[v] = static_cast<const uint16_t *>(F.residual)[(size_t)min(4 * c + v, P.M - 1) * P.N + n];
+  }
+  return e;
+}
+
 // fp16 outliers of a row block, added by the wave that stores it, all 64
 // lanes at once.  The kept weights of the block's 16 rows are one range
 // e0 .. e1 - 1 of the row-compressed arrays; round u hands entry e0 + 64 u +
@@ -398,20 +472,78 @@ __device__ __forceinline__ void store_rows(const Problem &P, float4v acc, int b,
   }
 }
 
+// The same for a plain launch (F is empty) or a fused one.  slot: the wave's
+// slot of the problem (b its row block); the epilogue is applied to the fp32
+// sum and each output rounded once.  Gated: the gate slot's first wave adds up
+// its own S partial sums and those of the up slot, the S waves after it.
+template <int kWaves, bool kOut, bool kBF>
+__device__ __forceinline__ void store_slot(const Problem &P, const NoFused &, const NoFused &,
+                                           float4v acc, int, int b, bool has_rows, int wave,
+                                           int ks, int c, int r, float (*red)[16][17],
+                                           int2 orange, const OutPrefetch &of) {
+  store_rows<kWaves, kOut, kBF>(P, acc, b, has_rows, wave, ks, c, r, red, orange, of);
+}
+template <int kWaves, bool kOut, bool kBF>
+__device__ __forceinline__ void store_slot(const Problem &P, const Fused &F,
+                                           const EpiloguePrefetch &e, float4v acc, int slot, int b,
+                                           bool has_rows, int wave, int ks, int c, int r,
+                                           float (*red)[16][17], int2 orange,
+                                           const OutPrefetch &of) {
+  const int M = P.M, N = P.N, S = P.split;
+  const bool stores = ks == 0 && has_rows && !(F.gated && (slot & 1));
+  if (kOut && ks == 0 && has_rows) acc += outlier_terms<kBF>(P, of, orange, 16 * c + r, c);
+  if (S > 1 || F.gated) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) red[wave][4 * c + v][r] = acc[v];
+    __syncthreads();
+  }
+  if (!stores) return;
+  const float bias = F.bias ? act_to_f32<kBF>(e.bias) : 0.f;
+  const float bias2 = F.bias2 ? act_to_f32<kBF>(e.bias2) : 0.f;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const int m = 4 * c + v;
+    if (m >= M) continue;
+    const size_t i = (size_t)m * N + (size_t)b * kTileRows + r;
+    float z = acc[v];
+    for (int w = 1; w < S; ++w) z += red[wave + w][m][r];
+    z += bias;
+    if (F.pre) static_cast<uint16_t *>(F.pre)[i] = f32_to_act<kBF>(z);
+    float y = act_value(z, F.act);
+    if (F.gated) {
+      float u = 0.f;
+      for (int w = 0; w < S; ++w) u += red[wave + S + w][m][r];
+      u += bias2;
+      if (F.pre2) static_cast<uint16_t *>(F.pre2)[i] = f32_to_act<kBF>(u);
+      y *= u;
+    }
+    if (F.residual) y += act_to_f32<kBF>(e.res[v]);
+    reinterpret_cast<uint16_t *>(P.Y)[i] = f32_to_act<kBF>(y);
+  }
+}
+
+// Whether the reduction scratch is used by these sums (it overlaps X * s).
+__device__ __forceinline__ bool uses_red(const Problem &P, const NoFused &) { return P.split > 1; }
+__device__ __forceinline__ bool uses_red(const Problem &P, const Fused &F) {
+  return P.split > 1 || F.gated;
+}
+
 // Whole-row body: xs (dynamic LDS) holds X * s, then (after the last use of
 // X) the split-K reduction.
-template <int kGW, int kWaves, int kDepth, bool kOut, bool kBF, bool kW8 = false, bool kML = false>
-__device__ __forceinline__ void skinny_body(const ProblemSet &ps, _Float16 *xs) {
+template <int kGW, int kWaves, int kDepth, bool kOut, bool kBF, bool kW8 = false, bool kML = false,
+          typename FS>
+__device__ __forceinline__ void skinny_body(const ProblemSet &ps, const FS &fs, _Float16 *xs) {
   constexpr int kCW = kW8 ? 2 : 1;  // 16-byte code loads per lane per tile
 
-  const Problem P = find_problem(ps);
+  Problem P = find_problem(ps);
   const int M = P.M, N = P.N, K = P.K, S = P.split;
   const int G = K / kGroup, NB = N / kTileRows;
   const int lane = threadIdx.x & 63, wave = uniform_int(threadIdx.x >> 6);
   const int c = lane >> 4;   // column octet (A/B operands), row quad (D)
   const int r = lane & 15;   // X row m (A), W row in the tile (B), column n (D)
-  const int b = ((int)blockIdx.x - P.block0) * (kWaves / S) + wave / S;  // row block
-  const int ks = wave % S;                                               // K slice
+  const int slot = ((int)blockIdx.x - P.block0) * (kWaves / S) + wave / S;
+  const int b = slot_block(P, fs, slot);  // row block
+  const int ks = wave % S;               // K slice
   const bool has_rows = b < NB;
   const int bb = has_rows ? b : NB - 1;
   // this wave's groups: [gb, ge), split on chunk boundaries
@@ -602,15 +734,23 @@ __device__ __forceinline__ void skinny_body(const ProblemSet &ps, _Float16 *xs) 
     if (j + 1 < nch) step(j + 1, m1);
   }
 
-  if (S > 1) __syncthreads();  // every wave is done with X * s: its LDS takes the partial sums
-  store_rows<kWaves, kOut, kBF>(P, acc, b, has_rows, wave, ks, c, r,
+  const auto F = find_fused(ps, fs);
+  const auto epi = prefetch_epilogue(P, F, slot, bb, ks, c, r);
+  if (uses_red(P, F)) __syncthreads();  // every wave is done with X * s: its LDS takes the partial sums
+  store_slot<kWaves, kOut, kBF>(P, F, epi, acc, slot, b, has_rows, wave, ks, c, r,
                                 reinterpret_cast<float (*)[16][17]>(xs), orange, of);
 }
 
 template <int kGW, int kWaves, int kDepth, bool kOut, bool kBF, bool kW8 = false, bool kML = false>
 __global__ __launch_bounds__(kWaves * 64) void skinny_kernel(ProblemSet ps) {
   extern __shared__ __attribute__((aligned(16))) _Float16 xs[];
-  skinny_body<kGW, kWaves, kDepth, kOut, kBF, kW8, kML>(ps, xs);
+  skinny_body<kGW, kWaves, kDepth, kOut, kBF, kW8, kML>(ps, NoFused{}, xs);
+}
+
+template <int kGW, int kWaves, int kDepth, bool kOut, bool kBF, bool kW8 = false, bool kML = false>
+__global__ __launch_bounds__(kWaves * 64) void skinny_fused_kernel(ProblemSet ps, FusedSet fs) {
+  extern __shared__ __attribute__((aligned(16))) _Float16 xs[];
+  skinny_body<kGW, kWaves, kDepth, kOut, kBF, kW8, kML>(ps, fs, xs);
 }
 
 // bf16 X * s and its per-group sums, once per call, for the windowed kernel
@@ -638,17 +778,18 @@ __global__ __launch_bounds__(256) void prescale_kernel(ProblemSet ps) {
 // launch has room for both), then (after the last window) the split-K
 // reduction.
 template <int kGW, int kWaves, int kDepth, int kSlots, bool kOut, bool kBF, bool kW8 = false,
-          bool kPre = false>
-__device__ __forceinline__ void skinny_window_body(const ProblemSet &ps, _Float16 *xs) {
+          bool kPre = false, typename FS>
+__device__ __forceinline__ void skinny_window_body(const ProblemSet &ps, const FS &fs, _Float16 *xs) {
   constexpr int kCW = kW8 ? 2 : 1;  // 16-byte code loads per lane per tile
   constexpr int kThreads = kWaves * 64;
 
-  const Problem P = find_problem(ps);
+  Problem P = find_problem(ps);
   const int M = P.M, N = P.N, K = P.K, S = P.split;
   const int G = K / kGroup, NB = N / kTileRows;
   const int lane = threadIdx.x & 63, wave = uniform_int(threadIdx.x >> 6);
   const int c = lane >> 4, r = lane & 15;
-  const int b = ((int)blockIdx.x - P.block0) * (kWaves / S) + wave / S;
+  const int slot = ((int)blockIdx.x - P.block0) * (kWaves / S) + wave / S;
+  const int b = slot_block(P, fs, slot);
   const int ks = wave % S;
   const bool has_rows = b < NB;
   const int bb = has_rows ? b : NB - 1;
@@ -876,7 +1017,9 @@ __device__ __forceinline__ void skinny_window_body(const ProblemSet &ps, _Float1
     lds_barrier();
   }
   // every wave is past the last barrier: the window's LDS takes the partial sums
-  store_rows<kWaves, kOut, kBF>(P, acc, b, has_rows, wave, ks, c, r,
+  const auto F = find_fused(ps, fs);
+  const auto epi = prefetch_epilogue(P, F, slot, bb, ks, c, r);
+  store_slot<kWaves, kOut, kBF>(P, F, epi, acc, slot, b, has_rows, wave, ks, c, r,
                                 reinterpret_cast<float (*)[16][17]>(xs), orange, of);
 }
 
@@ -884,7 +1027,14 @@ template <int kGW, int kWaves, int kDepth, int kSlots, bool kOut, bool kBF, bool
           bool kPre = false>
 __global__ __launch_bounds__(kWaves * 64) void skinny_window_kernel(ProblemSet ps) {
   extern __shared__ __attribute__((aligned(16))) _Float16 xs[];
-  skinny_window_body<kGW, kWaves, kDepth, kSlots, kOut, kBF, kW8, kPre>(ps, xs);
+  skinny_window_body<kGW, kWaves, kDepth, kSlots, kOut, kBF, kW8, kPre>(ps, NoFused{}, xs);
+}
+
+template <int kGW, int kWaves, int kDepth, int kSlots, bool kOut, bool kBF, bool kW8 = false,
+          bool kPre = false>
+__global__ __launch_bounds__(kWaves * 64) void skinny_window_fused_kernel(ProblemSet ps, FusedSet fs) {
+  extern __shared__ __attribute__((aligned(16))) _Float16 xs[];
+  skinny_window_body<kGW, kWaves, kDepth, kSlots, kOut, kBF, kW8, kPre>(ps, fs, xs);
 }
 
 // Both kinds in one launch (fp16 INT4 codes without outliers): a workgroup
@@ -898,9 +1048,9 @@ __global__ __launch_bounds__(kWaves * 64) void skinny_hybrid_kernel(ProblemSet p
   for (int i = 1; i < kMaxProblems; ++i)
     if (i < ps.count && (int)blockIdx.x >= ps.p[i].block0) pi = i;
   if (uniform_int(ps.p[pi].window))
-    skinny_window_body<kGW, kWaves, kDepth, kSlots, false, false>(ps, xs);
+    skinny_window_body<kGW, kWaves, kDepth, kSlots, false, false>(ps, NoFused{}, xs);
   else
-    skinny_body<kGW, kWaves, kDepth, false, false>(ps, xs);
+    skinny_body<kGW, kWaves, kDepth, false, false>(ps, NoFused{}, xs);
 }
 
 constexpr size_t kMaxStageBytes = 96 * 1024;
@@ -991,30 +1141,32 @@ int skinny_max_problems() { return kMaxProblems; }
 
 namespace {
 
+// One instance of a kernel family, plain or (fs not null) fused.
+#define W4_LAUNCH(family, ...)                                                                \
+  do {                                                                                        \
+    if (fs)                                                                                   \
+      hipLaunchKernelGGL((family##_fused_kernel<__VA_ARGS__>), grid, threads, lds, stream, ps, *fs); \
+    else                                                                                      \
+      hipLaunchKernelGGL((family##_kernel<__VA_ARGS__>), grid, threads, lds, stream, ps);     \
+  } while (0)
+
 // The windowed instances over INT8 codes.
 void launch_window8(bool bf, bool out, bool pre, dim3 grid, dim3 threads, size_t lds,
-                    hipStream_t stream, const ProblemSet &ps) {
+                    hipStream_t stream, const ProblemSet &ps, const FusedSet *fs) {
   constexpr int S = kWindowSlotsBF;
   if (bf && out && pre)
-    hipLaunchKernelGGL((skinny_window_kernel<kChunk, kWaves, kDepth, S, true, true, true, true>),
-                       grid, threads, lds, stream, ps);
+    W4_LAUNCH(skinny_window, kChunk, kWaves, kDepth, S, true, true, true, true);
   else if (bf && pre)
-    hipLaunchKernelGGL((skinny_window_kernel<kChunk, kWaves, kDepth, S, false, true, true, true>),
-                       grid, threads, lds, stream, ps);
+    W4_LAUNCH(skinny_window, kChunk, kWaves, kDepth, S, false, true, true, true);
   else if (bf && out)
-    hipLaunchKernelGGL((skinny_window_kernel<kChunk, kWaves, kDepth, S, true, true, true>), grid,
-                       threads, lds, stream, ps);
+    W4_LAUNCH(skinny_window, kChunk, kWaves, kDepth, S, true, true, true);
   else if (bf)
-    hipLaunchKernelGGL((skinny_window_kernel<kChunk, kWaves, kDepth, S, false, true, true>), grid,
-                       threads, lds, stream, ps);
+    W4_LAUNCH(skinny_window, kChunk, kWaves, kDepth, S, false, true, true);
   else if (out)
-    hipLaunchKernelGGL((skinny_window_kernel<kChunk, kWaves, kDepth, S, true, false, true>), grid,
-                       threads, lds, stream, ps);
+    W4_LAUNCH(skinny_window, kChunk, kWaves, kDepth, S, true, false, true);
   else
-    hipLaunchKernelGGL((skinny_window_kernel<kChunk, kWaves, kDepth, S, false, false, true>), grid,
-                       threads, lds, stream, ps);
+    W4_LAUNCH(skinny_window, kChunk, kWaves, kDepth, S, false, false, true);
 }
-
 
 enum LaunchKind { kWhole = 0, kWindowed = 1, kHybrid = 2 };
 
@@ -1027,7 +1179,7 @@ hipError_t launch_group(const GemmDesc *const *d, int count, LaunchKind kind, hi
   // How many waves share a row block: enough waves in the whole launch to keep
   // HBM busy, and no wave walking more than kMaxGroupsPerWave groups.
   long long rows = 0;
-  for (int i = 0; i < count; ++i) rows += d[i]->N / kTileRows;
+  for (int i = 0; i < count; ++i) rows += d[i]->row_blocks();
   const int s_fill =
       (int)min((long long)waves, (long long)pow2_at_least((int)((kTargetWaves + rows - 1) / rows)));
   // Problems are laid out longest-rows first so that the waves with the most
@@ -1041,6 +1193,8 @@ hipError_t launch_group(const GemmDesc *const *d, int count, LaunchKind kind, hi
       order[j - 1] = t;
     }
   ProblemSet ps = {};
+  FusedSet fset = {};
+  const FusedSet *fs = d[0]->fused ? &fset : nullptr;  // all or none of a call's problems
   int blocks = 0;
   size_t lds = 0;
   bool out = false;  // some problem has fp16 outliers
@@ -1052,11 +1206,13 @@ hipError_t launch_group(const GemmDesc *const *d, int count, LaunchKind kind, hi
   for (int i = 0; i < count; ++i) {
     const GemmDesc &q = *d[order[i]];
     Problem &p = ps.p[i];
-    const int G = q.K / kGroup, NB = q.N / kTileRows;
+    const int G = q.K / kGroup;
     const bool win = kind == kWindowed ||
                      (kind == kHybrid && stage_bytes(q.M, q.K, q.bf16) > kMaxStageBytes);
-    int split = s_fill;
-    while (split < waves && (G + split - 1) / split > kMaxGroupsPerWave) split *= 2;
+    // a gated problem's two sums meet within a workgroup: at least two slots in it
+    const int split_cap = q.gated() ? waves / 2 : waves;
+    int split = min(s_fill, split_cap);
+    while (split < split_cap && (G + split - 1) / split > kMaxGroupsPerWave) split *= 2;
     while (split > 1 && (G + kChunk - 1) / kChunk < split) split /= 2;  // a chunk per wave
     if (win)  // a window of split chunks must fit in LDS and in the staging registers
       while (split > 1 && (window_bytes(q.M, split, q.bf16) > kMaxWindowBytes ||
@@ -1083,7 +1239,11 @@ hipError_t launch_group(const GemmDesc *const *d, int count, LaunchKind kind, hi
     p.window = win;
     p.block0 = blocks;
     const int rb_per_wg = waves / split;
-    blocks += (NB + rb_per_wg - 1) / rb_per_wg;
+    blocks += (q.row_blocks() + rb_per_wg - 1) / rb_per_wg;
+    if (q.fused) {
+      fset.f[i] = *q.fused;
+      out |= q.fused->orp2 != nullptr;
+    }
     const size_t wb = window_bytes(q.M, split, q.bf16), wb16 = (wb + 15) / 16 * 16;
     const bool pair = win && 2 * wb16 <= kMaxWindowPairBytes;
     p.wpair = pair ? (int)(wb16 / 2) : 0;
@@ -1108,67 +1268,48 @@ hipError_t launch_group(const GemmDesc *const *d, int count, LaunchKind kind, hi
   const bool bf = d[0]->bf16;  // one activation type (and code width) per launch
   if (waves == kWideWaves) {
     if (kind != kWhole || bf || out || d[0]->w8) return hipErrorInvalidValue;  // not instantiated
-    hipLaunchKernelGGL((skinny_kernel<kChunk, kWideWaves, kDepth, false, false>), grid, threads,
-                       lds, stream, ps);
+    W4_LAUNCH(skinny, kChunk, kWideWaves, kDepth, false, false);
   } else if (kind == kHybrid) {
-    if (bf || out || d[0]->w8) return hipErrorInvalidValue;  // not instantiated
+    if (bf || out || d[0]->w8 || fs) return hipErrorInvalidValue;  // not instantiated
     hipLaunchKernelGGL((skinny_hybrid_kernel<kChunk, kWaves, kDepth, kWindowSlots>), grid, threads,
                        lds, stream, ps);
   } else if (d[0]->w8) {  // INT8 codes
     if (window)
-      launch_window8(bf, out, pre, grid, threads, lds, stream, ps);
+      launch_window8(bf, out, pre, grid, threads, lds, stream, ps, fs);
     else if (bf && out)
-      hipLaunchKernelGGL((skinny_kernel<kChunk, kWaves, kDepth, true, true, true>), grid, threads,
-                         lds, stream, ps);
+      W4_LAUNCH(skinny, kChunk, kWaves, kDepth, true, true, true);
     else if (bf)
-      hipLaunchKernelGGL((skinny_kernel<kChunk, kWaves, kDepth, false, true, true>), grid, threads,
-                         lds, stream, ps);
+      W4_LAUNCH(skinny, kChunk, kWaves, kDepth, false, true, true);
     else if (out)
-      hipLaunchKernelGGL((skinny_kernel<kChunk, kWaves, kDepth, true, false, true>), grid, threads,
-                         lds, stream, ps);
+      W4_LAUNCH(skinny, kChunk, kWaves, kDepth, true, false, true);
     else
-      hipLaunchKernelGGL((skinny_kernel<kChunk, kWaves, kDepth, false, false, true>), grid, threads,
-                         lds, stream, ps);
+      W4_LAUNCH(skinny, kChunk, kWaves, kDepth, false, false, true);
   } else if (window) {
     if (bf && out && pre)
-      hipLaunchKernelGGL(
-          (skinny_window_kernel<kChunk, kWaves, kDepth, kWindowSlotsBF, true, true, false, true>),
-          grid, threads, lds, stream, ps);
+      W4_LAUNCH(skinny_window, kChunk, kWaves, kDepth, kWindowSlotsBF, true, true, false, true);
     else if (bf && pre)
-      hipLaunchKernelGGL(
-          (skinny_window_kernel<kChunk, kWaves, kDepth, kWindowSlotsBF, false, true, false, true>),
-          grid, threads, lds, stream, ps);
+      W4_LAUNCH(skinny_window, kChunk, kWaves, kDepth, kWindowSlotsBF, false, true, false, true);
     else if (bf && out)
-      hipLaunchKernelGGL((skinny_window_kernel<kChunk, kWaves, kDepth, kWindowSlotsBF, true, true>),
-                         grid, threads, lds, stream, ps);
+      W4_LAUNCH(skinny_window, kChunk, kWaves, kDepth, kWindowSlotsBF, true, true);
     else if (bf)
-      hipLaunchKernelGGL((skinny_window_kernel<kChunk, kWaves, kDepth, kWindowSlotsBF, false, true>),
-                         grid, threads, lds, stream, ps);
+      W4_LAUNCH(skinny_window, kChunk, kWaves, kDepth, kWindowSlotsBF, false, true);
     else if (out)
-      hipLaunchKernelGGL((skinny_window_kernel<kChunk, kWaves, kDepth, kWindowSlots, true, false>),
-                         grid, threads, lds, stream, ps);
+      W4_LAUNCH(skinny_window, kChunk, kWaves, kDepth, kWindowSlots, true, false);
     else
-      hipLaunchKernelGGL((skinny_window_kernel<kChunk, kWaves, kDepth, kWindowSlots, false, false>),
-                         grid, threads, lds, stream, ps);
+      W4_LAUNCH(skinny_window, kChunk, kWaves, kDepth, kWindowSlots, false, false);
   } else {
     if (bf && out)
-      hipLaunchKernelGGL((skinny_kernel<kChunk, kWaves, kDepth, true, true>), grid, threads, lds,
-                         stream, ps);
+      W4_LAUNCH(skinny, kChunk, kWaves, kDepth, true, true);
     else if (bf && ml)
-      hipLaunchKernelGGL((skinny_kernel<kChunk, kWaves, kDepth, false, true, false, true>), grid,
-                         threads, lds, stream, ps);
+      W4_LAUNCH(skinny, kChunk, kWaves, kDepth, false, true, false, true);
     else if (bf)
-      hipLaunchKernelGGL((skinny_kernel<kChunk, kWaves, kDepth, false, true>), grid, threads, lds,
-                         stream, ps);
+      W4_LAUNCH(skinny, kChunk, kWaves, kDepth, false, true);
     else if (out)
-      hipLaunchKernelGGL((skinny_kernel<kChunk, kWaves, kDepth, true, false>), grid, threads, lds,
-                         stream, ps);
+      W4_LAUNCH(skinny, kChunk, kWaves, kDepth, true, false);
     else if (ml)
-      hipLaunchKernelGGL((skinny_kernel<kChunk, kWaves, kDepth, false, false, false, true>), grid,
-                         threads, lds, stream, ps);
+      W4_LAUNCH(skinny, kChunk, kWaves, kDepth, false, false, false, true);
     else
-      hipLaunchKernelGGL((skinny_kernel<kChunk, kWaves, kDepth, false, false>), grid, threads, lds,
-                         stream, ps);
+      W4_LAUNCH(skinny, kChunk, kWaves, kDepth, false, false);
   }
   return hipGetLastError();
 }
@@ -1229,7 +1370,7 @@ hipError_t launch_skinny_set(const GemmDesc *d, int count, hipStream_t stream, b
         any |= big;
         all &= big;
         wide &= stage_bytes(d[i].M, d[i].K, d[i].bf16) <= kWideStageBytes;
-        outl |= d[i].o_row_ptr != nullptr;
+        outl |= d[i].o_row_ptr != nullptr || (d[i].fused && d[i].fused->orp2);
         members[nm++] = d + i;
       }
     // fp16 INT4 without outliers, all X * s within kWideStageBytes: whole rows
@@ -1239,8 +1380,9 @@ hipError_t launch_skinny_set(const GemmDesc *d, int count, hipStream_t stream, b
       continue;
     }
     // fp16 INT4 without outliers: problems that fit stage whole rows and the
-    // others walk windows, in the same launch
-    if (kHybridLaunch && cls == 0 && any && !all && !outl && !force_window && kWindowMode == 3) {
+    // others walk windows, in the same launch (fused calls, whose problems mostly
+    // share one K, have no hybrid instance: they window the whole call)
+    if (kHybridLaunch && !d[0].fused && cls == 0 && any && !all && !outl && !force_window && kWindowMode == 3) {
       err = launch_group(members, nm, kHybrid, stream);
       continue;
     }

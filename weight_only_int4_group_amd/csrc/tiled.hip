@@ -29,6 +29,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "epilogue.h"
 #include "w4a16_device.h"
 #include "w4a16_internal.h"
 
@@ -141,6 +142,14 @@ struct TiledSet {
   int count;
 };
 
+// The epilogues of a fused launch, one per problem (EPI: kLinear or kGated);
+// plain launches carry none.
+struct TiledFused {
+  Fused f[kMaxTiled];
+};
+struct NoFused {};
+enum { kPlain = 0, kLinear = 1, kGated = 2 };
+
 template <typename T>
 __device__ __forceinline__ T *uniform_ptr(T *p) {
   const uint64_t v = reinterpret_cast<uint64_t>(p);
@@ -182,11 +191,122 @@ __device__ __forceinline__ TiledProblem find_tiled(const TiledSet &ts, int block
   return P;
 }
 
+// The epilogue of workgroup `block`'s problem, read when the sums are complete
+// (the index is hidden from the compiler, so that nothing of it stays in
+// registers through the K loop).
+template <bool REDUCE>
+__device__ __forceinline__ Fused find_fused(const TiledSet &ts, const TiledFused &fs, int block) {
+  int pi = 0;
+#pragma unroll
+  for (int i = 1; i < kMaxTiled; ++i)
+    if (i < ts.count && block >= (REDUCE ? ts.p[i].rblock0 : ts.p[i].block0)) pi = i;
+  pi = uniform_int(pi);
+  asm volatile("" : "+s"(pi));
+  const Fused &q = fs.f[pi];
+  Fused F = {};
+  F.bias = uniform_ptr(q.bias);
+  F.residual = uniform_ptr(q.residual);
+  F.pre = uniform_ptr(q.pre);
+  F.act = uniform_int(q.act);
+  F.bias2 = uniform_ptr(q.bias2);
+  F.pre2 = uniform_ptr(q.pre2);
+  return F;
+}
+
+// The second weight of a gated problem (the only problem of its call).  Its row
+// blocks alternate with the first's: block v of the problem is row block v / 2
+// of the first weight for even v and of the second for odd v, so a wave's tiles
+// hold G and U of the same outputs in the same lane, and a block of Y costs the
+// same reads of X as two blocks of a plain product.
+struct Second {
+  const uint8_t *Wq;
+  const _Float16 *scales, *zeros;
+  const int32_t *orp, *ocol;
+  const _Float16 *oval;
+};
+__device__ __forceinline__ Second find_second(const NoFused &) { return {}; }
+__device__ __forceinline__ Second find_second(const TiledFused &fs) {
+  const Fused &q = fs.f[0];
+  return {uniform_ptr(q.Wq2),  uniform_ptr(q.scales2), uniform_ptr(q.zeros2),
+          uniform_ptr(q.orp2), uniform_ptr(q.ocol2),   uniform_ptr(q.oval2)};
+}
+
+// Stores a wave's TM x TN sub-blocks of a fused product: lane (c, r) holds
+// rows m = m0 + 16 i + 4 c + v and column r of its 16-column blocks.  vb0: the
+// wave's first 16-column block of the problem (gated: of the alternating
+// blocks, even, so block pairs j, j + 1 are G and U).  Buffer resources that
+// start at the sub-block's first row and end at row M drop rows past M and read
+// their residuals as zeros; a 16-column block lies inside N as a whole or not
+// at all.
+template <int EPI, int TM, int TN, bool BF, typename Acc>
+__device__ __forceinline__ void store_fused(const TiledProblem &P, const Fused &F, const Acc &acc,
+                                            int m0, int vb0, int c, int r) {
+  constexpr int STEP = EPI == kGated ? 2 : 1;
+  const int M = P.M, N = P.N;
+  auto rsrc = [&](const void *p, int mi) {
+    const int rows = min(max(M - mi, 0), 16);
+    return __builtin_amdgcn_make_buffer_rsrc(
+        (void *)(static_cast<const char *>(p) + (size_t)mi * N * 2), (short)0, p ? rows * N * 2 : 0,
+        kRsrcWord3);
+  };
+  float bias[TN];
+#pragma unroll
+  for (int j = 0; j < TN; ++j) {
+    const int n = (vb0 + j) / STEP * 16 + r;
+    const void *b = STEP == 2 && (j & 1) ? F.bias2 : F.bias;
+    bias[j] = b && n < N ? act_to_f32<BF>(static_cast<const uint16_t *>(b)[n]) : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int mi = m0 + 16 * i;
+    if (mi >= M) break;
+    const __amdgpu_buffer_rsrc_t yrs = rsrc(P.Y, mi);
+    uint16_t res[TN / STEP][4];
+    if (EPI == kLinear && F.residual) {
+      const __amdgpu_buffer_rsrc_t rrs = rsrc(F.residual, mi);
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          res[j / STEP][v] = __builtin_amdgcn_raw_buffer_load_b16(
+              rrs, (vb0 + j) * 16 < N ? ((4 * c + v) * N + (vb0 + j) * 16 + r) * 2 : 0, 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < TN; j += STEP) {
+      const int nb = (vb0 + j) / STEP * 16;
+      if (nb >= N) continue;
+      float4v z = acc[i][j], y, u;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        z[v] += bias[j];
+        u[v] = STEP == 2 ? acc[i][j + STEP - 1][v] + bias[j + STEP - 1] : 1.f;
+      }
+      auto put = [&](const __amdgpu_buffer_rsrc_t &rs, const float4v &x) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          __builtin_amdgcn_raw_buffer_store_b16(f32_to_act<BF>(x[v]), rs,
+                                                ((4 * c + v) * N + nb + r) * 2, 0, 0);
+      };
+      if (F.pre) put(rsrc(F.pre, mi), z);
+      if (STEP == 2 && F.pre2) put(rsrc(F.pre2, mi), u);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        y[v] = act_value(z[v], F.act);
+        if (STEP == 2) y[v] *= u[v];
+      }
+      if (EPI == kLinear && F.residual) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) y[v] += act_to_f32<BF>(res[j / STEP][v]);
+      }
+      put(yrs, y);
+    }
+  }
+}
+
 // Two waves per SIMD: with one, the waits on LDS and the barriers are not
 // hidden and MFMA throughput roughly halves (measured on the 70B shapes).
-template <int WM, int WN, int TM, int TN, bool OUT, bool BF, bool W8 = false>
-__global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2, 2))) void tiled_kernel(
-    TiledSet ts) {
+template <int WM, int WN, int TM, int TN, bool OUT, bool BF, bool W8, int EPI, typename FS>
+__device__ __forceinline__ void tiled_body(const TiledSet &ts, const FS &fs) {
   constexpr int THREADS = WM * WN * 64;
   constexpr int kCW = W8 ? 2 : 1;  // 16-byte code pieces per lane per tile
   constexpr int BM = WM * TM * 16, BN = WN * TN * 16;
@@ -205,6 +325,7 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2,
   const _Float16 *__restrict__ zeros = P.zeros;
   const _Float16 *__restrict__ s = P.s;
   const bool has_s = s != nullptr;  // else s = 1
+  const Second S2 = find_second(fs);
   const int M = P.M, N = P.N, K = P.K;
 
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform_int(tid >> 6);
@@ -217,6 +338,8 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2,
   const int mt = t / P.tiles_n;
   const int n0 = (t - mt * P.tiles_n) * BN, m0 = mt * BM;
   const int G = K / kGroup, NB = N / kTileRows;
+  // gated: NV alternating row blocks, and N and n0 count their rows
+  const int NV = EPI == kGated ? 2 * NB : NB;
   const int Gq = meta_groups(G) / kMetaQuad;
   // this block's groups [gb, ge): the split-th of G, in whole groups
   const int gb = (int)((long long)G * sp / P.split), ge = (int)((long long)G * (sp + 1) / P.split);
@@ -246,7 +369,7 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2,
   // with fp16 outliers, the group's s goes to LDS too (the outlier terms
   // divide the staged X * s by it)
   __shared__ __attribute__((aligned(16))) _Float16 Ss[OUT ? 2 : 1][OUT ? kGroup : 8];
-  const bool has_out = OUT && P.orp != nullptr;
+  const bool has_out = OUT && (P.orp != nullptr || (EPI == kGated && S2.orp != nullptr));
   auto store_a = [&](int buf) {
 #pragma unroll
     for (int i = 0; i < A_PER_T; ++i) {
@@ -279,7 +402,18 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2,
       (void *)scales, (short)0, (int)min((size_t)0x7fffffff, meta_bytes), kRsrcWord3);
   const __amdgpu_buffer_rsrc_t zrs = __builtin_amdgcn_make_buffer_rsrc(
       (void *)zeros, (short)0, (int)min((size_t)0x7fffffff, meta_bytes), kRsrcWord3);
+  const __amdgpu_buffer_rsrc_t wrs2 = EPI == kGated ? __builtin_amdgcn_make_buffer_rsrc(
+      (void *)S2.Wq, (short)0, (int)min((size_t)0x7fffffff, (size_t)N * K * kCW / 2), kRsrcWord3) : wrs;
+  const __amdgpu_buffer_rsrc_t srs2 = EPI == kGated ? __builtin_amdgcn_make_buffer_rsrc(
+      (void *)S2.scales, (short)0, (int)min((size_t)0x7fffffff, meta_bytes), kRsrcWord3) : srs;
+  const __amdgpu_buffer_rsrc_t zrs2 = EPI == kGated ? __builtin_amdgcn_make_buffer_rsrc(
+      (void *)S2.zeros, (short)0, (int)min((size_t)0x7fffffff, meta_bytes), kRsrcWord3) : zrs;
   const int rb0 = n0 / kTileRows + wn * TN;  // first row block of this wave
+  // row block of the wave's tile j (gated: of the matrix that j's parity names)
+  auto row_block = [&](int j) {
+    const int v = min(rb0 + j, NV - 1);
+    return EPI == kGated ? v >> 1 : v;
+  };
   // INT8 tiles are twice as large: two 16-byte pieces per lane, the second
   // 1 KB after the first in LDS.  They use one LDS buffer, not two, so that
   // two workgroups still fit in a CU's LDS: each wave DMAs into and reads only
@@ -305,11 +439,11 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2,
   auto load_codes = [&](int g, int buf) {
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
-      const int rb = min(rb0 + j, NB - 1);
+      const int rb = row_block(j);
 #pragma unroll
       for (int h = 0; h < kCW; ++h)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            wrs,
+            j & 1 ? wrs2 : wrs,
             (__attribute__((address_space(3))) void *)(bslot(buf) + ((wave * TN + j) * kCW + h) * kTileBytes),
             16, (rb * 64 + lane) * 16 * kCW + 16 * h, g * tile_stride, 0, 0);
     }
@@ -317,11 +451,11 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2,
   auto load_meta = [&](int g, BRegs &b) {
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
-      const int rb = min(rb0 + j, NB - 1);
+      const int rb = row_block(j);
       const int mo = (rb * kTileRows + r) * kMetaQuad * 2;
       const int qo = (g / kMetaQuad) * meta_stride + (g % kMetaQuad) * 2;
-      b.sc[j] = __builtin_amdgcn_raw_buffer_load_b16(srs, mo, qo, 0);
-      b.zp[j] = __builtin_amdgcn_raw_buffer_load_b16(zrs, mo, qo, 0);
+      b.sc[j] = __builtin_amdgcn_raw_buffer_load_b16(j & 1 ? srs2 : srs, mo, qo, 0);
+      b.zp[j] = __builtin_amdgcn_raw_buffer_load_b16(j & 1 ? zrs2 : zrs, mo, qo, 0);
     }
   };
 
@@ -396,17 +530,22 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2,
   constexpr int kNone = 0x7fffffff;
   int oe = 0, oend = 0, ocol0 = kNone, ocol1 = kNone;
   float oval0 = 0.f, oval1 = 0.f;
+  // the arrays of the row this lane walks (gated: odd blocks are the second weight's)
+  const bool second = EPI == kGated && (c & 1);
+  const int32_t *orp = second ? S2.orp : P.orp, *ocol = second ? S2.ocol : P.ocol;
+  const _Float16 *oval = second ? S2.oval : P.oval;
   auto refill = [&](int &col, float &val) {
     col = kNone;
     if (oe < oend) {
-      col = P.ocol[oe];
-      val = (float)P.oval[oe];
+      col = ocol[oe];
+      val = (float)oval[oe];
       ++oe;
     }
   };
   auto outlier_start = [&]() {
-    const int n = n0 + (wn * TN + c) * 16 + r;
-    int lo = n < N ? P.orp[n] : 0, hi = n < N ? P.orp[n + 1] : 0;
+    const int n = EPI == kGated ? (n0 / 16 + wn * TN + c) / 2 * 16 + r : n0 + (wn * TN + c) * 16 + r;
+    const bool row = n < N && (EPI != kGated || orp);
+    int lo = row ? orp[n] : 0, hi = row ? orp[n + 1] : 0;
     oend = hi;
     // first entry at or after this K range (binary search; nothing to skip
     // for the first range)
@@ -415,7 +554,7 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2,
       while (__any(lo < hi)) {
         if (lo < hi) {
           const int mid = (lo + hi) >> 1;
-          if (P.ocol[mid] < kb)
+          if (ocol[mid] < kb)
             lo = mid + 1;
           else
             hi = mid;
@@ -584,9 +723,16 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2,
     }
   }
 
+  if constexpr (EPI != kPlain) {
+    if (P.split == 1) {
+      store_fused<EPI, TM, TN, BF>(P, find_fused<false>(ts, fs, block), acc, m0 + wm * TM * 16, rb0, c, r);
+      return;
+    }
+  }
   // lane holds D[4c + v][r] of each 16x16 sub-block: the output, or this
   // split's fp32 partial
-  float *part = P.split > 1 ? P.part + (size_t)sp * M * N : nullptr;
+  const int Np = EPI == kGated ? 2 * N : N;  // columns of a partial slab
+  float *part = P.split > 1 ? P.part + (size_t)sp * M * Np : nullptr;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
 #pragma unroll
@@ -595,9 +741,9 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2,
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         const int m = m0 + (wm * TM + i) * 16 + 4 * c + v;
-        if (m < M && n < N) {
+        if (m < M && n < Np) {
           if (part)
-            part[(size_t)m * N + n] = acc[i][j][v];
+            part[(size_t)m * Np + n] = acc[i][j][v];
           else if (BF)
             reinterpret_cast<uint16_t *>(P.Y)[(size_t)m * N + n] = f32_to_bf16(acc[i][j][v]);
           else
@@ -606,6 +752,18 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2,
       }
     }
   }
+}
+
+template <int WM, int WN, int TM, int TN, bool OUT, bool BF, bool W8 = false>
+__global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2, 2))) void tiled_kernel(
+    TiledSet ts) {
+  tiled_body<WM, WN, TM, TN, OUT, BF, W8, kPlain>(ts, NoFused{});
+}
+
+template <int WM, int WN, int TM, int TN, bool OUT, bool BF, bool W8, int EPI>
+__global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2, 2))) void tiled_fused_kernel(
+    TiledSet ts, TiledFused fs) {
+  tiled_body<WM, WN, TM, TN, OUT, BF, W8, EPI>(ts, fs);
 }
 
 // The tiled GEMM for INT4 codes without outliers (fp16 or bf16 activations,
@@ -641,9 +799,8 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2,
 // only down across workgroups and took 52-56 us against 61, while layers with
 // more blocks than slots (70B at M = 64) keep one slice.  (KS = 2 at TM = 8
 // needs more than 256 VGPRs.)
-template <int TM, int TN, int KS, bool BF = false, bool W8 = false>
-__global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(TN == 2 ? 4 : 2, TN == 2 ? 4 : 2))) void tiled_dma_kernel(
-    TiledSet ts) {
+template <int TM, int TN, int KS, bool BF, bool W8, int EPI, typename FS>
+__device__ __forceinline__ void tiled_dma_body(const TiledSet &ts, const FS &fs) {
   constexpr int WN = 4;
   constexpr int kCW = W8 ? 2 : 1;  // 16-byte code pieces per lane per tile
   static_assert(!(BF && W8), "INT8 codes: fp16 activations");
@@ -656,6 +813,7 @@ __global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(TN == 
 
   const int block = (int)blockIdx.x;
   const TiledProblem P = find_tiled<false>(ts, block);
+  const Second S2 = find_second(fs);
   const int M = P.M, N = P.N, K = P.K;
   const int tid = threadIdx.x, lane = tid & 63, wv = uniform_int(tid >> 6);
   const int ks = KS == 1 ? 0 : wv >> 2, wave = KS == 1 ? wv : wv & 3;  // K slice; the wave's column
@@ -718,7 +876,18 @@ __global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(TN == 
       (void *)P.scales, (short)0, (int)min((size_t)0x7fffffff, meta_bytes), kRsrcWord3);
   const __amdgpu_buffer_rsrc_t zrs = __builtin_amdgcn_make_buffer_rsrc(
       (void *)P.zeros, (short)0, (int)min((size_t)0x7fffffff, meta_bytes), kRsrcWord3);
+  const __amdgpu_buffer_rsrc_t wrs2 = EPI == kGated ? __builtin_amdgcn_make_buffer_rsrc(
+      (void *)S2.Wq, (short)0, (int)min((size_t)0x7fffffff, (size_t)N * K / 2 * kCW), kRsrcWord3) : wrs;
+  const __amdgpu_buffer_rsrc_t srs2 = EPI == kGated ? __builtin_amdgcn_make_buffer_rsrc(
+      (void *)S2.scales, (short)0, (int)min((size_t)0x7fffffff, meta_bytes), kRsrcWord3) : srs;
+  const __amdgpu_buffer_rsrc_t zrs2 = EPI == kGated ? __builtin_amdgcn_make_buffer_rsrc(
+      (void *)S2.zeros, (short)0, (int)min((size_t)0x7fffffff, meta_bytes), kRsrcWord3) : zrs;
   const int rb0 = n0 / kTileRows + wave * TN;
+  // row block of the wave's tile j (gated: of the matrix that j's parity names)
+  auto row_block = [&](int j) {
+    const int v = min(rb0 + j, (EPI == kGated ? 2 * NB : NB) - 1);
+    return EPI == kGated ? v >> 1 : v;
+  };
   const int tile_stride = NB * kTileBytes * kCW, meta_stride = NB * kTileRows * kMetaQuad * 2;
   // raw fp16 bits of each row block's scale and zero point: INT8 codes keep
   // both in one register (x: scale, y: zero point), which leaves the 128-row
@@ -735,20 +904,20 @@ __global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(TN == 
   auto load_b = [&](int g, BStage &b) {
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
-      const int rb = min(rb0 + j, NB - 1);
+      const int rb = row_block(j);
 #pragma unroll
       for (int h = 0; h < kCW; ++h)
         b.code[j][h] = __builtin_bit_cast(
-            u32x4, __builtin_amdgcn_raw_buffer_load_b128(wrs, (rb * 64 + lane) * 16 * kCW + 16 * h,
+            u32x4, __builtin_amdgcn_raw_buffer_load_b128(j & 1 ? wrs2 : wrs, (rb * 64 + lane) * 16 * kCW + 16 * h,
                                                          g * tile_stride, 0));
       const int mo = (rb * kTileRows + r) * kMetaQuad * 2;
       const int qo = (g / kMetaQuad) * meta_stride + (g % kMetaQuad) * 2;
       if constexpr (W8) {
-        b.sz[j][0] = __builtin_amdgcn_raw_buffer_load_b16(srs, mo, qo, 0);
-        b.sz[j][1] = __builtin_amdgcn_raw_buffer_load_b16(zrs, mo, qo, 0);
+        b.sz[j][0] = __builtin_amdgcn_raw_buffer_load_b16(j & 1 ? srs2 : srs, mo, qo, 0);
+        b.sz[j][1] = __builtin_amdgcn_raw_buffer_load_b16(j & 1 ? zrs2 : zrs, mo, qo, 0);
       } else {
-        b.sc[j] = __builtin_amdgcn_raw_buffer_load_b16(srs, mo, qo, 0);
-        b.zp[j] = __builtin_amdgcn_raw_buffer_load_b16(zrs, mo, qo, 0);
+        b.sc[j] = __builtin_amdgcn_raw_buffer_load_b16(j & 1 ? srs2 : srs, mo, qo, 0);
+        b.zp[j] = __builtin_amdgcn_raw_buffer_load_b16(j & 1 ? zrs2 : zrs, mo, qo, 0);
       }
     }
   };
@@ -895,6 +1064,13 @@ __global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(TN == 
         acc[i][j] += *reinterpret_cast<const float4v *>(&red[((i * TN + j) * 4 + wave) * 256 + lane * 4]);
   }
 
+  if constexpr (EPI != kPlain) {
+    if (P.split == 1) {
+      store_fused<EPI, TM, TN, BF>(P, find_fused<false>(ts, fs, block), acc, m0, rb0, c, r);
+      return;
+    }
+  }
+  const int Np = EPI == kGated ? 2 * N : N;  // columns of a partial slab
   // lane holds D[4c + v][r] of each 16x16 sub-block: the output, or this
   // split's fp32 partial
   if constexpr (TM <= 4) {
@@ -906,19 +1082,19 @@ __global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(TN == 
     // whole (N is a multiple of 16), a uniform test.
     const bool split = P.split > 1;
     const int esize = split ? 4 : 2;
-    char *out = split ? reinterpret_cast<char *>(P.part + (size_t)sp * M * N + (size_t)m0 * N)
+    char *out = split ? reinterpret_cast<char *>(P.part + (size_t)sp * M * Np + (size_t)m0 * Np)
                       : reinterpret_cast<char *>(P.Y) + (size_t)m0 * N * 2;
     const __amdgpu_buffer_rsrc_t yrs = __builtin_amdgcn_make_buffer_rsrc(
-        out, (short)0, (int)min((size_t)(M - m0) * N * esize, (size_t)0x7fffffff), kRsrcWord3);
+        out, (short)0, (int)min((size_t)(M - m0) * Np * esize, (size_t)0x7fffffff), kRsrcWord3);
     auto store_all = [&](auto &&store) {
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
         const int nb = n0 + (wave * TN + j) * 16;
-        if (nb >= N) continue;
+        if (nb >= Np) continue;
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
-          for (int v = 0; v < 4; ++v) store((i * 16 + 4 * c + v) * N + nb + r, acc[i][j][v]);
+          for (int v = 0; v < 4; ++v) store((i * 16 + 4 * c + v) * Np + nb + r, acc[i][j][v]);
       }
     };
     if (split)
@@ -932,7 +1108,7 @@ __global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(TN == 
       });
     return;
   }
-  float *part = P.split > 1 ? P.part + (size_t)sp * M * N : nullptr;
+  float *part = P.split > 1 ? P.part + (size_t)sp * M * Np : nullptr;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
 #pragma unroll
@@ -941,9 +1117,9 @@ __global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(TN == 
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         const int m = m0 + i * 16 + 4 * c + v;
-        if (m < M && n < N) {
+        if (m < M && n < Np) {
           if (part)
-            part[(size_t)m * N + n] = acc[i][j][v];
+            part[(size_t)m * Np + n] = acc[i][j][v];
           else if (BF)
             reinterpret_cast<uint16_t *>(P.Y)[(size_t)m * N + n] = f32_to_bf16(acc[i][j][v]);
           else
@@ -952,6 +1128,18 @@ __global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(TN == 
       }
     }
   }
+}
+
+template <int TM, int TN, int KS, bool BF, bool W8>
+__global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(TN == 2 ? 4 : 2, TN == 2 ? 4 : 2))) void tiled_dma_kernel(
+    TiledSet ts) {
+  tiled_dma_body<TM, TN, KS, BF, W8, kPlain>(ts, NoFused{});
+}
+
+template <int TM, int TN, int KS, bool BF, bool W8, int EPI>
+__global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(TN == 2 ? 4 : 2, TN == 2 ? 4 : 2))) void tiled_dma_fused_kernel(
+    TiledSet ts, TiledFused fs) {
+  tiled_dma_body<TM, TN, KS, BF, W8, EPI>(ts, fs);
 }
 
 // fp16(X * s) of the problems of a launch that have an s, rounded once like
@@ -1022,6 +1210,51 @@ __global__ __launch_bounds__(kReduceThreads) void split_reduce_kernel(TiledSet t
   }
 }
 
+// The same for a fused problem: Y (and the kept pre-activations) from the sums
+// of the partials, four outputs of one row per thread.  Gated partials hold the
+// alternating blocks, so G's quad lies 16 columns before U's.
+template <bool BF>
+__global__ __launch_bounds__(kReduceThreads) void split_reduce_fused_kernel(TiledSet ts, TiledFused fs) {
+  typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+  const TiledProblem P = find_tiled<true>(ts, (int)blockIdx.x);
+  const Fused F = find_fused<true>(ts, fs, (int)blockIdx.x);
+  const bool gated = uniform_int(fs.f[0].gated);
+  const int nq = P.N / 4;  // quads per row
+  const long long i = (long long)((int)blockIdx.x - P.rblock0) * kReduceThreads + threadIdx.x;
+  if (i >= (long long)P.M * nq) return;
+  const int m = (int)(i / nq), n = (int)(i - (long long)m * nq) * 4;
+  const size_t np = gated ? 2 * (size_t)P.N : (size_t)P.N;
+  const size_t src = (size_t)m * np + (gated ? 32 * (n / 16) + n % 16 : n), slab = (size_t)P.M * np;
+  auto sum = [&](size_t at) {
+    float4v a = *reinterpret_cast<const float4v *>(P.part + at);
+    for (int k = 1; k < P.split; ++k)
+      a += *reinterpret_cast<const float4v *>(P.part + at + (size_t)k * slab);
+    return a;
+  };
+  auto quad = [&](const void *p, size_t at) {
+    const u16x4 w = *reinterpret_cast<const u16x4 *>(static_cast<const uint16_t *>(p) + at);
+    return float4v{act_to_f32<BF>(w[0]), act_to_f32<BF>(w[1]), act_to_f32<BF>(w[2]), act_to_f32<BF>(w[3])};
+  };
+  const size_t out = (size_t)m * P.N + n;
+  auto put = [&](void *p, const float4v &x) {
+    *reinterpret_cast<u16x4 *>(static_cast<uint16_t *>(p) + out) =
+        u16x4{f32_to_act<BF>(x[0]), f32_to_act<BF>(x[1]), f32_to_act<BF>(x[2]), f32_to_act<BF>(x[3])};
+  };
+  float4v z = sum(src), y;
+  if (F.bias) z += quad(F.bias, n);
+  if (F.pre) put(F.pre, z);
+#pragma unroll
+  for (int v = 0; v < 4; ++v) y[v] = act_value(z[v], F.act);
+  if (gated) {
+    float4v u = sum(src + 16);
+    if (F.bias2) u += quad(F.bias2, n);
+    if (F.pre2) put(F.pre2, u);
+    y *= u;
+  }
+  if (F.residual) y += quad(F.residual, out);
+  put(P.Y, y);
+}
+
 // 64 x 256 blocks of 4 waves (64 x 64 each), two workgroups per CU: the
 // fastest of the measured shapes at every M of the workloads.
 template <int WM_, int WN_, int TM_, int TN_>
@@ -1045,7 +1278,19 @@ constexpr double kBlockStages = 2.0;
 constexpr double kReduceBytesPerUs = 4.0e6;
 
 int tiles_of(const GemmDesc &d, int bm = kBM, int bn = kBN) {
-  return ((d.N + bn - 1) / bn) * ((d.M + bm - 1) / bm);
+  return ((d.mats() * d.N + bn - 1) / bn) * ((d.M + bm - 1) / bm);
+}
+
+bool has_outliers(const GemmDesc &d) { return d.o_row_ptr || (d.fused && d.fused->orp2); }
+
+// Row tiles per wave of a tiled_kernel launch: kTM, but 3 (48-row blocks) for
+// fused problems with outliers, whose 64-row instances do not fit in 256 VGPRs
+// without spilling (fp16).
+constexpr int kOutFusedTM = 3;
+int regs_tm(const GemmDesc *d, int count) {
+  for (int i = 0; i < count; ++i)
+    if (d[i].fused && has_outliers(d[i])) return kOutFusedTM;
+  return kTM;
 }
 
 // tiled_dma_kernel takes fp16 or bf16 activations with INT4 codes, or fp16
@@ -1053,7 +1298,7 @@ int tiles_of(const GemmDesc &d, int bm = kBM, int bn = kBN) {
 // each) a buffer resource can cover; it serves launches whose largest M
 // exceeds 16.
 bool dma_capable(const GemmDesc &d) {
-  return !(d.w8 && d.bf16) && !d.o_row_ptr && (size_t)d.M * d.K * 2 < ((size_t)1 << 31);
+  return !(d.w8 && d.bf16) && !has_outliers(d) && (size_t)d.M * d.K * 2 < ((size_t)1 << 31);
 }
 constexpr int kDmaMinM = 17;
 
@@ -1105,7 +1350,7 @@ size_t prescale_need(const GemmDesc *d, int count) {
 }
 
 size_t part_bytes(const GemmDesc &d, int split) {
-  return split > 1 ? ((size_t)split * d.M * d.N * sizeof(float) + 255) / 256 * 256 : 0;
+  return split > 1 ? ((size_t)split * d.M * d.mats() * d.N * sizeof(float) + 255) / 256 * 256 : 0;
 }
 
 // Modelled time of one launch with the given splits: ceil(workgroups /
@@ -1121,7 +1366,7 @@ double launch_model(const GemmDesc *d, int count, const int *s, int bm, int bn, 
     const int G = d[i].K / kGroup;
     blocks += (long long)tiles_of(d[i], bm, bn) * s[i];
     longest = std::max(longest, ((G + s[i] - 1) / s[i] + ks - 1) / ks);
-    if (s[i] > 1) reduce_bytes += (double)(4 * s[i] + 2) * d[i].M * d[i].N;
+    if (s[i] > 1) reduce_bytes += (double)(4 * s[i] + 2) * d[i].M * d[i].mats() * d[i].N;
   }
   const long long rounds = (blocks + slots - 1) / slots;
   return (double)rounds * (longest + kBlockStages) * kStageUs + reduce_bytes / kReduceBytesPerUs;
@@ -1191,29 +1436,58 @@ int dma_plan(const GemmDesc *d, int count, int tm, bool unsplit, int *split) {
 }
 
 // The tiled_dma_kernel instance of a DMA plan (dma_tm's TM, dma_plan's K
-// slices) for one activation type and code width; any other shape is an
-// error, never a launch with a grid planned for another tile.
+// slices) for one activation type, code width and epilogue; any other shape is
+// an error, never a launch with a grid planned for another tile.
+template <int TM, int TN, int KS, bool BF, bool W8>
+void launch_dma_tile(int epi, dim3 grid, hipStream_t stream, const TiledSet &ts, const TiledFused &fs) {
+  const dim3 threads(256 * KS);
+  if (epi == kPlain)
+    hipLaunchKernelGGL((tiled_dma_kernel<TM, TN, KS, BF, W8>), grid, threads, 0, stream, ts);
+  else if (epi == kLinear)
+    hipLaunchKernelGGL((tiled_dma_fused_kernel<TM, TN, KS, BF, W8, kLinear>), grid, threads, 0,
+                       stream, ts, fs);
+  else
+    hipLaunchKernelGGL((tiled_dma_fused_kernel<TM, TN, KS, BF, W8, kGated>), grid, threads, 0,
+                       stream, ts, fs);
+}
 template <bool BF, bool W8>
-hipError_t launch_dma(int tm, int ks, dim3 grid, hipStream_t stream, const TiledSet &ts) {
+hipError_t launch_dma(int tm, int ks, int epi, dim3 grid, hipStream_t stream, const TiledSet &ts,
+                      const TiledFused &fs) {
   if (tm == 8 && ks == 1)
-    hipLaunchKernelGGL((tiled_dma_kernel<8, 4, 1, BF, W8>), grid, dim3(256), 0, stream, ts);
+    launch_dma_tile<8, 4, 1, BF, W8>(epi, grid, stream, ts, fs);
   else if (tm == 6 && ks == 1)
-    hipLaunchKernelGGL((tiled_dma_kernel<6, 4, 1, BF, W8>), grid, dim3(256), 0, stream, ts);
+    launch_dma_tile<6, 4, 1, BF, W8>(epi, grid, stream, ts, fs);
   else if (tm == 4 && ks == 2)
-    hipLaunchKernelGGL((tiled_dma_kernel<4, 2, 2, BF, W8>), grid, dim3(512), 0, stream, ts);
+    launch_dma_tile<4, 2, 2, BF, W8>(epi, grid, stream, ts, fs);
   else if (tm == 4 && ks == 1)
-    hipLaunchKernelGGL((tiled_dma_kernel<4, 2, 1, BF, W8>), grid, dim3(256), 0, stream, ts);
+    launch_dma_tile<4, 2, 1, BF, W8>(epi, grid, stream, ts, fs);
   else if (tm == 3 && ks == 2)
-    hipLaunchKernelGGL((tiled_dma_kernel<3, 2, 2, BF, W8>), grid, dim3(512), 0, stream, ts);
+    launch_dma_tile<3, 2, 2, BF, W8>(epi, grid, stream, ts, fs);
   else if (tm == 3 && ks == 1)
-    hipLaunchKernelGGL((tiled_dma_kernel<3, 2, 1, BF, W8>), grid, dim3(256), 0, stream, ts);
+    launch_dma_tile<3, 2, 1, BF, W8>(epi, grid, stream, ts, fs);
   else if (tm == 2 && ks == 2)
-    hipLaunchKernelGGL((tiled_dma_kernel<2, 2, 2, BF, W8>), grid, dim3(512), 0, stream, ts);
+    launch_dma_tile<2, 2, 2, BF, W8>(epi, grid, stream, ts, fs);
   else if (tm == 2 && ks == 1)
-    hipLaunchKernelGGL((tiled_dma_kernel<2, 2, 1, BF, W8>), grid, dim3(256), 0, stream, ts);
+    launch_dma_tile<2, 2, 1, BF, W8>(epi, grid, stream, ts, fs);
   else
     return hipErrorInvalidValue;
   return hipSuccess;
+}
+
+// The tiled_kernel instance for one activation type, code width, presence of
+// outliers and epilogue.
+template <bool OUT, bool BF, bool W8>
+void launch_regs(int epi, dim3 grid, hipStream_t stream, const TiledSet &ts, const TiledFused &fs) {
+  const dim3 threads(kWM * kWN * 64);
+  constexpr int FTM = OUT ? kOutFusedTM : kTM;  // as regs_tm
+  if (epi == kPlain)
+    hipLaunchKernelGGL((tiled_kernel<kWM, kWN, kTM, kTN, OUT, BF, W8>), grid, threads, 0, stream, ts);
+  else if (epi == kLinear)
+    hipLaunchKernelGGL((tiled_fused_kernel<kWM, kWN, FTM, kTN, OUT, BF, W8, kLinear>), grid, threads,
+                       0, stream, ts, fs);
+  else
+    hipLaunchKernelGGL((tiled_fused_kernel<kWM, kWN, FTM, kTN, OUT, BF, W8, kGated>), grid, threads,
+                       0, stream, ts, fs);
 }
 
 }  // namespace
@@ -1226,7 +1500,7 @@ size_t tiled_workspace_bytes(const GemmDesc *d, int count) {
   if (dma)
     dma_plan(d, count, tm, false, split);
   else
-    choose_splits(d, count, split);
+    choose_splits(d, count, split, 16 * regs_tm(d, count));
   size_t bytes = dma ? prescale_need(d, count) : 0;
   for (int i = 0; i < count; ++i) bytes += part_bytes(d[i], split[i]);
   return bytes;
@@ -1245,13 +1519,13 @@ hipError_t launch_tiled_set(const GemmDesc *d, int count, void *workspace, size_
   const int tm = dma_tm(d, count);
   const bool dma = tm != 0 && pre <= have;
   const DmaShape ds = dma_shape(tm);
-  const int bm = dma ? ds.bm() : kBM, bn = dma ? ds.bn() : kBN;
+  const int bm = dma ? ds.bm() : 16 * regs_tm(d, count), bn = dma ? ds.bn() : kBN;
   int split[kMaxTiled];
   int ks = 1;
   if (dma)
     ks = dma_plan(d, count, tm, false, split);
   else
-    choose_splits(d, count, split);
+    choose_splits(d, count, split, bm);
   size_t parts = 0;
   for (int i = 0; i < count; ++i) parts += part_bytes(d[i], split[i]);
   if ((dma ? pre : 0) + parts > have) {  // no room for partials: one K range
@@ -1259,6 +1533,7 @@ hipError_t launch_tiled_set(const GemmDesc *d, int count, void *workspace, size_
     if (dma) ks = dma_plan(d, count, tm, true, split);
   }
   TiledSet ts = {};
+  TiledFused fs = {};
   int blocks = 0, rblocks = 0;
   size_t off = 0;
   // prescaled X * s after the partials
@@ -1278,7 +1553,7 @@ hipError_t launch_tiled_set(const GemmDesc *d, int count, void *workspace, size_
     p.M = d[i].M;
     p.N = d[i].N;
     p.K = d[i].K;
-    p.tiles_n = (d[i].N + bn - 1) / bn;
+    p.tiles_n = (d[i].mats() * d[i].N + bn - 1) / bn;
     p.tiles = tiles_of(d[i], bm, bn);
     p.split = split[i];
     p.part = split[i] > 1 ? reinterpret_cast<float *>(static_cast<char *>(workspace) + off) : nullptr;
@@ -1286,7 +1561,8 @@ hipError_t launch_tiled_set(const GemmDesc *d, int count, void *workspace, size_
     p.orp = static_cast<const int32_t *>(d[i].o_row_ptr);
     p.ocol = static_cast<const int32_t *>(d[i].o_col);
     p.oval = static_cast<const _Float16 *>(d[i].o_val);
-    out |= d[i].o_row_ptr != nullptr;
+    out |= has_outliers(d[i]);
+    if (d[i].fused) fs.f[i] = *d[i].fused;
     p.bf16 = d[i].bf16;
     p.xs = static_cast<const _Float16 *>(d[i].X);
     if (dma && d[i].s) {
@@ -1324,38 +1600,40 @@ hipError_t launch_tiled_set(const GemmDesc *d, int count, void *workspace, size_
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const dim3 grid(blocks), threads(kWM * kWN * 64);
+  const dim3 grid(blocks);
+  // one activation type, code width and kind of epilogue per launch
+  const int epi = !d[0].fused ? kPlain : d[0].gated() ? kGated : kLinear;
   if (dma) {
-    const hipError_t e = d[0].w8     ? launch_dma<false, true>(tm, ks, grid, stream, ts)
-                         : d[0].bf16 ? launch_dma<true, false>(tm, ks, grid, stream, ts)
-                                     : launch_dma<false, false>(tm, ks, grid, stream, ts);
+    const hipError_t e = d[0].w8     ? launch_dma<false, true>(tm, ks, epi, grid, stream, ts, fs)
+                         : d[0].bf16 ? launch_dma<true, false>(tm, ks, epi, grid, stream, ts, fs)
+                                     : launch_dma<false, false>(tm, ks, epi, grid, stream, ts, fs);
     if (e != hipSuccess) return e;
   } else if (d[0].w8 && d[0].bf16 && out)  // INT8 codes
-    hipLaunchKernelGGL((tiled_kernel<kWM, kWN, kTM, kTN, true, true, true>), grid, threads, 0,
-                       stream, ts);
+    launch_regs<true, true, true>(epi, grid, stream, ts, fs);
   else if (d[0].w8 && d[0].bf16)
-    hipLaunchKernelGGL((tiled_kernel<kWM, kWN, kTM, kTN, false, true, true>), grid, threads, 0,
-                       stream, ts);
+    launch_regs<false, true, true>(epi, grid, stream, ts, fs);
   else if (d[0].w8 && out)
-    hipLaunchKernelGGL((tiled_kernel<kWM, kWN, kTM, kTN, true, false, true>), grid, threads, 0,
-                       stream, ts);
+    launch_regs<true, false, true>(epi, grid, stream, ts, fs);
   else if (d[0].w8)
-    hipLaunchKernelGGL((tiled_kernel<kWM, kWN, kTM, kTN, false, false, true>), grid, threads, 0,
-                       stream, ts);
-  else if (d[0].bf16 && out)  // one activation type (and code width) per launch
-    hipLaunchKernelGGL((tiled_kernel<kWM, kWN, kTM, kTN, true, true>), grid, threads, 0, stream, ts);
+    launch_regs<false, false, true>(epi, grid, stream, ts, fs);
+  else if (d[0].bf16 && out)
+    launch_regs<true, true, false>(epi, grid, stream, ts, fs);
   else if (d[0].bf16)
-    hipLaunchKernelGGL((tiled_kernel<kWM, kWN, kTM, kTN, false, true>), grid, threads, 0, stream,
-                       ts);
+    launch_regs<false, true, false>(epi, grid, stream, ts, fs);
   else if (out)
-    hipLaunchKernelGGL((tiled_kernel<kWM, kWN, kTM, kTN, true, false>), grid, threads, 0, stream,
-                       ts);
+    launch_regs<true, false, false>(epi, grid, stream, ts, fs);
   else
-    hipLaunchKernelGGL((tiled_kernel<kWM, kWN, kTM, kTN, false, false>), grid, threads, 0, stream,
-                       ts);
+    launch_regs<false, false, false>(epi, grid, stream, ts, fs);
   hipError_t err = hipGetLastError();
   if (err == hipSuccess && rblocks > 0) {
-    hipLaunchKernelGGL(split_reduce_kernel, dim3(rblocks), dim3(kReduceThreads), 0, stream, ts);
+    if (epi == kPlain)
+      hipLaunchKernelGGL(split_reduce_kernel, dim3(rblocks), dim3(kReduceThreads), 0, stream, ts);
+    else if (d[0].bf16)
+      hipLaunchKernelGGL(split_reduce_fused_kernel<true>, dim3(rblocks), dim3(kReduceThreads), 0,
+                         stream, ts, fs);
+    else
+      hipLaunchKernelGGL(split_reduce_fused_kernel<false>, dim3(rblocks), dim3(kReduceThreads), 0,
+                         stream, ts, fs);
     err = hipGetLastError();
   }
   return err;

@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "epilogue.h"
+
 namespace w4a16 {
 
 // Bits of the packer's device status word.
@@ -54,6 +56,11 @@ struct GemmDesc {
   // streaming path, bf16: workspace for X * s prescaled once per call
   // (skinny_prescale_bytes(M, K) bytes), set by launch_skinny_set
   void *xpre = nullptr;
+  // fused epilogue (all or none of a call's problems), or null
+  const Fused *fused = nullptr;
+  bool gated() const { return fused && fused->gated; }
+  int mats() const { return gated() ? 2 : 1; }              // weights of the problem
+  int row_blocks() const { return mats() * (N / 16); }      // of all its weights
 };
 
 // Streaming kernel for small M (decode and speculative verify): M <= 16.
@@ -83,6 +90,39 @@ hipError_t launch_tiled_set(const GemmDesc *problems, int count, void *workspace
                             size_t workspace_bytes, hipStream_t stream);
 hipError_t launch_tiled(const void *X, const void *Wq, const void *scales, const void *zeros,
                         const void *s, void *Y, int M, int N, int K, hipStream_t stream);
+
+// Transposed copy of a packed weight for the backward product: codes Wt and
+// per-128-row metadata (asynchronous).
+hipError_t launch_transpose(const void *Wq, const void *scales, const void *zeros, int N, int K,
+                            bool w8, void *Wt, void *meta, hipStream_t stream);
+
+// Gradients of an epilogue: dz = dY * act'(z) and, when u is set, gated: dz =
+// dY * u * act'(z), du = dY * act(z).  z null: dz is dY (not written).  db, db2:
+// fp32 column sums of dz and du (null: not wanted), which take
+// grad_workspace_bytes(M, N, how many) of workspace.
+struct GradDesc {
+  const void *dY, *z, *u;
+  void *dz, *du, *db, *db2;
+  int M, N, act;
+  bool bf16;
+};
+size_t grad_workspace_bytes(int M, int N, int sums);
+hipError_t launch_grad(const GradDesc &d, void *workspace, hipStream_t stream);
+
+// dX = add + s * sum over the terms of dZ . D (M >= 1, validated by the caller;
+// the workspace holds dx_workspace_bytes()).
+constexpr int kMaxDxTerms = 4;
+struct DxDesc {
+  int count;
+  const void *dZ[kMaxDxTerms], *Wt[kMaxDxTerms], *meta[kMaxDxTerms];
+  int N[kMaxDxTerms];
+  const void *s, *add;
+  void *dX;
+  int M, K;
+  bool bf16, w8;
+};
+size_t dx_workspace_bytes(const DxDesc &d);
+hipError_t launch_dx(const DxDesc &d, void *workspace, hipStream_t stream);
 
 // Speculative-sampling verification of B sequences (validated by the caller):
 // the vocabulary is cut into spec_verify_chunks(V) chunks, and the workspace
