@@ -138,7 +138,7 @@ def run_linear(M, N, K, dtype, act="none", bias=False, residual=False, pre=False
     Z, zbuf = guarded(dtype, M, N) if pre else (None, None)
     call = w4.LinearCall([(X, w.pw, w.sd, Y, w4.Epilogue(b, ACT[act], R, Z))])
     if not workspace:
-        call.ws_ptr, call.ws_bytes = None, 0
+        call.args = (*call.args[:-2], None, 0)
     call()
     ref, z = of.linear(Xv, w.W, bv, act, Rv)
     u = U[dtype]
@@ -169,7 +169,7 @@ def run_gated(M, N, K, dtype, act="silu", bias=False, pre=False, awq=False, bits
     call = w4.GatedCall(X, wg.pw, wu.pw, wg.sd, H, ACT[act], bg, bu,
                         tuple(t for t, _ in saved) or None)
     if not workspace:
-        call.ws_ptr, call.ws_bytes = None, 0
+        call.args = (*call.args[:-2], None, 0)
     call()
     ref, g, uu = of.gated(Xv, wg.W, wu.W, act, bgv, buv)
     u = U[dtype]

@@ -167,13 +167,25 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
   if (GATED) column_sums(s1, a.part2);
 }
 
-// out[n] = the strips' sums, in order (0 without strips).
+// out[n] = the strips' sums (0 without strips): 8 lanes per column, each over
+// every 8th strip, then the lanes in order.  (One thread per column, one load
+// after the other, took 13 us for 50 strips of 3584 columns.)
 __global__ __launch_bounds__(256) void bias_kernel(const float *part, int strips, int N, float *out) {
-  const int n = (int)blockIdx.x * 256 + (int)threadIdx.x;
-  if (n >= N) return;
+  const int x = threadIdx.x & 31, lane = threadIdx.x >> 5;
+  const int n = (int)blockIdx.x * 32 + x;
   float s = 0.f;
-  for (int k = 0; k < strips; ++k) s += part[(size_t)k * N + n];
-  out[n] = s;
+  if (n < N) {
+#pragma unroll 4
+    for (int k = lane; k < strips; k += 8) s += part[(size_t)k * N + n];
+  }
+  __shared__ float red[8][32];
+  red[lane][x] = s;
+  __syncthreads();
+  if (lane == 0 && n < N) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) s += red[i][x];
+    out[n] = s;
+  }
 }
 
 // ---- dX ------------------------------------------------------------------------------
@@ -210,19 +222,25 @@ struct DxArgs {
 // and scale to fp32 first would take 7.
 // N is split across workgroups when the output blocks leave CUs idle: fp32
 // partials, added in a fixed order by dx_reduce_kernel.
-template <int TM, int TN, bool BF, bool W8>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TN == 2 ? 4 : 2, TN == 2 ? 4 : 2))) void dx_kernel(
+// KS = 2: two slices of four waves each walk every other stage of the
+// workgroup's range into LDS stages of their own, and the sums meet through
+// LDS at the end (slice 0's plus slice 1's): two waves per SIMD without fp32
+// partials in memory.
+template <int TM, int TN, int KS, bool BF, bool W8>
+__global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(TN == 2 ? 4 : 2, TN == 2 ? 4 : 2))) void dx_kernel(
     DxArgs P) {
   constexpr int kCW = W8 ? 2 : 1;  // 16-byte code pieces per lane per tile
   constexpr int BM = TM * 16, BN = 64 * TN;
   constexpr int kRowChunks = kGroup / 8;  // 16-byte chunks per row per stage
   constexpr int kDma = TM;                // DMA loads per wave per stage
   static_assert(kDma * 4 * 64 == BM * kRowChunks, "a stage is whole DMA loads");
-  __shared__ __attribute__((aligned(16))) _Float16 As[2][BM * kGroup];
-  __shared__ __attribute__((aligned(16))) unsigned char Ms[2][1024];
+  static_assert(KS == 1 || BM * BN * 4 <= KS * 2 * BM * kGroup * 2, "the slices' sums fit the dZ stages");
+  __shared__ __attribute__((aligned(16))) _Float16 As[KS][2][BM * kGroup];
+  __shared__ __attribute__((aligned(16))) unsigned char Ms[KS][2][1024];
 
   const int M = P.M, K = P.K;
-  const int tid = threadIdx.x, lane = tid & 63, wave = uniform_int(tid >> 6);
+  const int tid = threadIdx.x, lane = tid & 63, wv = uniform_int(tid >> 6);
+  const int ks = KS == 1 ? 0 : wv >> 2, wave = KS == 1 ? wv : wv & 3;  // slice; the wave's column
   const int c = lane >> 4, r = lane & 15;
   // Workgroups go to the eight XCDs round robin: a split launch is renumbered
   // so that each XCD takes a contiguous run of (split, block) pairs, which
@@ -261,19 +279,20 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TN == 2 ? 4
         (void *)T.meta, (short)0, (int)min((size_t)0x7fffffff, (size_t)NG * G * kMetaBytes), kRsrcWord3);
     const int row0 = 4 * wave + (lane >> 4), lc = (lane & 15) ^ row0;
     const int xoff = (row0 * N + 8 * lc) * 2;
-    auto load_x = [&](int g, int buf) {
-      const int vo = 8 * lc < N - g * kGroup ? xoff : kOutOfRange;
+    // (left: columns of the stage that count, 0 for one past the range)
+    auto load_x = [&](int g, int left, int buf) {
+      const int vo = 8 * lc < left ? xoff : kOutOfRange;
 #pragma unroll
       for (int u = 0; u < kDma; ++u) {
         const int vu = (int)((unsigned)vo + 32u * u * N);  // still out of range where vo is
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            xrs, (__attribute__((address_space(3))) void *)(&As[buf][(u * 4 + wave) * 64 * 8]), 16,
+            xrs, (__attribute__((address_space(3))) void *)(&As[ks][buf][(u * 4 + wave) * 64 * 8]), 16,
             vu, g * kGroup * 2, 0, 0);
       }
       // scales and zero points of the block's quantization groups: 256 bytes a wave
       const int mo = (wave * 64 + lane) * 4;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          mrs, (__attribute__((address_space(3))) void *)(&Ms[buf][wave * 256]), 4, mo,
+          mrs, (__attribute__((address_space(3))) void *)(&Ms[ks][buf][wave * 256]), 4, mo,
           (g * G + k0 / kGroup) * kMetaBytes, 0, 0);
     };
     const int kb0 = k0 / kTileRows + wave * TN;
@@ -297,7 +316,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TN == 2 ? 4
     const int ul = (wave * TN * kTileRows) / kGroup;
 
     auto compute = [&](const BStage &b, int buf) {
-      const _Float16 *ms = reinterpret_cast<const _Float16 *>(&Ms[buf][ul * kMetaBytes]) + 8 * c;
+      const _Float16 *ms = reinterpret_cast<const _Float16 *>(&Ms[ks][buf][ul * kMetaBytes]) + 8 * c;
       struct Meta {
         half8 scale, bias;
       };
@@ -336,7 +355,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TN == 2 ? 4
         }
         return out;
       };
-      const _Float16 *abuf = As[buf];
+      const _Float16 *abuf = As[ks][buf];
       // software pipeline: k step tt + 1's B operands are dequantized while k
       // step tt's MFMAs run
       u32x4 bop[TN];
@@ -373,24 +392,47 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TN == 2 ? 4
     // the next stage's, compute.  Past the range the loads re-read its last
     // stage into buffers and registers that nobody reads.
     BStage b0, b1;
-    auto step = [&](int g, BStage &cur, BStage &nxt, int buf) {
+    // stage i of this slice; every slice runs the same number of steps (and
+    // barriers), and one past the range adds zeros: its dZ is read as zeros
+    const int nsteps = (ge - gb + KS - 1) / KS;
+    auto load_stage = [&](int i, BStage &b, int buf) {
+      const int g = gb + ks + min(i, nsteps - 1) * KS, gc = KS == 1 ? g : min(g, ge - 1);
+      load_x(gc, KS == 1 || g < ge ? N - g * kGroup : 0, buf);
+      load_b(gc, b);
+    };
+    auto step = [&](int i, BStage &cur, BStage &nxt, int buf) {
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      const int gn = min(g + 1, ge - 1);
-      load_x(gn, buf ^ 1);
-      load_b(gn, nxt);
+      load_stage(i + 1, nxt, buf ^ 1);
       compute(cur, buf);
     };
     // the term before may still be read, and its last loads still land, in LDS
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    load_x(gb, 0);
-    load_b(gb, b0);
-    for (int g = gb; g < ge; g += 2) {
-      step(g, b0, b1, 0);
-      if (g + 1 < ge) step(g + 1, b1, b0, 1);
+    load_stage(0, b0, 0);
+    for (int i = 0; i < nsteps; i += 2) {
+      step(i, b0, b1, 0);
+      if (i + 1 < nsteps) step(i + 1, b1, b0, 1);
     }
   }
   // the last step's DMA must land before the workgroup's LDS is released
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  if constexpr (KS == 2) {
+    float *red = reinterpret_cast<float *>(&As[0][0][0]);
+    __syncthreads();  // every wave is done with the dZ stages
+    if (ks == 1) {
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+          *reinterpret_cast<float4v *>(&red[((i * TN + j) * 4 + wave) * 256 + lane * 4]) = acc[i][j];
+    }
+    __syncthreads();
+    if (ks == 1) return;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+        acc[i][j] += *reinterpret_cast<const float4v *>(&red[((i * TN + j) * 4 + wave) * 256 + lane * 4]);
+  }
 
   // lane holds D[4c + v][r] of each 16x16 sub-block.  Buffer resources that
   // start at the sub-block's first row and end at row M drop rows past M; a
@@ -493,49 +535,65 @@ int strips_of(int M, int N, bool sums) {
 }
 
 struct DxPlan {
-  int tm, tn, split, stages;
+  int tm, tn, ks, split, stages;
   long long tiles;
 };
-constexpr int kDxMaxSplit = 16;
-constexpr int kDxMinStages = 8;  // stages per split at the shortest
+// A block shape and its time per step (ks stages) with one and with two
+// workgroups on a CU, in us (measured with bf16 activations and INT4 codes).
+struct DxShape {
+  int tm, tn, ks;
+  double one, two;
+};
+constexpr int kDxMaxSplit = 32;
 
-// The block shape goes by M, as few 16-row tiles as cover it (128 x 256 blocks
-// above 64 rows), the split of the stages by a model of the launch: rounds of
-// workgroups that fill the GPU, each as long as its stages plus a fixed cost,
-// plus the partials' traffic.
+// Blocks of 128 x 256 (96 x 256 for INT8 codes, whose registers do not allow
+// 128) for large products; 64 x 128, 32 x 128 or 16 x 128, as few rows as cover
+// a small M, with two slices per workgroup, where those would leave CUs idle.  The
+// stages are split across workgroups (fp32 partials) and the shape is chosen by
+// a model of the launch: rounds of at most two workgroups per CU, each as long
+// as its steps, plus the partials' traffic and the second launch.  Measured, in
+// us: M = 2048, N = 14336, K = 4096: 128 x 256 split in two 211, 64 x 128 289;
+// M = 200, N = K = 3584: 128 x 256 split in four 27.2, 64 x 128 split in four
+// 16.7 (one slice: 17.4); M = 64, N = 2 x 14336, K = 4096: 42.6 and 29.2 (34.4).
 DxPlan plan_dx(const DxDesc &d) {
-  DxPlan p;
-  p.tm = d.M > 64 ? (d.w8 ? 6 : 8) : d.M > 32 ? 4 : d.M > 16 ? 2 : 1;
-  p.tn = p.tm >= 6 ? 4 : 2;
-  p.stages = 0;
-  for (int i = 0; i < d.count; ++i) p.stages += (d.N[i] + kGroup - 1) / kGroup;
-  p.tiles = (long long)((d.K + 64 * p.tn - 1) / (64 * p.tn)) * ((d.M + 16 * p.tm - 1) / (16 * p.tm));
-  const long long slots = p.tn == 4 ? 512 : 1024;
-  double best = 0.0;
-  p.split = 1;
-  for (int s = 1; s <= kDxMaxSplit && (s == 1 || p.stages / s >= kDxMinStages); ++s) {
-    const long long rounds = (p.tiles * s + slots - 1) / slots;
-    const double us = (double)rounds * ((p.stages + s - 1) / s + 2.0) * 2.3 +
-                      (s > 1 ? (double)(4 * s + 2) * d.M * d.K / 4.0e6 : 0.0);
-    if (s == 1 || us < best) {
-      best = us;
-      p.split = s;
+  static const DxShape large = {8, 4, 1, 2.9, 3.5}, large8 = {6, 4, 1, 2.5, 3.1};
+  static const DxShape s64 = {4, 2, 2, 1.55, 2.65}, s32 = {2, 2, 2, 1.3, 2.4}, s16 = {1, 2, 2, 1.2, 2.2};
+  DxPlan best = {};
+  double best_us = 0.0;
+  int stages = 0;
+  for (int i = 0; i < d.count; ++i) stages += (d.N[i] + kGroup - 1) / kGroup;
+  const DxShape *const small = d.M > 32 ? &s64 : d.M > 16 ? &s32 : &s16;
+  const DxShape *const shapes[2] = {small, d.M > 64 ? (d.w8 ? &large8 : &large) : nullptr};
+  for (const DxShape *s : shapes) {
+    if (!s) continue;
+    const long long tiles =
+        (long long)((d.K + 64 * s->tn - 1) / (64 * s->tn)) * ((d.M + 16 * s->tm - 1) / (16 * s->tm));
+    for (int split = 1; split <= kDxMaxSplit && split <= stages; ++split) {
+      const long long wgs = tiles * split, rest = wgs % 512;
+      const double rounds = (double)(wgs / 512) * s->two + (rest == 0 ? 0.0 : rest <= 256 ? s->one : s->two);
+      const int steps = ((stages + split - 1) / split + s->ks - 1) / s->ks;
+      const double mk = (double)d.M * d.K;
+      const double us = rounds * (steps + 0.5) +
+                        (split > 1 ? 2.5 + (4 * split + 2) * mk / 4.5e6 + (4 * split - 2) * mk / 9.0e6 : 0.0);
+      if (best.split == 0 || us < best_us) {
+        best_us = us;
+        best = {s->tm, s->tn, s->ks, split, stages, tiles};
+      }
     }
   }
-  return p;
+  return best;
 }
 
 template <bool BF, bool W8>
-void launch_dx_tile(int tm, dim3 grid, hipStream_t stream, const DxArgs &a) {
-  constexpr int kLarge = W8 ? 6 : 8;
-  if (tm == kLarge)
-    hipLaunchKernelGGL((dx_kernel<kLarge, 4, BF, W8>), grid, dim3(256), 0, stream, a);
-  else if (tm == 4)
-    hipLaunchKernelGGL((dx_kernel<4, 2, BF, W8>), grid, dim3(256), 0, stream, a);
-  else if (tm == 2)
-    hipLaunchKernelGGL((dx_kernel<2, 2, BF, W8>), grid, dim3(256), 0, stream, a);
-  else
-    hipLaunchKernelGGL((dx_kernel<1, 2, BF, W8>), grid, dim3(256), 0, stream, a);
+void launch_dx_tile(const DxPlan &p, dim3 grid, hipStream_t stream, const DxArgs &a) {
+#define W4_DX(TM, TN, KS)                                                                        \
+  if (p.tm == TM && p.tn == TN && p.ks == KS)                                                    \
+  hipLaunchKernelGGL((dx_kernel<TM, TN, KS, BF, W8>), grid, dim3(256 * KS), 0, stream, a)
+  W4_DX((W8 ? 6 : 8), 4, 1);
+  W4_DX(4, 2, 2);
+  W4_DX(2, 2, 2);
+  W4_DX(1, 2, 2);
+#undef W4_DX
 }
 
 }  // namespace
@@ -587,7 +645,7 @@ hipError_t launch_grad(const GradDesc &d, void *workspace, hipStream_t stream) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const dim3 bg((unsigned)((d.N + 255) / 256)), th(256);
+  const dim3 bg((unsigned)((d.N + 31) / 32)), th(256);
   if (d.db) hipLaunchKernelGGL(bias_kernel, bg, th, 0, stream, a.part, strips, d.N, static_cast<float *>(d.db));
   if (d.db2) hipLaunchKernelGGL(bias_kernel, bg, th, 0, stream, a.part2, strips, d.N, static_cast<float *>(d.db2));
   return hipGetLastError();
@@ -622,13 +680,13 @@ hipError_t launch_dx(const DxDesc &d, void *workspace, hipStream_t stream) {
   a.stages = p.stages;
   const dim3 grid((unsigned)(p.tiles * p.split));
   if (d.bf16 && d.w8)
-    launch_dx_tile<true, true>(p.tm, grid, stream, a);
+    launch_dx_tile<true, true>(p, grid, stream, a);
   else if (d.bf16)
-    launch_dx_tile<true, false>(p.tm, grid, stream, a);
+    launch_dx_tile<true, false>(p, grid, stream, a);
   else if (d.w8)
-    launch_dx_tile<false, true>(p.tm, grid, stream, a);
+    launch_dx_tile<false, true>(p, grid, stream, a);
   else
-    launch_dx_tile<false, false>(p.tm, grid, stream, a);
+    launch_dx_tile<false, false>(p, grid, stream, a);
   hipError_t err = hipGetLastError();
   if (err == hipSuccess && p.split > 1) {
     const dim3 rg((unsigned)(((long long)d.M * d.K / 4 + 255) / 256));

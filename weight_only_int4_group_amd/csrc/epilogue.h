@@ -10,8 +10,7 @@
 // Activations (act_value) and their derivatives (act_grad):
 //   relu       max(z, 0); derivative 1 for z > 0, else 0
 //   silu       z * sg(z), sg(z) = 1 / (1 + exp(-z));  sg + z sg (1 - sg)
-//   gelu       z Phi(z), Phi(z) = erfc(-z / sqrt 2) / 2 (erfc, not 1 + erf, which
-//              cancels for z < -3);  Phi(z) + z exp(-z^2 / 2) / sqrt(2 pi)
+//   gelu       z Phi(z), Phi the normal distribution function;  Phi(z) + z phi(z)
 //   gelu_tanh  z (1 + tanh u) / 2 = z sg(2u), u = sqrt(2 / pi) (z + 0.044715 z^3);
 //              sg(2u) + z sg(2u) (1 - sg(2u)) 2 u'
 // sg takes the hardware reciprocal (1 ulp of fp32, 2^-23 relative): far below the
@@ -45,6 +44,22 @@ __device__ __forceinline__ float sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
 }
 
+// Phi(z), with e = exp(-z^2 / 2) given: Abramowitz and Stegun, formula 7.1.26,
+// erfc(x) = (a1 t + ... + a5 t^5) exp(-x^2), t = 1 / (1 + p x), x = |z| / sqrt 2,
+// error at most 1.5e-7 (2^-22.7) anywhere, from the lower tail's side, so that it
+// does not cancel; the derivative shares its exponential.  The device library's
+// erfc takes several times the instructions: the gradient of a 2048 x 14336
+// gelu layer took 54-59 us with it, 1.4 times the time of its bytes.
+__device__ __forceinline__ float normal_cdf(float z, float e) {
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f * 0.7071067811865476f, fabsf(z), 1.0f));
+  float q = __builtin_fmaf(1.061405429f, t, -1.453152027f);
+  q = __builtin_fmaf(q, t, 1.421413741f);
+  q = __builtin_fmaf(q, t, -0.284496736f);
+  q = __builtin_fmaf(q, t, 0.254829592f);
+  const float half_erfc = 0.5f * q * t * e;
+  return z > 0.f ? 1.0f - half_erfc : half_erfc;
+}
+
 // 2u of gelu_tanh: 2 sqrt(2 / pi) (z + 0.044715 z^3)
 __device__ __forceinline__ float gelu_tanh_2u(float z) {
   return 1.5957691216057308f * __builtin_fmaf(0.044715f * z * z, z, z);
@@ -54,7 +69,7 @@ __device__ __forceinline__ float act_value(float z, int act) {
   switch (act) {
     case kActRelu: return z > 0.f || z != z ? z : 0.f;  // NaN stays NaN
     case kActSilu: return z * sigmoid(z);
-    case kActGelu: return 0.5f * z * erfcf(z * -0.7071067811865476f);
+    case kActGelu: return z * normal_cdf(z, __expf(-0.5f * z * z));
     case kActGeluTanh: return z * sigmoid(gelu_tanh_2u(z));
     default: return z;
   }
@@ -67,9 +82,10 @@ __device__ __forceinline__ float act_grad(float z, int act) {
       const float sg = sigmoid(z);
       return sg * __builtin_fmaf(z, 1.f - sg, 1.f);
     }
-    case kActGelu:
-      return __builtin_fmaf(z * 0.3989422804014327f, __expf(-0.5f * z * z),
-                            0.5f * erfcf(z * -0.7071067811865476f));
+    case kActGelu: {
+      const float e = __expf(-0.5f * z * z);
+      return __builtin_fmaf(z * 0.3989422804014327f, e, normal_cdf(z, e));
+    }
     case kActGeluTanh: {
       // past |z| = 16 the derivative is 0 or 1 in fp32; z is held there so that
       // the vanishing factor never meets an overflowed one (NaN stays NaN)
