@@ -666,11 +666,11 @@ def test_same_bits_every_time(M):
 
 
 def test_plain_epilogue_gives_the_plain_products_bits():
-    """No bias, activation or residual: w4a16_linear is w4a16_gemm, bit for bit, where both
-    take the same path and split."""
+    """No bias, activation or residual on the streaming path (M <= 16), where both calls
+    split K alike: w4a16_linear is w4a16_gemm, bit for bit."""
     torch = torch_cuda()
     for dtype in ("fp16", "bf16"):
-        for M in (1, 16, 64, 200):
+        for M in (1, 5, 16):
             w = weight(1, 272, 640, True)
             X, _ = act_array(dtype, 1, M, 640)
             note(f"plain epilogue {dtype} M={M}")

@@ -1435,6 +1435,78 @@ int dma_plan(const GemmDesc *d, int count, int tm, bool unsplit, int *split) {
   return best_ks;
 }
 
+// A block shape of tiled_dma_kernel and its time per step (ks groups), in us,
+// with 1, 2, 3 and 4 workgroups on a CU (0: that many do not fit), measured
+// with bf16 activations and INT4 codes.
+struct FusedShape {
+  int tm, ks;
+  double us[4];
+};
+constexpr FusedShape kFusedShapes[] = {
+    {8, 1, {2.9, 3.5, 0, 0}},     {6, 1, {2.5, 3.0, 0, 0}},   {4, 1, {1.3, 1.5, 2.0, 2.57}},
+    {4, 2, {1.6, 2.65, 0, 0}},    {3, 1, {1.15, 1.35, 1.75, 2.25}}, {3, 2, {1.45, 2.4, 0, 0}},
+    {2, 1, {1.0, 1.2, 1.5, 1.85}}, {2, 2, {1.25, 2.1, 0, 0}},
+};
+
+// The plan of a fused launch: block shape (*tm, the returned K slices) and
+// splits of each problem, the least modelled time of every shape and range
+// length.  Unlike launch_model, which plans the plain products (and whose
+// choices fix their bits), it knows that a workgroup alone on a CU runs faster
+// than one of two or four, so that small blocks without partials are taken
+// where large ones would have to be split.  Measured against launch_model's
+// plans, in us: linear M = 1531, 4096 x 4096 bf16: 77.1 -> 70.0 (64 x 128 blocks,
+// unsplit); M = 512: 37.7 -> 31.1; gated M = 64, 18944 x 3584 bf16: 43.7 -> 39.3;
+// M = 200, 14336 x 4096 fp16: 75.9 -> 66.8.
+int fused_plan(const GemmDesc *d, int count, bool unsplit, int *tm, int *split) {
+  // distinct range lengths, as in choose_splits, down to kMinFusedGroups groups
+  constexpr int kMinFusedGroups = 4;
+  int cand[kMaxTiled * kMaxSplit];
+  int nc = 0;
+  for (int i = 0; i < count; ++i) {
+    const int G = d[i].K / kGroup;
+    for (int n = 1; n <= (unsplit ? 1 : kMaxSplit) && n <= G; ++n) cand[nc++] = (G + n - 1) / n;
+  }
+  std::sort(cand, cand + nc, [](int a, int b) { return a > b; });
+  nc = (int)(std::unique(cand, cand + nc) - cand);
+  const double type = d[0].bf16 ? 1.0 : 0.8;  // fp16 weights dequantize in fewer instructions
+  double best = 0.0;
+  int best_ks = 0;
+  for (const FusedShape &f : kFusedShapes) {
+    const DmaShape ds = dma_shape(f.tm);
+    const int per_cu = f.us[3] > 0 ? 4 : 2;
+    for (int ci = 0; ci < nc; ++ci) {
+      int s[kMaxTiled], longest = 0;
+      long long wgs = 0;
+      double parts = 0.0, outs = 0.0;  // values written as partials, and from them
+      for (int i = 0; i < count; ++i) {
+        const int G = d[i].K / kGroup;
+        const int cap = std::min(std::min(kMaxSplit, G), (G + kMinFusedGroups - 1) / kMinFusedGroups);
+        s[i] = unsplit ? 1 : std::max(1, std::min(cap, (G + cand[ci] - 1) / cand[ci]));
+        wgs += (long long)tiles_of(d[i], ds.bm(), ds.bn()) * s[i];
+        longest = std::max(longest, ((G + s[i] - 1) / s[i] + f.ks - 1) / f.ks);
+        if (s[i] > 1) {
+          const double mn = (double)d[i].M * d[i].mats() * d[i].N;
+          parts += s[i] * mn;
+          outs += mn;
+        }
+      }
+      const long long slots = 256 * per_cu, rest = wgs % slots;
+      const double rounds = (double)(wgs / slots) * f.us[per_cu - 1] +
+                            (rest == 0 ? 0.0 : f.us[(rest + 255) / 256 - 1]);
+      // partials: written, read back, a second launch
+      const double us = type * rounds * (longest + 0.7) +
+                        (parts > 0 ? 2.5 + (4 * parts + 2 * outs) / 4.0e6 + (4 * parts - 2 * outs) / 6.0e6 : 0.0);
+      if (best_ks == 0 || us < best) {
+        best = us;
+        best_ks = f.ks;
+        *tm = f.tm;
+        for (int i = 0; i < count; ++i) split[i] = s[i];
+      }
+    }
+  }
+  return best_ks;
+}
+
 // The tiled_dma_kernel instance of a DMA plan (dma_tm's TM, dma_plan's K
 // slices) for one activation type, code width and epilogue; any other shape is
 // an error, never a launch with a grid planned for another tile.
@@ -1494,10 +1566,12 @@ void launch_regs(int epi, dim3 grid, hipStream_t stream, const TiledSet &ts, con
 
 size_t tiled_workspace_bytes(const GemmDesc *d, int count) {
   if (count < 1 || count > kMaxTiled) return 0;
-  const int tm = dma_tm(d, count);
+  int tm = dma_tm(d, count);
   const bool dma = tm != 0;
   int split[kMaxTiled];
-  if (dma)
+  if (dma && d[0].fused)
+    fused_plan(d, count, false, &tm, split);
+  else if (dma)
     dma_plan(d, count, tm, false, split);
   else
     choose_splits(d, count, split, 16 * regs_tm(d, count));
@@ -1516,22 +1590,27 @@ hipError_t launch_tiled_set(const GemmDesc *d, int count, void *workspace, size_
   // room for the split partials as well, K is not split.
   const size_t have = workspace ? workspace_bytes : 0;
   const size_t pre = prescale_need(d, count);
-  const int tm = dma_tm(d, count);
+  int tm = dma_tm(d, count);
   const bool dma = tm != 0 && pre <= have;
-  const DmaShape ds = dma_shape(tm);
-  const int bm = dma ? ds.bm() : 16 * regs_tm(d, count), bn = dma ? ds.bn() : kBN;
   int split[kMaxTiled];
   int ks = 1;
-  if (dma)
+  if (dma && d[0].fused)
+    ks = fused_plan(d, count, false, &tm, split);
+  else if (dma)
     ks = dma_plan(d, count, tm, false, split);
   else
-    choose_splits(d, count, split, bm);
+    choose_splits(d, count, split, 16 * regs_tm(d, count));
   size_t parts = 0;
   for (int i = 0; i < count; ++i) parts += part_bytes(d[i], split[i]);
   if ((dma ? pre : 0) + parts > have) {  // no room for partials: one K range
     for (int i = 0; i < count; ++i) split[i] = 1;
-    if (dma) ks = dma_plan(d, count, tm, true, split);
+    if (dma && d[0].fused)
+      ks = fused_plan(d, count, true, &tm, split);
+    else if (dma)
+      ks = dma_plan(d, count, tm, true, split);
   }
+  const DmaShape ds = dma_shape(tm);
+  const int bm = dma ? ds.bm() : 16 * regs_tm(d, count), bn = dma ? ds.bn() : kBN;
   TiledSet ts = {};
   TiledFused fs = {};
   int blocks = 0, rblocks = 0;
