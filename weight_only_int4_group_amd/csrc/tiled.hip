@@ -70,20 +70,24 @@ __device__ __forceinline__ half8 dequant_word(uint32_t w, half2v bias_lo, half2v
   return r;
 }
 
-// bf16 activations: eight codes -> bf16((q_j - z) * scale), each rounded once.
-// and_or builds the exact bf16 128 + q (see the streaming kernel); as fp32 it
-// is one shift or mask away, and one FMA with the fp32 scale, minus
-// (128 + z) * scale, leaves (q - z) * scale before the bf16 rounding.
-__device__ __forceinline__ u32x4 dequant_word_bf16(uint32_t w, float scale, float zb) {
-  const uint32_t m = 0x000F000Fu;
+// bf16 activations: eight codes -> bf16((q_j - z) * scale), each rounded once:
+// (q - z) exact in fp16 as above, its product with the scale exact in fp32 (4 by
+// 11 bits: v_fma_mix_f32, which converts its fp16 operands itself), rounded to
+// bf16.  21 instructions; decoding to 128 + q and one fp32 FMA per weight took 27.
+__device__ __forceinline__ u32x4 dequant_word_bf16(uint32_t w, half2v bias_lo, half2v bias_hi,
+                                                   _Float16 scale) {
+  const half2v sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
+  const uint32_t m_lo = 0x000F000Fu, m_hi = 0x00F000F0u, magic = kMagic2;
+  const uint32_t w8 = w >> 8;
+  const half2v e[4] = {as_half2(and_or(w, m_lo, magic)) - bias_lo,
+                       as_half2(and_or(w, m_hi, magic)) * sixteenth - bias_hi,
+                       as_half2(and_or(w8, m_lo, magic)) - bias_lo,
+                       as_half2(and_or(w8, m_hi, magic)) * sixteenth - bias_hi};
   u32x4 r;
 #pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    const uint32_t x = and_or(w >> (4 * p), m, kMagicBF);
-    const float lo = __builtin_fmaf(__builtin_bit_cast(float, x << 16), scale, -zb);
-    const float hi = __builtin_fmaf(__builtin_bit_cast(float, x & 0xFFFF0000u), scale, -zb);
-    r[p] = pack_bf16x2(lo, hi);
-  }
+  for (int p = 0; p < 4; ++p)
+    r[p] = pack_bf16x2(__builtin_fmaf((float)e[p][0], (float)scale, 0.f),
+                       __builtin_fmaf((float)e[p][1], (float)scale, 0.f));
   return r;
 }
 
@@ -475,12 +479,14 @@ __device__ __forceinline__ void tiled_body(const TiledSet &ts, const FS &fs) {
         u32x4 bop[TN];
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
-          const float z = (float)__builtin_bit_cast(_Float16, (uint16_t)b.zp[j]);
-          const float sv = (float)__builtin_bit_cast(_Float16, (uint16_t)b.sc[j]);
+          const _Float16 z = __builtin_bit_cast(_Float16, (uint16_t)b.zp[j]);
+          const _Float16 sv = __builtin_bit_cast(_Float16, (uint16_t)b.sc[j]);
+          const _Float16 blo = (_Float16)1024.0f + z, bhi = (_Float16)64.0f + z;
+          const half2v bias_lo = {blo, blo}, bias_hi = {bhi, bhi};
           bop[j] = W8 ? dequant_words8_bf16(b.code[j][tt >> 1 & (kCW - 1)][2 * (tt & 1)],
-                                            b.code[j][tt >> 1 & (kCW - 1)][2 * (tt & 1) + 1], sv,
-                                            z * sv)
-                      : dequant_word_bf16(b.code[j][0][tt], sv, (128.0f + z) * sv);
+                                            b.code[j][tt >> 1 & (kCW - 1)][2 * (tt & 1) + 1],
+                                            (float)sv, (float)z * (float)sv)
+                      : dequant_word_bf16(b.code[j][0][tt], bias_lo, bias_hi, sv);
         }
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
@@ -932,7 +938,6 @@ __device__ __forceinline__ void tiled_dma_body(const TiledSet &ts, const FS &fs)
   // k step, then TM x TN MFMAs with A read from LDS buffer `buf`
   auto compute = [&](const BStage &b, int buf) {
     half2v bias_lo[TN], bias_hi[TN], scale[TN];
-    float fsc[TN], fzb[TN];  // bf16: the fp32 scale and (128 + z) * scale
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
       uint16_t zr, sr;
@@ -945,21 +950,16 @@ __device__ __forceinline__ void tiled_dma_body(const TiledSet &ts, const FS &fs)
       }
       const _Float16 z = __builtin_bit_cast(_Float16, zr);
       const _Float16 sv = __builtin_bit_cast(_Float16, sr);
-      if (BF) {
-        fsc[j] = (float)sv;
-        fzb[j] = (128.0f + (float)z) * fsc[j];
-      } else {
-        const _Float16 blo = (_Float16)1024.0f + z, bhi = (_Float16)64.0f + z;
-        const half2v bl = {blo, blo}, bh = {bhi, bhi}, sc = {sv, sv};
-        bias_lo[j] = bl;
-        bias_hi[j] = bh;
-        scale[j] = sc;
-      }
+      const _Float16 blo = (_Float16)1024.0f + z, bhi = (_Float16)64.0f + z;
+      const half2v bl = {blo, blo}, bh = {bhi, bhi}, sc = {sv, sv};
+      bias_lo[j] = bl;
+      bias_hi[j] = bh;
+      scale[j] = sc;
     }
     // a B operand: eight dequantized weights, fp16 or bf16 bits
     auto dequant = [&](int j, int t) -> u32x4 {
       if constexpr (BF)
-        return dequant_word_bf16(b.code[j][0][t], fsc[j], fzb[j]);
+        return dequant_word_bf16(b.code[j][0][t], bias_lo[j], bias_hi[j], scale[j][0]);
       else if constexpr (W8)  // k step t: the lane's code words 2t and 2t + 1
         return __builtin_bit_cast(u32x4, dequant_words8(b.code[j][t >> 1][2 * (t & 1)],
                                                         b.code[j][t >> 1][2 * (t & 1) + 1],
