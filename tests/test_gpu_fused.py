@@ -213,6 +213,16 @@ def test_linear_int8_codes(M, dtype):
 
 @pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("M,K", [(5, 14464), (16, 4224), (16, 12416)])
+def test_streamed_in_ranges_of_k(M, K, dtype, bits):
+    """Rows too long for LDS at this M: K in ranges of whole metadata quads (113, 33 and 97
+    groups: unequal ranges, a last quad in part), one weight and a gated pair."""
+    run_linear(M, 48, K, dtype, "silu", bias=True, residual=True, pre=True, awq=True, bits=bits)
+    run_gated(M, 48, K, dtype, "silu", bias=True, pre=True, awq=True, bits=bits)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("M", [1, 9, 40, 130])
 def test_linear_outliers(M, dtype, bits):
     run_linear(M, 272, 640, dtype, "none", bias=True, residual=True, pre=True, awq=True, bits=bits,
@@ -275,11 +285,11 @@ def test_gated_without_workspace(M):
     run_gated(M, 272, 4096, "bf16", "gelu_tanh", bias=True, pre=True, awq=True, workspace=False)
 
 
-@pytest.mark.parametrize("M", [1, 16, 40, 200])
-def test_linear_group_of_layers(M):
+@pytest.mark.parametrize("M,K", [(1, 640), (16, 640), (40, 640), (200, 640), (16, 4224)])
+def test_linear_group_of_layers(M, K):
     """q, k and v with biases, and a fourth layer with another epilogue, in one call."""
     torch = torch_cuda()
-    K, dtype = 640, "bf16"
+    dtype = "bf16"
     X, Xv = act_array(dtype, 1, M, K)
     items, refs = [], []
     for i, (N, act) in enumerate([(272, "none"), (48, "none"), (16, "relu"), (144, "silu")]):

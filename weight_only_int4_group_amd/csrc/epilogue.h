@@ -26,7 +26,10 @@ constexpr int kActs = 5;
 
 // One problem's epilogue.  bias [N], residual, pre [M][N] are of the activations'
 // type, each null when absent.  gated: the second weight (the "up" matrix, same
-// shape as the first), its bias, pre-activation output and outliers.
+// shape as the first), its bias, pre-activation output and outliers.  part, ldx:
+// set by the streaming launcher for one K range of a problem: the fp32 sums go to
+// part [M][N] (gated: [M][2 N], the two weights' 16-column blocks alternating)
+// instead of the epilogue, and X's rows are ldx apart (0: K).
 struct Fused {
   const void *bias, *residual;
   void *pre;
@@ -38,6 +41,8 @@ struct Fused {
   void *pre2;
   const int32_t *orp2, *ocol2;
   const _Float16 *oval2;
+  float *part;
+  int ldx;
 };
 
 __device__ __forceinline__ float sigmoid(float z) {

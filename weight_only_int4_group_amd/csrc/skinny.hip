@@ -269,20 +269,38 @@ __device__ __forceinline__ Fused find_fused(const ProblemSet &ps, const FusedSet
   F.gated = uniform_int(q.gated);
   F.bias2 = uniform_ptr(q.bias2);
   F.pre2 = uniform_ptr(q.pre2);
+  F.part = uniform_ptr(q.part);
   return F;
 }
 __device__ __forceinline__ NoFused find_fused(const ProblemSet &, const NoFused &) { return {}; }
 
+// Distance of X's rows.
+__device__ __forceinline__ int row_stride(const ProblemSet &, const NoFused &, int K) { return K; }
+__device__ __forceinline__ int row_stride(const ProblemSet &ps, const FusedSet &fs, int K) {
+  int ldx = fs.f[0].ldx;
+#pragma unroll
+  for (int i = 1; i < kMaxProblems; ++i)
+    if (i < ps.count && (int)blockIdx.x >= ps.p[i].block0) ldx = fs.f[i].ldx;
+  ldx = uniform_int(ldx);
+  return ldx ? ldx : K;
+}
+
 // Row block of slot v (the slots of a problem are given to the waves in order).
 // Plain and linear problems have one slot per row block.  A gated problem (the
-// only one of its call) has two, gate then up, so that the two waves (or groups
+// only one of its call, perhaps cut into K ranges) has two, gate then up, so that the two waves (or groups
 // of S waves) whose sums meet in act(G) * U are neighbours in one workgroup and
 // both read the X * s staged there; P becomes the slot's own matrix.
-__device__ __forceinline__ int slot_block(Problem &, const NoFused &, int v) { return v; }
-__device__ __forceinline__ int slot_block(Problem &P, const FusedSet &fs, int v) {
-  const Fused &q = fs.f[0];
-  if (!q.gated) return v;
+__device__ __forceinline__ int slot_block(Problem &, const ProblemSet &, const NoFused &, int v) {
+  return v;
+}
+__device__ __forceinline__ int slot_block(Problem &P, const ProblemSet &ps, const FusedSet &fs, int v) {
+  if (!fs.f[0].gated) return v;
   if (v & 1) {
+    int pi = 0;
+#pragma unroll
+    for (int i = 1; i < kMaxProblems; ++i)
+      if (i < ps.count && (int)blockIdx.x >= ps.p[i].block0) pi = i;
+    const Fused &q = fs.f[uniform_int(pi)];
     P.Wq = uniform_ptr(q.Wq2);
     P.scales = uniform_ptr(q.scales2);
     P.zeros = uniform_ptr(q.zeros2);
@@ -305,7 +323,7 @@ __device__ __forceinline__ NoFused prefetch_epilogue(const Problem &, const NoFu
 __device__ __forceinline__ EpiloguePrefetch prefetch_epilogue(const Problem &P, const Fused &F,
                                                               int slot, int b, int ks, int c, int r) {
   EpiloguePrefetch e = {};
-  if (ks != 0 || (F.gated && (slot & 1))) return e;  // another wave stores
+  if (F.part || ks != 0 || (F.gated && (slot & 1))) return e;  // another wave (or kernel) stores
   const int n = b * kTileRows + r;
   if (F.bias) e.bias = static_cast<const uint16_t *>(F.bias)[n];
   if (F.bias2) e.bias2 = static_cast<const uint16_t *>(F.bias2)[n];
@@ -490,7 +508,7 @@ __device__ __forceinline__ void store_slot(const Problem &P, const Fused &F,
                                            float (*red)[16][17], int2 orange,
                                            const OutPrefetch &of) {
   const int M = P.M, N = P.N, S = P.split;
-  const bool stores = ks == 0 && has_rows && !(F.gated && (slot & 1));
+  const bool stores = ks == 0 && has_rows && (F.part || !(F.gated && (slot & 1)));
   if (kOut && ks == 0 && has_rows) acc += outlier_terms<kBF>(P, of, orange, 16 * c + r, c);
   if (S > 1 || F.gated) {
 #pragma unroll
@@ -498,6 +516,19 @@ __device__ __forceinline__ void store_slot(const Problem &P, const Fused &F,
     __syncthreads();
   }
   if (!stores) return;
+  if (F.part) {  // one K range's sums
+    const size_t np = F.gated ? 2 * (size_t)N : (size_t)N;
+    const int col = (F.gated ? 2 * b + (slot & 1) : b) * kTileRows + r;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int m = 4 * c + v;
+      if (m >= M) continue;
+      float z = acc[v];
+      for (int w = 1; w < S; ++w) z += red[wave + w][m][r];
+      F.part[m * np + col] = z;
+    }
+    return;
+  }
   const float bias = F.bias ? act_to_f32<kBF>(e.bias) : 0.f;
   const float bias2 = F.bias2 ? act_to_f32<kBF>(e.bias2) : 0.f;
 #pragma unroll
@@ -542,7 +573,7 @@ __device__ __forceinline__ void skinny_body(const ProblemSet &ps, const FS &fs, 
   const int c = lane >> 4;   // column octet (A/B operands), row quad (D)
   const int r = lane & 15;   // X row m (A), W row in the tile (B), column n (D)
   const int slot = ((int)blockIdx.x - P.block0) * (kWaves / S) + wave / S;
-  const int b = slot_block(P, fs, slot);  // row block
+  const int b = slot_block(P, ps, fs, slot);  // row block
   const int ks = wave % S;               // K slice
   const bool has_rows = b < NB;
   const int bb = has_rows ? b : NB - 1;
@@ -649,11 +680,11 @@ __device__ __forceinline__ void skinny_body(const ProblemSet &ps, const FS &fs, 
   // a 16-lane segment stages exactly one group of one row)
   float *gsum = reinterpret_cast<float *>(xs + M * (K + kLdsPad));
   {
-    const int ldx = K + kLdsPad, k8 = K / 8;
+    const int ldx = K + kLdsPad, k8 = K / 8, xstride = row_stride(ps, fs, K);
     for (int idx = threadIdx.x; idx < M * k8; idx += kWaves * 64) {
       const int m = idx / k8, kk = (idx - m * k8) * 8;
       float part = 0.f;
-      const u32x4 v = scale_x8<kBF>(*reinterpret_cast<const u32x4 *>(P.X + (size_t)m * K + kk),
+      const u32x4 v = scale_x8<kBF>(*reinterpret_cast<const u32x4 *>(P.X + (size_t)m * xstride + kk),
                                     P.s ? P.s + kk : nullptr, part);
       *reinterpret_cast<u32x4 *>(&xs[m * ldx + kk]) = v;
       if (kBF) {
@@ -789,7 +820,7 @@ __device__ __forceinline__ void skinny_window_body(const ProblemSet &ps, const F
   const int lane = threadIdx.x & 63, wave = uniform_int(threadIdx.x >> 6);
   const int c = lane >> 4, r = lane & 15;
   const int slot = ((int)blockIdx.x - P.block0) * (kWaves / S) + wave / S;
-  const int b = slot_block(P, fs, slot);
+  const int b = slot_block(P, ps, fs, slot);
   const int ks = wave % S;
   const bool has_rows = b < NB;
   const int bb = has_rows ? b : NB - 1;
@@ -1338,7 +1369,124 @@ hipError_t launch_prescale(const GemmDesc *const *d, int count, hipStream_t stre
 
 }  // namespace
 
+namespace {
+
+// K ranges (workgroups apart, fp32 partials in the workspace) of a fused
+// problem on the streaming path; 1: not split.  Split where X * s of whole rows
+// does not fit in LDS and the launch has few row blocks: the workgroups would
+// be one or two row blocks by all of K and each stage all of X * s, in windows
+// whose latencies add up; cut into ranges they are 4 to 8 row blocks by an eighth
+// (short rows: a quarter) of K, which fits.  Measured in us, windows or wide
+// workgroups against ranges and the second launch that adds them: 4096 x
+// 14336, M = 5: 16.7 -> 13.7 (bf16 19.2 -> 14.0), M = 16: 21.3 -> 16.4 (29.5 ->
+// 18.1); 1024 x 8192 bf16, M = 9: 19.3 -> 10.8; 4096 x 4096, M = 16: 10.9 -> 9.8.  With 896
+// row blocks (14336 x 4096, M = 16) 13.7 -> 14.9, and where the rows fit (M = 1) 9.9
+// -> 12.8: not split.
+constexpr int kPartsMaxBlocks = 512;
+int k_parts(const GemmDesc &q, int count, int row_blocks) {
+  if (q.o_row_ptr || (q.fused && q.fused->orp2)) return 1;  // outliers go by rows
+  if (row_blocks > kPartsMaxBlocks || stage_bytes(q.M, q.K, q.bf16) <= kMaxStageBytes) return 1;
+  int parts = q.K > 4096 ? 8 : 4;
+  while (parts > 1 && parts * count > kMaxProblems) parts /= 2;
+  return parts;
+}
+
+size_t parts_bytes(const GemmDesc &q, int parts) {
+  return parts > 1 ? align256((size_t)parts * q.M * q.mats() * q.N * sizeof(float)) : 0;
+}
+
+// The K ranges of the problems d[0..count) of a fused launch: all of them must
+// fit one launch and stage whole rows, else none is split.
+size_t plan_parts(const GemmDesc *const *d, int count, int *parts) {
+  int total = 0, row_blocks = 0;
+  size_t bytes = 0;
+  bool ok = true, any = false;
+  for (int i = 0; i < count; ++i) row_blocks += d[i]->row_blocks();
+  for (int i = 0; i < count; ++i) {
+    parts[i] = d[i]->fused ? k_parts(*d[i], count, row_blocks) : 1;
+    any |= parts[i] > 1;
+    total += parts[i];
+    bytes += parts_bytes(*d[i], parts[i]);
+    const int G = d[i]->K / kGroup, quads = (G + kMetaQuad - 1) / kMetaQuad;
+    const int longest = (quads + parts[i] - 1) / parts[i] * kMetaQuad * kGroup;
+    ok &= stage_bytes(d[i]->M, longest < d[i]->K ? longest : d[i]->K, d[i]->bf16) <= kMaxStageBytes;
+  }
+  if (any && ok && total <= kMaxProblems) return bytes;
+  for (int i = 0; i < count; ++i) parts[i] = 1;
+  return 0;
+}
+
+// One launch over all K ranges, then one that adds them and applies the
+// epilogues.  Ranges are whole metadata quads, so a range's codes, scales and
+// zero points are contiguous parts of the problem's.
+hipError_t launch_parts(const GemmDesc *const *d, int count, const int *parts, void *workspace,
+                        hipStream_t stream) {
+  GemmDesc sub[kMaxProblems];
+  Fused fused[kMaxProblems];
+  const GemmDesc *ptr[kMaxProblems];
+  float *slabs[kMaxProblems];
+  int n = 0;
+  char *ws = static_cast<char *>(workspace);
+  for (int i = 0; i < count; ++i) {
+    const GemmDesc &q = *d[i];
+    const int G = q.K / kGroup, quads = (G + kMetaQuad - 1) / kMetaQuad, NB = q.N / kTileRows;
+    slabs[i] = reinterpret_cast<float *>(ws);
+    ws += parts_bytes(q, parts[i]);
+    for (int p = 0; p < parts[i]; ++p) {
+      const int g0 = (int)((long long)quads * p / parts[i]) * kMetaQuad;
+      const int g1 = p + 1 == parts[i] ? G : (int)((long long)quads * (p + 1) / parts[i]) * kMetaQuad;
+      const size_t codes = (size_t)g0 * NB * kTileBytes * (q.w8 ? 2 : 1), meta = (size_t)g0 * q.N;
+      sub[n] = q;
+      fused[n] = *q.fused;
+      if (parts[i] > 1) {
+        sub[n].X = static_cast<const _Float16 *>(q.X) + (size_t)g0 * kGroup;
+        sub[n].s = q.s ? static_cast<const _Float16 *>(q.s) + (size_t)g0 * kGroup : nullptr;
+        sub[n].Wq = static_cast<const uint8_t *>(q.Wq) + codes;
+        sub[n].scales = static_cast<const _Float16 *>(q.scales) + meta;
+        sub[n].zeros = static_cast<const _Float16 *>(q.zeros) + meta;
+        sub[n].K = (g1 - g0) * kGroup;
+        if (q.gated()) {
+          fused[n].Wq2 += codes;
+          fused[n].scales2 += meta;
+          fused[n].zeros2 += meta;
+        }
+        fused[n].part = slabs[i] + (size_t)p * q.M * q.mats() * q.N;
+        fused[n].ldx = q.K;
+      }
+      sub[n].fused = fused + n;
+      ptr[n] = sub + n;
+      ++n;
+    }
+  }
+  const hipError_t e = launch_group(ptr, n, kWhole, stream);
+  return e != hipSuccess ? e : launch_fused_reduce(d, count, parts, slabs, stream);
+}
+
+}  // namespace
+
+// Classes of a launch (one kernel instance each): fp16 INT4, bf16 INT4, fp16
+// INT8, bf16 INT8.
+static int class_of(const GemmDesc &q) { return (q.w8 ? 2 : 0) + (q.bf16 ? 1 : 0); }
+
+// The classes run one after the other and share the workspace.
 size_t skinny_workspace_bytes(const GemmDesc *d, int count) {
+  if (count > 0 && d[0].fused) {
+    size_t need = 0;
+    for (int cls = 0; cls < 4; ++cls) {
+      const GemmDesc *members[kMaxProblems];
+      int nm = 0, parts[kMaxProblems];
+      size_t pre = 0;
+      for (int i = 0; i < count; ++i)
+        if (class_of(d[i]) == cls) {
+          members[nm++] = d + i;
+          if (d[i].bf16) pre += prescale_bytes(d[i].M, d[i].K);
+        }
+      const size_t b = plan_parts(members, nm, parts);
+      const size_t n = b ? b : pre;
+      need = n > need ? n : need;
+    }
+    return need;
+  }
   size_t n = 0;
   for (int i = 0; i < count; ++i)
     if (d[i].bf16) n += prescale_bytes(d[i].M, d[i].K);
@@ -1357,8 +1505,8 @@ hipError_t launch_skinny_set(const GemmDesc *d, int count, hipStream_t stream, b
   hipError_t err = hipSuccess;
   for (int cls = 0; cls < 4 && err == hipSuccess; ++cls) {
     // classes: fp16 INT4, bf16 INT4, fp16 INT8, bf16 INT8
-    const bool want_bf = (cls & 1) != 0, want_w8 = cls >= 2;
-    auto in_class = [&](const GemmDesc &q) { return q.bf16 == want_bf && q.w8 == want_w8; };
+    const bool want_bf = (cls & 1) != 0;
+    auto in_class = [&](const GemmDesc &q) { return class_of(q) == cls; };
     const GemmDesc *whole[kMaxProblems], *windowed[kMaxProblems];
     int nwhole = 0, nwin = 0;
     bool any = false, all = true, outl = false, wide = true;
@@ -1373,6 +1521,16 @@ hipError_t launch_skinny_set(const GemmDesc *d, int count, hipStream_t stream, b
         outl |= d[i].o_row_ptr != nullptr || (d[i].fused && d[i].fused->orp2);
         members[nm++] = d + i;
       }
+    if (nm == 0) continue;
+    // fused: K ranges apart where that is faster and the workspace has room
+    if (d[0].fused && workspace && !force_window) {
+      int parts[kMaxProblems];
+      const size_t need = plan_parts(members, nm, parts);
+      if (need > 0 && need <= workspace_bytes) {
+        err = launch_parts(members, nm, parts, workspace, stream);
+        continue;
+      }
+    }
     // fp16 INT4 without outliers, all X * s within kWideStageBytes: whole rows
     // in 16-wave workgroups
     if (cls == 0 && any && wide && !outl && !force_window) {

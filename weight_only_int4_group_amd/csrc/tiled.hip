@@ -1718,6 +1718,32 @@ hipError_t launch_tiled_set(const GemmDesc *d, int count, void *workspace, size_
   return err;
 }
 
+hipError_t launch_fused_reduce(const GemmDesc *const *d, int count, const int *split,
+                               float *const *parts, hipStream_t stream) {
+  if (count < 1 || count > kMaxTiled) return hipErrorInvalidValue;
+  TiledSet ts = {};
+  TiledFused fs = {};
+  int rblocks = 0;
+  for (int i = 0; i < count; ++i) {
+    TiledProblem &p = ts.p[i];
+    p.Y = static_cast<_Float16 *>(d[i]->Y);
+    p.part = parts[i];
+    p.M = d[i]->M;
+    p.N = d[i]->N;
+    p.split = split[i];
+    p.rblock0 = rblocks;
+    if (split[i] > 1) rblocks += (int)(((long long)p.M * p.N / 4 + kReduceThreads - 1) / kReduceThreads);
+    fs.f[i] = *d[i]->fused;
+  }
+  ts.count = count;
+  if (rblocks == 0) return hipSuccess;
+  if (d[0]->bf16)
+    hipLaunchKernelGGL(split_reduce_fused_kernel<true>, dim3(rblocks), dim3(kReduceThreads), 0, stream, ts, fs);
+  else
+    hipLaunchKernelGGL(split_reduce_fused_kernel<false>, dim3(rblocks), dim3(kReduceThreads), 0, stream, ts, fs);
+  return hipGetLastError();
+}
+
 hipError_t launch_tiled(const void *X, const void *Wq, const void *scales, const void *zeros,
                         const void *s, void *Y, int M, int N, int K, hipStream_t stream) {
   const GemmDesc d = {X, Wq, scales, zeros, s, Y, M, N, K};

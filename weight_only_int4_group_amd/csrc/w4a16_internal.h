@@ -88,6 +88,10 @@ int tiled_max_problems();
 size_t tiled_workspace_bytes(const GemmDesc *problems, int count);
 hipError_t launch_tiled_set(const GemmDesc *problems, int count, void *workspace,
                             size_t workspace_bytes, hipStream_t stream);
+// Adds the split fp32 partials of the fused problems with split > 1 ([M][N] slabs,
+// gated [M][2 N]) and applies their epilogues; one activation type per call.
+hipError_t launch_fused_reduce(const GemmDesc *const *d, int count, const int *split,
+                               float *const *parts, hipStream_t stream);
 hipError_t launch_tiled(const void *X, const void *Wq, const void *scales, const void *zeros,
                         const void *s, void *Y, int M, int N, int K, hipStream_t stream);
 
