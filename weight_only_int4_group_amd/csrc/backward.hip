@@ -315,7 +315,16 @@ __global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(TN == 
     // the wave's quantization group among the block's
     const int ul = (wave * TN * kTileRows) / kGroup;
 
-    auto compute = [&](const BStage &b, int buf) {
+    // A operands of one k step; small tiles have registers to read them a k step
+    // ahead, the first before the next stage's loads are issued
+    constexpr bool kAhead = TN == 2;
+    auto read_a = [&](int tt, int buf, u32x4 (&a)[TM]) {
+      const int pc = (4 * tt + c) ^ r;
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+        a[i] = *reinterpret_cast<const u32x4 *>(&As[ks][buf][(16 * i + r) * kGroup + 8 * pc]);
+    };
+    auto compute = [&](const BStage &b, int buf, u32x4 (&a)[TM]) {
       const _Float16 *ms = reinterpret_cast<const _Float16 *>(&Ms[ks][buf][ul * kMetaBytes]) + 8 * c;
       struct Meta {
         half8 scale, bias;
@@ -355,7 +364,6 @@ __global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(TN == 
         }
         return out;
       };
-      const _Float16 *abuf = As[ks][buf];
       // software pipeline: k step tt + 1's B operands are dequantized while k
       // step tt's MFMAs run
       u32x4 bop[TN];
@@ -370,10 +378,13 @@ __global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(TN == 
 #pragma unroll
           for (int j = 0; j < TN; ++j) bnx[j] = dequant(j, tt + 1, m);
         }
+        u32x4 anx[TM];
+        if (kAhead && tt < 3) read_a(tt + 1, buf, anx);
         const int pc = (4 * tt + c) ^ r;
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
-          const u32x4 aop = *reinterpret_cast<const u32x4 *>(abuf + (16 * i + r) * kGroup + 8 * pc);
+          const u32x4 aop = kAhead ? a[i] : *reinterpret_cast<const u32x4 *>(
+                                                &As[ks][buf][(16 * i + r) * kGroup + 8 * pc]);
 #pragma unroll
           for (int j = 0; j < TN; ++j)
             acc[i][j] = BF ? mfma16_bf16(aop, bop[j], acc[i][j])
@@ -381,6 +392,10 @@ __global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(TN == 
                                     acc[i][j]);
         }
         if (tt < 3) {
+          if (kAhead) {
+#pragma unroll
+            for (int i = 0; i < TM; ++i) a[i] = anx[i];
+          }
 #pragma unroll
           for (int j = 0; j < TN; ++j) bop[j] = bnx[j];
         }
@@ -402,8 +417,10 @@ __global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(TN == 
     };
     auto step = [&](int i, BStage &cur, BStage &nxt, int buf) {
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      u32x4 a[TM];
+      if (kAhead) read_a(0, buf, a);
       load_stage(i + 1, nxt, buf ^ 1);
-      compute(cur, buf);
+      compute(cur, buf, a);
     };
     // the term before may still be read, and its last loads still land, in LDS
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -547,8 +564,8 @@ struct DxShape {
 constexpr int kDxMaxSplit = 32;
 
 // Blocks of 128 x 256 (96 x 256 for INT8 codes, whose registers do not allow
-// 128) for large products; 64 x 128, 32 x 128 or 16 x 128, as few rows as cover
-// a small M, with two slices per workgroup, where those would leave CUs idle.  The
+// 128) for large products; 64 x 128 or 48 x 128 (32 x 128 and 16 x 128 where
+// those cover M), with two slices per workgroup, where those would leave CUs idle.  The
 // stages are split across workgroups (fp32 partials) and the shape is chosen by
 // a model of the launch: rounds of at most two workgroups per CU, each as long
 // as its steps, plus the partials' traffic and the second launch.  Measured, in
@@ -557,13 +574,15 @@ constexpr int kDxMaxSplit = 32;
 // 16.7 (one slice: 17.4); M = 64, N = 2 x 14336, K = 4096: 42.6 and 29.2 (34.4).
 DxPlan plan_dx(const DxDesc &d) {
   static const DxShape large = {8, 4, 1, 2.9, 3.5}, large8 = {6, 4, 1, 2.5, 3.1};
-  static const DxShape s64 = {4, 2, 2, 1.55, 2.65}, s32 = {2, 2, 2, 1.3, 2.4}, s16 = {1, 2, 2, 1.2, 2.2};
+  static const DxShape s64 = {4, 2, 2, 1.55, 2.65}, s48 = {3, 2, 2, 1.45, 2.4};
+  static const DxShape s32 = {2, 2, 2, 1.3, 2.4}, s16 = {1, 2, 2, 1.2, 2.2};
   DxPlan best = {};
   double best_us = 0.0;
   int stages = 0;
   for (int i = 0; i < d.count; ++i) stages += (d.N[i] + kGroup - 1) / kGroup;
   const DxShape *const small = d.M > 32 ? &s64 : d.M > 16 ? &s32 : &s16;
-  const DxShape *const shapes[2] = {small, d.M > 64 ? (d.w8 ? &large8 : &large) : nullptr};
+  const DxShape *const shapes[3] = {small, d.M > 32 ? &s48 : nullptr,
+                                    d.M > 64 ? (d.w8 ? &large8 : &large) : nullptr};
   for (const DxShape *s : shapes) {
     if (!s) continue;
     const long long tiles =
@@ -591,6 +610,7 @@ void launch_dx_tile(const DxPlan &p, dim3 grid, hipStream_t stream, const DxArgs
   hipLaunchKernelGGL((dx_kernel<TM, TN, KS, BF, W8>), grid, dim3(256 * KS), 0, stream, a)
   W4_DX((W8 ? 6 : 8), 4, 1);
   W4_DX(4, 2, 2);
+  W4_DX(3, 2, 2);
   W4_DX(2, 2, 2);
   W4_DX(1, 2, 2);
 #undef W4_DX

@@ -934,9 +934,20 @@ __device__ __forceinline__ void tiled_dma_body(const TiledSet &ts, const FS &fs)
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = float4v{0.f, 0.f, 0.f, 0.f};
 
+  // A operands of one k step, from LDS buffer `buf`
+  auto read_a = [&](int tt, int buf, u32x4 (&a)[TM]) {
+    const int pc = (4 * tt + c) ^ r;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+      a[i] = *reinterpret_cast<const u32x4 *>(&As[ks][buf][(16 * i + r) * kGroup + 8 * pc]);
+  };
+  // Small tiles have registers to read a whole k step's A operands one k step
+  // ahead, the first before the next group's loads are issued (1 to 4% faster:
+  // gated M = 64, 18944 x 3584 bf16 35.5 -> 34.2 us).
+  constexpr bool kAhead = TN == 2;
   // the four k steps of a group: this wave's B operands dequantized once per
   // k step, then TM x TN MFMAs with A read from LDS buffer `buf`
-  auto compute = [&](const BStage &b, int buf) {
+  auto compute = [&](const BStage &b, int buf, u32x4 (&a)[TM]) {
     half2v bias_lo[TN], bias_hi[TN], scale[TN];
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
@@ -967,7 +978,6 @@ __device__ __forceinline__ void tiled_dma_body(const TiledSet &ts, const FS &fs)
       else
         return __builtin_bit_cast(u32x4, dequant_word(b.code[j][0][t], bias_lo[j], bias_hi[j], scale[j]));
     };
-    const _Float16 *abuf = As[ks][buf];
     // software pipeline: k step tt + 1's B operands are dequantized while k
     // step tt's MFMAs run.  fp16 at TN = 4: interleaved by the scheduler (one LDS
     // read, TN MFMAs and about seven VALU ops at a time; 1% faster than the
@@ -984,10 +994,13 @@ __device__ __forceinline__ void tiled_dma_body(const TiledSet &ts, const FS &fs)
 #pragma unroll
         for (int j = 0; j < TN; ++j) bnx[j] = dequant(j, tt + 1);
       }
+      u32x4 anx[TM];
+      if (kAhead && tt < 3) read_a(tt + 1, buf, anx);
       const int pc = (4 * tt + c) ^ r;
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
-        const u32x4 aop = *reinterpret_cast<const u32x4 *>(abuf + (16 * i + r) * kGroup + 8 * pc);
+        const u32x4 aop = kAhead ? a[i] : *reinterpret_cast<const u32x4 *>(
+                                              &As[ks][buf][(16 * i + r) * kGroup + 8 * pc]);
 #pragma unroll
         for (int j = 0; j < TN; ++j)
           acc[i][j] = BF ? mfma16_bf16(aop, bop[j], acc[i][j])
@@ -1003,6 +1016,10 @@ __device__ __forceinline__ void tiled_dma_body(const TiledSet &ts, const FS &fs)
         }
       }
       if (tt < 3) {
+        if (kAhead) {
+#pragma unroll
+          for (int i = 0; i < TM; ++i) a[i] = anx[i];
+        }
 #pragma unroll
         for (int j = 0; j < TN; ++j) bop[j] = bnx[j];
       }
@@ -1020,9 +1037,11 @@ __device__ __forceinline__ void tiled_dma_body(const TiledSet &ts, const FS &fs)
     auto step = [&](int g, BStage &cur, BStage &nxt, int buf) {
       asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
       const int gn = min(g + 1, ge - 1);
+      u32x4 a[TM];
+      if (kAhead) read_a(0, buf, a);
       load_x(gn, buf ^ 1);
       load_b(gn, nxt);
-      compute(cur, buf);
+      compute(cur, buf, a);
     };
     load_x(gb, 0);
     load_b(gb, b0);
@@ -1034,9 +1053,11 @@ __device__ __forceinline__ void tiled_dma_body(const TiledSet &ts, const FS &fs)
     auto step = [&](int i, BStage &cur, BStage &nxt, int buf) {
       asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
       const int gn = group_at(min(i + 1, nsteps - 1));
+      u32x4 a[TM];
+      if (kAhead) read_a(0, buf, a);
       load_x(gn, buf ^ 1);
       load_b(gn, nxt);
-      if (gb + ks + i * KS < ge) compute(cur, buf);
+      if (gb + ks + i * KS < ge) compute(cur, buf, a);
     };
     load_x(group_at(0), 0);
     load_b(group_at(0), b0);
