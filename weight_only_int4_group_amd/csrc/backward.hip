@@ -511,9 +511,7 @@ __global__ __launch_bounds__(256) void dx_reduce_kernel(DxArgs P) {
   const long long quads = (long long)P.M * P.K / 4;
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
   if (i >= quads) return;
-  const float4v *src = reinterpret_cast<const float4v *>(P.part) + i;
-  float4v x = src[0];
-  for (int k = 1; k < P.split; ++k) x += src[(size_t)k * quads];
+  float4v x = sum_partials(reinterpret_cast<const float4v *>(P.part) + i, quads, P.split);
   typedef _Float16 half4 __attribute__((ext_vector_type(4)));
   if (P.s) {
     const half4 s = *reinterpret_cast<const half4 *>(P.s + (i * 4) % P.K);

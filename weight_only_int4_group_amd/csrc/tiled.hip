@@ -1251,10 +1251,7 @@ __global__ __launch_bounds__(kReduceThreads) void split_reduce_fused_kernel(Tile
   const size_t np = gated ? 2 * (size_t)P.N : (size_t)P.N;
   const size_t src = (size_t)m * np + (gated ? 32 * (n / 16) + n % 16 : n), slab = (size_t)P.M * np;
   auto sum = [&](size_t at) {
-    float4v a = *reinterpret_cast<const float4v *>(P.part + at);
-    for (int k = 1; k < P.split; ++k)
-      a += *reinterpret_cast<const float4v *>(P.part + at + (size_t)k * slab);
-    return a;
+    return sum_partials(reinterpret_cast<const float4v *>(P.part + at), slab / 4, P.split);
   };
   auto quad = [&](const void *p, size_t at) {
     const u16x4 w = *reinterpret_cast<const u16x4 *>(static_cast<const uint16_t *>(p) + at);

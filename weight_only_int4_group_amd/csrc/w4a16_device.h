@@ -103,6 +103,30 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((float2x){lo, hi}, bf16x2));
 }
 
+// src[0] + src[stride] + ... (n partial sums), added in order, with up to eight
+// loads in flight: a launch that joins small outputs has few waves, and one load
+// after the other took most of its time (M = 5, N = 4096, 8 partials: 3.7 us,
+// now 2.7).
+template <int B>  // up to B more, from the k-th (past the last: re-read, not added)
+__device__ __forceinline__ void add_partials(float4v &a, const float4v *src, size_t stride, int k, int n) {
+  float4v x[B];
+#pragma unroll
+  for (int i = 0; i < B; ++i) x[i] = src[(size_t)min(k + i, n - 1) * stride];
+#pragma unroll
+  for (int i = 0; i < B; ++i)
+    if (k + i < n) a += x[i];
+}
+__device__ __forceinline__ float4v sum_partials(const float4v *src, size_t stride, int n) {
+  float4v a = src[0];
+  int k = 1;
+  for (; n - k > 4; k += 8) add_partials<8>(a, src, stride, k, n);
+  if (n - k > 2)
+    add_partials<4>(a, src, stride, k, n);
+  else if (n - k > 0)
+    add_partials<2>(a, src, stride, k, n);
+  return a;
+}
+
 // bf16 128.0 in both halves: OR-ing a 4-bit code q into the low mantissa bits
 // gives the exact bf16 value 128 + q
 constexpr uint32_t kMagicBF = 0x43004300u;
