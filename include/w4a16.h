@@ -86,7 +86,8 @@ enum {
   W4A16_EUNSUPPORTED = -3, /* unknown kernel path or quantization mode requested */
   W4A16_ENONFINITE = -4,   /* NaN/Inf in W or s, or some s <= 0 (packer)        */
   W4A16_ERANGE = -5,       /* a group scale rounds up past the fp16 range       */
-  W4A16_EHIP = -6,         /* a HIP runtime call or kernel launch failed        */
+  W4A16_EHIP = -6,         /* a HIP runtime call or kernel launch failed (fused
+                              calls: or host memory ran out)                    */
   W4A16_ESCRATCH = -7      /* w4a16_gemm_grouped_static: the call needs more
                               workspace than W4A16_STATIC_SCRATCH_BYTES         */
 };
@@ -384,8 +385,13 @@ typedef struct w4a16_epilogue {
 
 /* Y of several independent problems, each with its epilogue (bias, residual and
  * preact of the problem's activation type, 16-byte aligned).  problems and
- * epilogues are host arrays of `count` entries; other arguments, the workspace,
- * the sharing of launches and the errors are those of w4a16_gemm_grouped_ws.
+ * epilogues are host arrays of `count` entries; other arguments, the sharing of
+ * launches and the errors are those of w4a16_gemm_grouped_ws.  The workspace
+ * (w4a16_linear_workspace_size() bytes for the same arrays, 16-byte aligned;
+ * EALIGN) serves prescaled activations and fp32 partial sums; with less, or
+ * NULL, X * s is scaled in the kernels and K is not split.  Block shapes and
+ * splits are chosen for the fused calls, so their fp32 summation order can
+ * differ from w4a16_gemm's; the same call always gives the same bits.
  * Outputs (Y, preact) must not overlap each other or any input, except that
  * residual may be the same problem's Y.  Asynchronous on `stream`. */
 int w4a16_linear_workspace_size(const w4a16_problem *problems, const w4a16_epilogue *epilogues,

@@ -549,6 +549,80 @@ def test_backward_without_dx():
     assert (np.abs(values(db) - dYv.sum(0)) <= (M + 8) * 2.0 ** -24 * np.abs(dYv).sum(0) + 1e-30).all()
 
 
+def test_linear_past_32_bit_offsets():
+    """X and Y of more than 2^31 bytes: rows at the start, around the 2 GiB offsets and at the
+    end against the oracle."""
+    torch = torch_cuda()
+    M, N, K = 270_001, 4096, 4096
+    note(f"linear M={M} N={N} K={K}: X and Y past 2 GiB")
+    w = weight(30, N, K)
+    X = torch.randn(M, K, device="cuda", generator=torch.Generator("cuda").manual_seed(3)).half()
+    R = X.flip(0).contiguous()
+    Y = w4.w4a16_linear(X, w.pw, residual=R, act=w4.ACT_RELU)
+    rows = torch.tensor([0, 1, 131071, 131072, 262143, 262144, 262145, M - 2, M - 1])
+    Xv = values(X[rows.cuda()])
+    ref, z = of.linear(Xv, w.W, None, "relu", values(R[rows.cuda()]))
+    e = act_bound(z, product_bound(Xv, w.W, U["fp16"], K))
+    close(values(Y[rows.cuda()]), ref, e + U["fp16"] * (np.abs(ref) + e) + TINY, "large", 5 * REL["fp16"])
+
+
+def test_backward_past_32_bit_offsets():
+    torch = torch_cuda()
+    M, N, K = 270_001, 4112, 128
+    note(f"backward M={M} N={N} K={K}: dY past 2 GiB")
+    w = weight(31, N, K)
+    dY = (torch.randn(M, N, device="cuda", generator=torch.Generator("cuda").manual_seed(4)) * 0.25).half()
+    dX, dZ, db = w4.w4a16_linear_backward(dY, w4.w4a16_transpose(w.pw), bias_grad=True)
+    rows = torch.tensor([0, 1, 130559, 130560, 261118, 261119, 261120, M - 2, M - 1])
+    d = values(dY[rows.cuda()])
+    ref = of.input_grad([d], [w.W])
+    close(values(dX[rows.cuda()]), ref,
+          dx_bound([d], [w.D], None, U["fp16"], N, ref, [np.zeros_like(d)]), "large", REL["fp16"])
+    total, size = values(dY.double().sum(0)), values(dY.abs().double().sum(0))
+    # at most (M / 256 rows + 4 lanes + 256 strips) additions in a row
+    assert (np.abs(values(db) - total) <= (M / 256 + 260) * 2.0 ** -24 * size).all()
+
+
+def test_binding_refuses_views_types_and_shapes():
+    torch = torch_cuda()
+    w = weight(1, 48, 384)
+    X = torch.zeros(6, 384, dtype=torch.float16, device="cuda")
+    b = torch.zeros(48, dtype=torch.float16, device="cuda")
+    wt = w4.w4a16_transpose(w.pw)
+    dY = torch.zeros(6, 48, dtype=torch.float16, device="cuda")
+    for bad, kw in ((X[::2], {}), (X.t().contiguous().t(), {}), (X[:, :256], {}), (X[None], {})):
+        with pytest.raises(ValueError):
+            w4.w4a16_linear(bad, w.pw, **kw)
+    for kw in (dict(bias=b[:32]), dict(residual=dY[:3]), dict(preact=dY.t().contiguous().t()),
+               dict(out=torch.zeros(6, 64, dtype=torch.float16, device="cuda"))):
+        with pytest.raises(ValueError):
+            w4.w4a16_linear(X, w.pw, **kw)
+    for kw in (dict(bias=b.float()), dict(bias=b.bfloat16()), dict(residual=dY.cpu()), dict(s=b.float())):
+        with pytest.raises((TypeError, ValueError)):
+            w4.w4a16_linear(X, w.pw, **kw)
+    with pytest.raises(TypeError):
+        w4.w4a16_linear(X.float(), w.pw)
+    with pytest.raises(ValueError):
+        w4.w4a16_gated(X, w.pw, weight(1, 272, 640).pw)
+    with pytest.raises(ValueError):
+        w4.w4a16_linear_backward(dY[:, ::2], wt)
+    with pytest.raises(ValueError):
+        w4.w4a16_linear_backward(dY, wt, act=w4.ACT_SILU, preact=dY[:3])
+    with pytest.raises(w4.W4A16Error) as e:
+        w4.w4a16_linear_backward(dY, wt, act=w4.ACT_SILU)            # no pre-activation
+    assert e.value.status == -1
+    with pytest.raises(w4.W4A16Error) as e:
+        w4.w4a16_linear(X, w.pw, act=17)
+    assert e.value.status == -3
+    with pytest.raises(ValueError):
+        w4.w4a16_transpose(weight(1, 272, 640, False, 4, 900).pw)    # fp16 outliers
+    small = torch.zeros(16, dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError):
+        w4.LinearCall([(torch.zeros(64, 4096, dtype=torch.float16, device="cuda"), weight(1, 16, 4096).pw,
+                        None, torch.zeros(64, 16, dtype=torch.float16, device="cuda"), w4.Epilogue())],
+                      workspace=small)
+
+
 # ---- together -----------------------------------------------------------------------
 
 @pytest.mark.parametrize("M", [5, 70])

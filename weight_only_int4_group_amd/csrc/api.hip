@@ -510,22 +510,32 @@ int fuse_gated(const w4a16_problem *gate, const w4a16_problem *up, const void *b
 
 extern "C" {
 
+// The fused calls keep host lists of their problems; no exception of those
+// (out of host memory) leaves the C ABI.
 int w4a16_linear_workspace_size(const w4a16_problem *problems, const w4a16_epilogue *epilogues,
                                 int count, size_t *bytes) {
   if (!bytes) return W4A16_EINVAL;
-  std::vector<w4a16::Fused> f;
-  const int rc = fuse_linear(problems, epilogues, count, f);
-  if (rc) return rc;
-  *bytes = grouped_bytes(problems, count, f.data());
-  return W4A16_OK;
+  try {
+    std::vector<w4a16::Fused> f;
+    const int rc = fuse_linear(problems, epilogues, count, f);
+    if (rc) return rc;
+    *bytes = grouped_bytes(problems, count, f.data());
+    return W4A16_OK;
+  } catch (...) {
+    return W4A16_EHIP;
+  }
 }
 
 int w4a16_linear(const w4a16_problem *problems, const w4a16_epilogue *epilogues, int count,
                  void *workspace, size_t workspace_bytes, void *stream) {
-  std::vector<w4a16::Fused> f;
-  const int rc = fuse_linear(problems, epilogues, count, f);
-  if (rc) return rc;
-  return launch_grouped(problems, count, f.data(), workspace, workspace_bytes, stream);
+  try {
+    std::vector<w4a16::Fused> f;
+    const int rc = fuse_linear(problems, epilogues, count, f);
+    if (rc) return rc;
+    return launch_grouped(problems, count, f.data(), workspace, workspace_bytes, stream);
+  } catch (...) {
+    return W4A16_EHIP;
+  }
 }
 
 int w4a16_gated_workspace_size(const w4a16_problem *gate, const w4a16_problem *up, size_t *bytes) {
@@ -534,8 +544,12 @@ int w4a16_gated_workspace_size(const w4a16_problem *gate, const w4a16_problem *u
   w4a16::Fused f;
   const int rc = fuse_gated(gate, up, nullptr, nullptr, W4A16_ACT_NONE, gate ? gate->X : nullptr, &p, &f);
   if (rc) return rc;
-  *bytes = grouped_bytes(&p, 1, &f);
-  return W4A16_OK;
+  try {
+    *bytes = grouped_bytes(&p, 1, &f);
+    return W4A16_OK;
+  } catch (...) {
+    return W4A16_EHIP;
+  }
 }
 
 int w4a16_gated(const w4a16_problem *gate, const w4a16_problem *up, const void *bias_gate,
@@ -545,7 +559,11 @@ int w4a16_gated(const w4a16_problem *gate, const w4a16_problem *up, const void *
   w4a16::Fused f;
   const int rc = fuse_gated(gate, up, bias_gate, bias_up, act, H, &p, &f);
   if (rc) return rc;
-  return launch_grouped(&p, 1, &f, workspace, workspace_bytes, stream);
+  try {
+    return launch_grouped(&p, 1, &f, workspace, workspace_bytes, stream);
+  } catch (...) {
+    return W4A16_EHIP;
+  }
 }
 
 }  // extern "C"
