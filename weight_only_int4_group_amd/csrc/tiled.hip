@@ -941,10 +941,16 @@ __device__ __forceinline__ void tiled_dma_body(const TiledSet &ts, const FS &fs)
     for (int i = 0; i < TM; ++i)
       a[i] = *reinterpret_cast<const u32x4 *>(&As[ks][buf][(16 * i + r) * kGroup + 8 * pc]);
   };
-  // Small tiles have registers to read a whole k step's A operands one k step
-  // ahead, the first before the next group's loads are issued (1 to 4% faster:
-  // gated M = 64, 18944 x 3584 bf16 35.5 -> 34.2 us).
-  constexpr bool kAhead = TN == 2;
+  // How a k step's instructions are ordered.  Pinned (fp16 plain launches, and
+  // fp16 128- and 96-row blocks): one LDS read, its MFMAs and about seven VALU ops
+  // at a time.  Otherwise in the compiler's order, and small tiles, which have the
+  // registers, read a whole k step's A operands one k step ahead, the first
+  // before the next group's loads are issued.  Measured, pinned against not, in
+  // us: gated M = 64, 14336 x 4096 fp16: 25.5 and 22.8; M = 24: 18.6 and 18.3; 18944
+  // x 3584 bf16: 37.4 and 34.2; M = 4096 bf16: 845 and 834, fp16: 804 and 812; the
+  // Qwen2-7B layer's grouped fp16 launch at M = 17: 33.9 and 35.8.
+  constexpr bool kPinned = !BF && (TN == 4 || EPI == kPlain);
+  constexpr bool kAhead = TN == 2 && !kPinned;
   // the four k steps of a group: this wave's B operands dequantized once per
   // k step, then TM x TN MFMAs with A read from LDS buffer `buf`
   auto compute = [&](const BStage &b, int buf, u32x4 (&a)[TM]) {
@@ -979,11 +985,7 @@ __device__ __forceinline__ void tiled_dma_body(const TiledSet &ts, const FS &fs)
         return __builtin_bit_cast(u32x4, dequant_word(b.code[j][0][t], bias_lo[j], bias_hi[j], scale[j]));
     };
     // software pipeline: k step tt + 1's B operands are dequantized while k
-    // step tt's MFMAs run.  fp16 at TN = 4: interleaved by the scheduler (one LDS
-    // read, TN MFMAs and about seven VALU ops at a time; 1% faster than the
-    // compiler's own order, which the others keep: pinned, gated M = 64 took 25.6
-    // against 23.4 us (14336 x 4096 fp16) and 37.4 against 35.6 (18944 x 3584
-    // bf16), M = 4096 bf16 845 against 834)
+    // step tt's MFMAs run
     u32x4 bop[TN];
 #pragma unroll
     for (int j = 0; j < TN; ++j) bop[j] = dequant(j, 0);
@@ -1007,7 +1009,7 @@ __device__ __forceinline__ void tiled_dma_body(const TiledSet &ts, const FS &fs)
                          : mfma16(__builtin_bit_cast(half8, aop), __builtin_bit_cast(half8, bop[j]),
                                   acc[i][j]);
       }
-      if constexpr (!BF && TN == 4) {
+      if constexpr (kPinned) {
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
           __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // one LDS read
