@@ -279,6 +279,15 @@ def test_gated_outliers(M, dtype, counts):
         run_gated(M, 272, 640, dtype, "silu", bits=8, counts=counts)
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("M", [130, 200, 256])
+def test_blocks_of_128_rows_and_columns(M, dtype, bits):
+    """Row counts and widths whose plan is two 128 x 128 blocks on a CU."""
+    run_linear(M, 28672, 256, dtype, "silu", bias=True, residual=True, pre=True, awq=True, bits=bits)
+    run_gated(M, 14336, 256, dtype, "silu", bias=True, pre=True, awq=True, bits=bits)
+
+
 @pytest.mark.parametrize("M", [4, 64, 130])
 def test_gated_without_workspace(M):
     run_gated(M, 272, 4096, "fp16", "gelu_tanh", bias=True, pre=True, awq=True, workspace=False)

@@ -1157,14 +1157,17 @@ __device__ __forceinline__ void tiled_dma_body(const TiledSet &ts, const FS &fs)
   }
 }
 
+// waves per SIMD that the registers of a block shape leave room for
+constexpr int dma_waves(int TM, int TN) { return TN == 2 && TM <= 4 ? 4 : 2; }
+
 template <int TM, int TN, int KS, bool BF, bool W8>
-__global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(TN == 2 ? 4 : 2, TN == 2 ? 4 : 2))) void tiled_dma_kernel(
+__global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(dma_waves(TM, TN), dma_waves(TM, TN)))) void tiled_dma_kernel(
     TiledSet ts) {
   tiled_dma_body<TM, TN, KS, BF, W8, kPlain>(ts, NoFused{});
 }
 
 template <int TM, int TN, int KS, bool BF, bool W8, int EPI>
-__global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(TN == 2 ? 4 : 2, TN == 2 ? 4 : 2))) void tiled_dma_fused_kernel(
+__global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(dma_waves(TM, TN), dma_waves(TM, TN)))) void tiled_dma_fused_kernel(
     TiledSet ts, TiledFused fs) {
   tiled_dma_body<TM, TN, KS, BF, W8, EPI>(ts, fs);
 }
@@ -1463,16 +1466,18 @@ int dma_plan(const GemmDesc *d, int count, int tm, bool unsplit, int *split) {
 // with 1, 2, 3 and 4 workgroups on a CU (0: that many do not fit), measured
 // with bf16 activations and INT4 codes.
 struct FusedShape {
-  int tm, ks;
+  int tm, tn, ks;
   double us[4];
 };
 constexpr FusedShape kFusedShapes[] = {
-    {8, 1, {2.9, 3.5, 0, 0}},     {6, 1, {2.5, 3.0, 0, 0}},   {4, 1, {1.3, 1.5, 2.0, 2.57}},
-    {4, 2, {1.6, 2.65, 0, 0}},    {3, 1, {1.15, 1.35, 1.75, 2.25}}, {3, 2, {1.45, 2.4, 0, 0}},
-    {2, 1, {1.0, 1.2, 1.5, 1.85}}, {2, 2, {1.25, 2.1, 0, 0}},
+    {8, 4, 1, {2.9, 3.5, 0, 0}},         {6, 4, 1, {2.5, 3.0, 0, 0}},
+    {8, 2, 1, {1.65, 2.1, 0, 0}},        {4, 2, 1, {1.3, 1.5, 2.0, 2.57}},
+    {4, 2, 2, {1.6, 2.65, 0, 0}},        {3, 2, 1, {1.15, 1.35, 1.75, 2.25}},
+    {3, 2, 2, {1.45, 2.4, 0, 0}},        {2, 2, 1, {1.0, 1.2, 1.5, 1.85}},
+    {2, 2, 2, {1.25, 2.1, 0, 0}},
 };
 
-// The plan of a fused launch: block shape (*tm, the returned K slices) and
+// The plan of a fused launch: block shape (*shape, the returned K slices) and
 // splits of each problem, the least modelled time of every shape and range
 // length.  Unlike launch_model, which plans the plain products (and whose
 // choices fix their bits), it knows that a workgroup alone on a CU runs faster
@@ -1480,8 +1485,13 @@ constexpr FusedShape kFusedShapes[] = {
 // where large ones would have to be split.  Measured against launch_model's
 // plans, in us: linear M = 1531, 4096 x 4096 bf16: 77.1 -> 70.0 (64 x 128 blocks,
 // unsplit); M = 512: 37.7 -> 31.1; gated M = 64, 18944 x 3584 bf16: 43.7 -> 39.3;
-// M = 200, 14336 x 4096 fp16: 75.9 -> 66.8.
-int fused_plan(const GemmDesc *d, int count, bool unsplit, int *tm, int *split) {
+// M = 200, 14336 x 4096 fp16: 75.9 -> 66.8.  Blocks of 128 x 128 (fused
+// launches only: the plain product's shapes fix its bits) fill two workgroups on
+// a CU where 128 x 256 leaves one: that gated M = 200 72.3 -> 62.8 (fp16, one
+// box), M = 256 bf16 78.2 -> 68.1; linear M = 200, 28672 x 8192 bf16 137.8 -> 129.3.
+// They are no gain where 64 x 128 blocks fill the CUs evenly (linear M = 1531 above:
+// 67.0 against 68.4).
+int fused_plan(const GemmDesc *d, int count, bool unsplit, DmaShape *shape, int *split) {
   // distinct range lengths, as in choose_splits, down to kMinFusedGroups groups
   constexpr int kMinFusedGroups = 4;
   int cand[kMaxTiled * kMaxSplit];
@@ -1496,7 +1506,7 @@ int fused_plan(const GemmDesc *d, int count, bool unsplit, int *tm, int *split) 
   double best = 0.0;
   int best_ks = 0;
   for (const FusedShape &f : kFusedShapes) {
-    const DmaShape ds = dma_shape(f.tm);
+    const DmaShape ds = {f.tm, f.tn};
     const int per_cu = f.us[3] > 0 ? 4 : 2;
     for (int ci = 0; ci < nc; ++ci) {
       int s[kMaxTiled], longest = 0;
@@ -1523,7 +1533,7 @@ int fused_plan(const GemmDesc *d, int count, bool unsplit, int *tm, int *split) 
       if (best_ks == 0 || us < best) {
         best = us;
         best_ks = f.ks;
-        *tm = f.tm;
+        *shape = ds;
         for (int i = 0; i < count; ++i) split[i] = s[i];
       }
     }
@@ -1537,9 +1547,13 @@ int fused_plan(const GemmDesc *d, int count, bool unsplit, int *tm, int *split) 
 template <int TM, int TN, int KS, bool BF, bool W8>
 void launch_dma_tile(int epi, dim3 grid, hipStream_t stream, const TiledSet &ts, const TiledFused &fs) {
   const dim3 threads(256 * KS);
-  if (epi == kPlain)
-    hipLaunchKernelGGL((tiled_dma_kernel<TM, TN, KS, BF, W8>), grid, threads, 0, stream, ts);
-  else if (epi == kLinear)
+  if constexpr (TM != 8 || TN != 2) {  // 128 x 128 blocks: fused plans only
+    if (epi == kPlain) {
+      hipLaunchKernelGGL((tiled_dma_kernel<TM, TN, KS, BF, W8>), grid, threads, 0, stream, ts);
+      return;
+    }
+  }
+  if (epi == kLinear)
     hipLaunchKernelGGL((tiled_dma_fused_kernel<TM, TN, KS, BF, W8, kLinear>), grid, threads, 0,
                        stream, ts, fs);
   else
@@ -1547,27 +1561,24 @@ void launch_dma_tile(int epi, dim3 grid, hipStream_t stream, const TiledSet &ts,
                        stream, ts, fs);
 }
 template <bool BF, bool W8>
-hipError_t launch_dma(int tm, int ks, int epi, dim3 grid, hipStream_t stream, const TiledSet &ts,
+hipError_t launch_dma(DmaShape s, int ks, int epi, dim3 grid, hipStream_t stream, const TiledSet &ts,
                       const TiledFused &fs) {
-  if (tm == 8 && ks == 1)
-    launch_dma_tile<8, 4, 1, BF, W8>(epi, grid, stream, ts, fs);
-  else if (tm == 6 && ks == 1)
-    launch_dma_tile<6, 4, 1, BF, W8>(epi, grid, stream, ts, fs);
-  else if (tm == 4 && ks == 2)
-    launch_dma_tile<4, 2, 2, BF, W8>(epi, grid, stream, ts, fs);
-  else if (tm == 4 && ks == 1)
-    launch_dma_tile<4, 2, 1, BF, W8>(epi, grid, stream, ts, fs);
-  else if (tm == 3 && ks == 2)
-    launch_dma_tile<3, 2, 2, BF, W8>(epi, grid, stream, ts, fs);
-  else if (tm == 3 && ks == 1)
-    launch_dma_tile<3, 2, 1, BF, W8>(epi, grid, stream, ts, fs);
-  else if (tm == 2 && ks == 2)
-    launch_dma_tile<2, 2, 2, BF, W8>(epi, grid, stream, ts, fs);
-  else if (tm == 2 && ks == 1)
-    launch_dma_tile<2, 2, 1, BF, W8>(epi, grid, stream, ts, fs);
-  else
-    return hipErrorInvalidValue;
-  return hipSuccess;
+#define W4_DMA(TM, TN, KS)                                          \
+  if (s.tm == TM && s.tn == TN && ks == KS) {                       \
+    launch_dma_tile<TM, TN, KS, BF, W8>(epi, grid, stream, ts, fs); \
+    return hipSuccess;                                              \
+  }
+  W4_DMA(8, 4, 1)
+  W4_DMA(6, 4, 1)
+  W4_DMA(8, 2, 1)
+  W4_DMA(4, 2, 2)
+  W4_DMA(4, 2, 1)
+  W4_DMA(3, 2, 2)
+  W4_DMA(3, 2, 1)
+  W4_DMA(2, 2, 2)
+  W4_DMA(2, 2, 1)
+#undef W4_DMA
+  return hipErrorInvalidValue;
 }
 
 // The tiled_kernel instance for one activation type, code width, presence of
@@ -1590,11 +1601,12 @@ void launch_regs(int epi, dim3 grid, hipStream_t stream, const TiledSet &ts, con
 
 size_t tiled_workspace_bytes(const GemmDesc *d, int count) {
   if (count < 1 || count > kMaxTiled) return 0;
-  int tm = dma_tm(d, count);
+  const int tm = dma_tm(d, count);
   const bool dma = tm != 0;
   int split[kMaxTiled];
+  DmaShape shape;
   if (dma && d[0].fused)
-    fused_plan(d, count, false, &tm, split);
+    fused_plan(d, count, false, &shape, split);
   else if (dma)
     dma_plan(d, count, tm, false, split);
   else
@@ -1614,12 +1626,13 @@ hipError_t launch_tiled_set(const GemmDesc *d, int count, void *workspace, size_
   // room for the split partials as well, K is not split.
   const size_t have = workspace ? workspace_bytes : 0;
   const size_t pre = prescale_need(d, count);
-  int tm = dma_tm(d, count);
+  const int tm = dma_tm(d, count);
   const bool dma = tm != 0 && pre <= have;
+  DmaShape ds = dma_shape(tm);
   int split[kMaxTiled];
   int ks = 1;
   if (dma && d[0].fused)
-    ks = fused_plan(d, count, false, &tm, split);
+    ks = fused_plan(d, count, false, &ds, split);
   else if (dma)
     ks = dma_plan(d, count, tm, false, split);
   else
@@ -1629,11 +1642,10 @@ hipError_t launch_tiled_set(const GemmDesc *d, int count, void *workspace, size_
   if ((dma ? pre : 0) + parts > have) {  // no room for partials: one K range
     for (int i = 0; i < count; ++i) split[i] = 1;
     if (dma && d[0].fused)
-      ks = fused_plan(d, count, true, &tm, split);
+      ks = fused_plan(d, count, true, &ds, split);
     else if (dma)
       ks = dma_plan(d, count, tm, true, split);
   }
-  const DmaShape ds = dma_shape(tm);
   const int bm = dma ? ds.bm() : 16 * regs_tm(d, count), bn = dma ? ds.bn() : kBN;
   TiledSet ts = {};
   TiledFused fs = {};
@@ -1707,9 +1719,9 @@ hipError_t launch_tiled_set(const GemmDesc *d, int count, void *workspace, size_
   // one activation type, code width and kind of epilogue per launch
   const int epi = !d[0].fused ? kPlain : d[0].gated() ? kGated : kLinear;
   if (dma) {
-    const hipError_t e = d[0].w8     ? launch_dma<false, true>(tm, ks, epi, grid, stream, ts, fs)
-                         : d[0].bf16 ? launch_dma<true, false>(tm, ks, epi, grid, stream, ts, fs)
-                                     : launch_dma<false, false>(tm, ks, epi, grid, stream, ts, fs);
+    const hipError_t e = d[0].w8     ? launch_dma<false, true>(ds, ks, epi, grid, stream, ts, fs)
+                         : d[0].bf16 ? launch_dma<true, false>(ds, ks, epi, grid, stream, ts, fs)
+                                     : launch_dma<false, false>(ds, ks, epi, grid, stream, ts, fs);
     if (e != hipSuccess) return e;
   } else if (d[0].w8 && d[0].bf16 && out)  // INT8 codes
     launch_regs<true, true, true>(epi, grid, stream, ts, fs);
