@@ -433,9 +433,9 @@ int w4a16_transpose(const void *Wq, const void *scales, const void *zeros, int64
 /* Backward of one linear layer with frozen (packed) weights:
  *   dZ = dY * act'(Z),   dbias = sum over rows of dZ.
  * dY [M][N]; Z = preact [M][N] as the forward kept it, and dZ [M][N] output
- * (it may be dY or preact itself), both required unless act is
- * W4A16_ACT_NONE, where dZ is dY and both must be NULL; dbias: fp32 [N], or
- * NULL.  dZ is rounded once to the activations' type, and the product below
+ * (it may be the same term's dY or preact, where no other term reads that),
+ * both required unless act is W4A16_ACT_NONE, where dZ is dY and both must be
+ * NULL; dbias: fp32 [N], or NULL.  dZ is rounded once to the activations' type, and the product below
  * reads the rounded values; dbias sums the unrounded ones in fp32, in a fixed
  * order.  Wt, meta: the layer's transposed weight. */
 typedef struct w4a16_backward_term {
@@ -457,10 +457,12 @@ typedef struct w4a16_backward_term {
  * W4A16_DTYPE_*); sums are fp32, s and add are applied in fp32, and dX is
  * rounded once.  Outlier weights have no transposed form.  All terms share
  * wbits (EUNSUPPORTED otherwise).  M >= 0, dX may be NULL to get only dZ and
- * dbias.  Outputs must not overlap each other or any input except as said.
- * workspace: w4a16_backward_workspace_size() bytes (depends on M, K, dtype and
- * the terms' N, act, dbias and whether dX is NULL; may be 0), 256-byte aligned;
- * EINVAL if smaller.  Asynchronous on `stream`. */
+ * dbias.  Outputs must not overlap each other or any input except as said
+ * (EINVAL where two terms' dZ or dbias overlap, or a dZ or dX what another term
+ * or the product reads).
+ * workspace: w4a16_linear_backward_workspace_size() bytes (depends on M, K,
+ * dtype and the terms' N, wbits and whether dbias is set; may be 0), 256-byte
+ * aligned; EINVAL if smaller than this call needs.  Asynchronous on `stream`. */
 int w4a16_linear_backward_workspace_size(const w4a16_backward_term *terms, int count, int64_t M,
                                          int64_t K, int dtype, size_t *bytes);
 int w4a16_linear_backward(const w4a16_backward_term *terms, int count, const void *s,
@@ -469,7 +471,7 @@ int w4a16_linear_backward(const w4a16_backward_term *terms, int count, const voi
 
 /* Backward of the gated block, from dH and the G and U that its forward kept:
  *   dG = dH * U * act'(G),  dU = dH * act(G),  dX = add + s * (dG . Dg + dU . Du),
- * dbias_gate and dbias_up the fp32 row sums of dG and dU.  gate and up carry
+ * dbias_gate and dbias_up the fp32 sums over rows of dG and dU.  gate and up carry
  * Wt, meta, N, wbits and dbias (or NULL) of the two weights, preact = G or U,
  * and dZ = the output for dG or dU (each may be the same term's preact); the
  * gate's act is the block's (act must be 0 in up) and both dY are ignored.

@@ -144,6 +144,30 @@ def test_gated_backward_refusals(kw, code):
     assert gated_backward_rc(**kw) == code
 
 
+C, D, E = 1 << 22, 1 << 23, 1 << 24  # apart from A and B and each other
+
+
+@pytest.mark.parametrize("kw", [
+    dict(count=2, dX=E, terms=[term(dY=A, preact=B, dZ=A), term(dY=A, preact=C, dZ=D)]),   # dZ over a shared dY
+    dict(count=2, dX=E, terms=[term(dY=A, preact=B, dZ=D), term(dY=C, preact=C, dZ=D)]),   # one dZ for both
+    dict(count=2, dX=E, M=4, terms=[term(dY=A, preact=B, dZ=D), term(dY=C, preact=C, dZ=D + 64)]),
+    dict(count=2, dX=E, terms=[term(dY=A, preact=B, dZ=C), term(dY=D, preact=C, dZ=D)]),   # another's preact
+    dict(count=2, dX=E, terms=[term(dY=A, preact=B, dZ=C, dbias=1 << 25),
+                               term(dY=D, preact=D, dZ=D, dbias=1 << 25)]),                # one dbias
+    dict(dX=A, t=dict(dY=A, preact=B, dZ=C)), dict(dX=C, t=dict(dY=A, preact=B, dZ=C)),
+    dict(dX=B, t=dict(dY=A, preact=B, dZ=C)), dict(dX=A, t=dict(dY=A, preact=None, dZ=None, act=0)),
+])
+def test_backward_refuses_outputs_over_what_is_still_read(kw):
+    assert backward_rc(**kw) == -1
+
+
+def test_gated_backward_refuses_outputs_over_what_is_still_read():
+    G = dict(preact=B, dZ=B)
+    assert gated_backward_rc(G, dict(preact=C, dZ=B), dH=D, dX=E) == -1
+    assert gated_backward_rc(dict(preact=B, dZ=C), dict(preact=C, dZ=B), dH=D, dX=E) == -1
+    assert gated_backward_rc(G, dict(preact=C, dZ=C), dH=D, dX=C) == -1
+
+
 def test_backward_workspace_sizes():
     L, n = w4.lib(), ctypes.c_size_t()
 

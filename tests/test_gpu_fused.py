@@ -223,6 +223,16 @@ def test_streamed_in_ranges_of_k(M, K, dtype, bits):
 
 @pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("M,K", [(5, 14464), (16, 4224)])
+def test_streamed_without_room_for_ranges(M, K, dtype, bits):
+    """The same rows without a workspace: windows of X * s in one launch."""
+    run_linear(M, 48, K, dtype, "silu", bias=True, residual=True, pre=True, awq=True, bits=bits,
+               workspace=False)
+    run_gated(M, 48, K, dtype, "silu", bias=True, pre=True, awq=True, bits=bits, workspace=False)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("M", [1, 9, 40, 130])
 def test_linear_outliers(M, dtype, bits):
     run_linear(M, 272, 640, dtype, "none", bias=True, residual=True, pre=True, awq=True, bits=bits,

@@ -1,5 +1,6 @@
 // C-ABI front end: argument validation (host only, before any HIP call),
 // kernel choice by M, and launches on the caller's stream.
+#include <functional>
 #include <mutex>
 #include <vector>
 
@@ -817,6 +818,35 @@ int check_backward_pointers(const w4a16_backward_term &t, bool gated, bool dx, i
   return W4A16_OK;
 }
 
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+  const char *x = static_cast<const char *>(a), *y = static_cast<const char *>(b);
+  return x && y && std::less<const char *>()(x, y + nb) && std::less<const char *>()(y, x + na);
+}
+
+// dX is formed after every dZ, from all of them, and the terms' dZ one after
+// the other: a dZ or dX over what another term or the product still reads would
+// give wrong sums.
+bool backward_overlaps(const w4a16_backward_term *terms, int count, const void *dX, int64_t M,
+                       int64_t K) {
+  for (int i = 0; i < count; ++i) {
+    const size_t n = (size_t)(M * terms[i].N) * 2;
+    const void *read[2] = {terms[i].dY, terms[i].preact};
+    if (overlap(dX, (size_t)(M * K) * 2, terms[i].dZ, n)) return true;
+    for (const void *r : read)
+      if (overlap(dX, (size_t)(M * K) * 2, r, n)) return true;
+    for (int j = 0; j < count; ++j) {
+      if (i == j) continue;
+      const size_t nj = (size_t)(M * terms[j].N) * 2;
+      if (overlap(terms[j].dZ, nj, terms[i].dZ, n) ||
+          overlap(terms[j].dbias, (size_t)terms[j].N * 4, terms[i].dbias, (size_t)terms[i].N * 4))
+        return true;
+      for (const void *r : read)
+        if (overlap(terms[j].dZ, nj, r, n)) return true;
+    }
+  }
+  return false;
+}
+
 int check_backward_common(const w4a16_backward_term *terms, int count, bool gated, const void *s,
                           const void *add, const void *dX, int64_t M, int64_t K, int dtype,
                           const void *workspace, size_t workspace_bytes) {
@@ -828,7 +858,8 @@ int check_backward_common(const w4a16_backward_term *terms, int count, bool gate
   if (!aligned16(s) || !aligned16(add) || !aligned16(dX)) return W4A16_EALIGN;
   const size_t need = backward_bytes(terms, count, gated, dX != nullptr, M, K, dtype);
   if (need > 0 && (!workspace || workspace_bytes < need)) return W4A16_EINVAL;
-  return workspace && !aligned256(workspace) ? W4A16_EALIGN : W4A16_OK;
+  if (workspace && !aligned256(workspace)) return W4A16_EALIGN;
+  return M > 0 && backward_overlaps(terms, count, dX, M, K) ? W4A16_EINVAL : W4A16_OK;
 }
 
 }  // namespace
@@ -907,7 +938,8 @@ int w4a16_gated_backward(const void *dH, const w4a16_backward_term *gate,
                          int64_t M, int64_t K, int dtype, void *workspace, size_t workspace_bytes,
                          void *stream) {
   if (!gate || !up || gate->N != up->N) return W4A16_EINVAL;
-  const w4a16_backward_term terms[2] = {*gate, *up};
+  w4a16_backward_term terms[2] = {*gate, *up};
+  terms[0].dY = terms[1].dY = nullptr;  // ignored
   int rc = check_backward_shape(terms, 2, M, K, dtype);
   if (rc) return rc;
   if (up->act != W4A16_ACT_NONE) return W4A16_EINVAL;
