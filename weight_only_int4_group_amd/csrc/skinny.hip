@@ -1378,7 +1378,7 @@ namespace {
 // whose latencies add up; cut into ranges they are 4 to 8 row blocks by an eighth
 // (short rows: a quarter) of K, which fits.  Measured in us, windows or wide
 // workgroups against ranges and the second launch that adds them: 4096 x
-// 14336, M = 5: 16.7 -> 13.7 (bf16 19.2 -> 14.0), M = 16: 21.3 -> 16.4 (29.5 ->
+// 14336, M = 5: 16.7 -> 12.4 (bf16 19.2 -> 13.0), M = 16: 21.3 -> 16.4 (29.5 ->
 // 18.1); 1024 x 8192 bf16, M = 9: 19.3 -> 10.8; 4096 x 4096, M = 16: 10.9 -> 9.8.  With 896
 // row blocks (14336 x 4096, M = 16) 13.7 -> 14.9, and where the rows fit (M = 1) 9.9
 // -> 12.8: not split.

@@ -1336,7 +1336,7 @@ constexpr int kDmaMinM = 17;
 // 64 x 128) with one K slice (four waves) or two (eight waves), whichever the
 // launch model below prefers; bf16 activations and INT8 codes take the same
 // tiles (the 70B prefill layer with bf16 activations ran at 898-918 TFLOP/s
-// with 96-row tiles and 1090-1102 with 128-row ones; with INT8 codes at
+// with 96-row tiles and 1148-1188 with 128-row ones; with INT8 codes at
 // 941-944 and 1073-1076).  Below 64 rows the padded rows'
 // MFMAs and A reads are not free: the Qwen2-7B layer at M = 17 took 43 us
 // with 64-row tiles and 34 us with 32-row ones (bf16: 54 and 47 us; INT8
