@@ -120,8 +120,8 @@ def backward_rc(t=None, count=1, s=None, add=None, dX=A, M=1, K=128, dtype=0, ws
     (dict(t=dict(dZ=None)), -1), (dict(t=dict(act=0)), -1), (dict(t=dict(Wt=None)), -1),
     (dict(t=dict(meta=None)), -1), (dict(t=dict(dY=ODD)), -2), (dict(t=dict(dbias=ODD)), -2),
     (dict(t=dict(Wt=ODD)), -2), (dict(s=ODD), -2), (dict(add=ODD), -2), (dict(dX=ODD), -2),
-    (dict(add=A, dX=None), -1), (dict(ws=None, t=dict(dbias=A)), -1),
-    (dict(nbytes=8, t=dict(dbias=A)), -1), (dict(ws=A + 16, t=dict(dbias=A)), -2),
+    (dict(add=A, dX=None), -1), (dict(ws=None, M=300, t=dict(dbias=A)), -1),
+    (dict(nbytes=8, M=300, t=dict(dbias=A)), -1), (dict(ws=A + 16, t=dict(dbias=A)), -2),
     (dict(count=2, terms=[term(), term(wbits=8)]), -3),
 ])
 def test_linear_backward_refusals(kw, code):
@@ -138,7 +138,7 @@ def gated_backward_rc(g=None, u=None, dH=A, dX=A, M=1, K=128, dtype=0, ws=A, nby
     (dict(dH=None), -1), (dict(dH=ODD), -2), (dict(u=dict(N=32)), -1), (dict(u=dict(act=2)), -1),
     (dict(g=dict(preact=None)), -1), (dict(u=dict(preact=None)), -1), (dict(g=dict(dZ=None)), -1),
     (dict(u=dict(dZ=ODD)), -2), (dict(u=dict(wbits=8)), -3), (dict(g=dict(act=8)), -3), (dict(K=64), -1),
-    (dict(dtype=-1), -3), (dict(g=dict(Wt=None)), -1), (dict(g=dict(dbias=A), ws=None), -1),
+    (dict(dtype=-1), -3), (dict(g=dict(Wt=None)), -1), (dict(g=dict(dbias=A), M=300, ws=None), -1),
 ])
 def test_gated_backward_refusals(kw, code):
     assert gated_backward_rc(**kw) == code

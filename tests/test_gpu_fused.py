@@ -475,6 +475,15 @@ def test_linear_backward_extreme_shapes(M, N, K, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("M", [31, 128, 129, 256, 257])
+def test_bias_gradients_around_the_one_strip_limit(M, dtype):
+    """Column blocks in part (80 and 528 columns) on both sides of where one strip holds all rows."""
+    run_linear_backward(M, 80, 256, dtype, "none", bias=True)
+    run_linear_backward(M, 528, 128, dtype, "silu", bias=True, inplace=True)
+    run_gated_backward(M, 80, 128, dtype, "gelu_tanh", bias=True)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("M", [1, 20, 40, 100, 200])
 def test_backward_int8_codes(M, dtype):
     run_linear_backward(M, 272, 640, dtype, "silu", add=True, bias=True, awq=True, bits=8)

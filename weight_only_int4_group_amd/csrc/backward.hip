@@ -99,11 +99,14 @@ __global__ __launch_bounds__(256) void transpose_meta_kernel(const _Float16 *sca
 
 // ---- gradients of the epilogues -----------------------------------------------------
 
-// dZ (gated: dG and dU) of a strip of rows, 8 columns per thread, 4 rows at a
-// time, and the strip's column sums: each thread sums its rows in order, then
-// the 4 row lanes meet in LDS, so the sums do not depend on scheduling.
+// dZ (gated: dG and dU) of a strip of rows, 8 columns per thread, and the
+// strip's column sums: each thread sums its rows in order, then the row lanes
+// meet in LDS, so the sums do not depend on scheduling.
 // Bound by HBM: one read of dY and the pre-activations, one write of dZ.
-constexpr int kGradCols = 512;  // columns per workgroup
+// COLS columns per workgroup, 2048 / COLS rows at a time: 512 and 4, or, for
+// column sums of few rows (one_strip), 64 and 32, where one strip is all
+// rows and its sums are the result: no partial sums and no second launch.
+constexpr int kGradCols = 512, kOneStripCols = 64;
 struct GradArgs {
   const void *dY, *z, *u;      // z, u: pre-activations (null: dZ = dY, not written)
   void *dz, *du;
@@ -112,16 +115,18 @@ struct GradArgs {
   int act;
 };
 
-template <bool BF, bool GATED>
+template <bool BF, bool GATED, int COLS>
 __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
+  constexpr int kAcross = COLS / 8, kRows = 256 / kAcross;  // threads along a row, rows at a time
   const int strip = (int)blockIdx.x / a.col_blocks;
-  const int n = ((int)blockIdx.x - strip * a.col_blocks) * kGradCols + (int)(threadIdx.x & 63) * 8;
-  const int lane_row = threadIdx.x >> 6;
+  const int col0 = ((int)blockIdx.x - strip * a.col_blocks) * COLS;
+  const int x8 = (int)threadIdx.x % kAcross * 8, n = col0 + x8;
+  const int lane_row = threadIdx.x / kAcross;
   const int m1 = min(a.M, (strip + 1) * a.rows);
   float s0[8] = {0, 0, 0, 0, 0, 0, 0, 0}, s1[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   if (n < a.N) {
 #pragma unroll 2
-    for (int m = strip * a.rows + lane_row; m < m1; m += 4) {
+    for (int m = strip * a.rows + lane_row; m < m1; m += kRows) {
       const size_t at = (size_t)m * a.N + n;
       const u32x4 d = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.dY) + at);
       u32x4 z = d, u = d, oz, ou;
@@ -151,15 +156,22 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
       if (GATED) *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(a.du) + at) = ou;
     }
   }
-  __shared__ float red[4][kGradCols];
+  __shared__ float red[kRows][COLS];
   auto column_sums = [&](const float (&s)[8], float *part) {
     if (!part) return;  // uniform
 #pragma unroll
-    for (int j = 0; j < 8; ++j) red[lane_row][(threadIdx.x & 63) * 8 + j] = s[j];
+    for (int j = 0; j < 8; ++j) red[lane_row][x8 + j] = s[j];
     __syncthreads();
-    for (int x = threadIdx.x; x < kGradCols; x += 256) {
-      const int col = ((int)blockIdx.x - strip * a.col_blocks) * kGradCols + x;
-      if (col < a.N) part[(size_t)strip * a.N + col] = (red[0][x] + red[1][x]) + (red[2][x] + red[3][x]);
+    for (int x = threadIdx.x; x < COLS; x += 256) {
+      float sum;
+      if constexpr (kRows == 4) {
+        sum = (red[0][x] + red[1][x]) + (red[2][x] + red[3][x]);
+      } else {
+        sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) sum += red[i][x];
+      }
+      if (col0 + x < a.N) part[(size_t)strip * a.N + col0 + x] = sum;
     }
     __syncthreads();
   };
@@ -533,6 +545,12 @@ __global__ __launch_bounds__(256) void dx_reduce_kernel(DxArgs P) {
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
+// Column sums of few rows: one strip, without a second launch.  Measured in us
+// (bf16, 14336 columns), strips against one: no activation, M = 200 7.0 and 4.2,
+// M = 384 7.2 and 6.9, M = 512 7.1 and 9.5; SiLU, M = 128 8.8 and 6.4, M = 200 9.2
+// and 11.9; gated, M = 64 10.2 and 6.0, M = 128 11.7 and 11.1, M = 200 14.9 and 16.9.
+bool one_strip(int M, bool sums, bool act) { return sums && M <= (act ? 128 : 256); }
+
 // Rows per strip of grad_kernel: 32, fewer while the launch has under 512
 // workgroups (each is 256 threads: two per CU), more where column sums are
 // wanted and 256 strips would not cover M (their partials stay below 1/128 of
@@ -633,35 +651,47 @@ hipError_t launch_transpose(const void *Wq, const void *scales, const void *zero
   return hipGetLastError();
 }
 
-size_t grad_workspace_bytes(int M, int N, int sums) {
-  return sums ? sums * align256((size_t)strips_of(M, N, true) * N * sizeof(float)) : 0;
+size_t grad_workspace_bytes(int M, int N, int sums, bool act) {
+  if (!sums || one_strip(M, true, act)) return 0;
+  return sums * align256((size_t)strips_of(M, N, true) * N * sizeof(float));
 }
 
 hipError_t launch_grad(const GradDesc &d, void *workspace, hipStream_t stream) {
   const bool gated = d.u != nullptr, sums = d.db || d.db2;
-  const int strips = d.M > 0 ? strips_of(d.M, d.N, sums) : 0;
+  const bool one = d.M > 0 && one_strip(d.M, sums, d.z != nullptr);
+  const int strips = d.M == 0 ? 0 : one ? 1 : strips_of(d.M, d.N, sums);
   GradArgs a = {d.dY, d.z, d.u, d.dz, d.du, nullptr, nullptr, d.M, d.N, 0, 0, d.act};
   char *ws = static_cast<char *>(workspace);
   const size_t slab = align256((size_t)strips * d.N * sizeof(float));
-  if (d.db) {
-    a.part = reinterpret_cast<float *>(ws);
-    ws += slab;
+  if (one) {
+    a.part = static_cast<float *>(d.db);
+    a.part2 = static_cast<float *>(d.db2);
+  } else {
+    if (d.db) {
+      a.part = reinterpret_cast<float *>(ws);
+      ws += slab;
+    }
+    if (d.db2) a.part2 = reinterpret_cast<float *>(ws);
   }
-  if (d.db2) a.part2 = reinterpret_cast<float *>(ws);
   if (strips > 0) {
-    a.rows = strip_rows(d.M, d.N, sums);
-    a.col_blocks = (d.N + kGradCols - 1) / kGradCols;
+    a.rows = one ? d.M : strip_rows(d.M, d.N, sums);
+    const int cols = one ? kOneStripCols : kGradCols;
+    a.col_blocks = (d.N + cols - 1) / cols;
     const dim3 grid((unsigned)(strips * (long long)a.col_blocks)), th(256);
-    if (d.bf16 && gated)
-      hipLaunchKernelGGL((grad_kernel<true, true>), grid, th, 0, stream, a);
-    else if (d.bf16)
-      hipLaunchKernelGGL((grad_kernel<true, false>), grid, th, 0, stream, a);
-    else if (gated)
-      hipLaunchKernelGGL((grad_kernel<false, true>), grid, th, 0, stream, a);
-    else
-      hipLaunchKernelGGL((grad_kernel<false, false>), grid, th, 0, stream, a);
+#define W4_GRAD(BF, GATED)                                                                       \
+  if (d.bf16 == BF && gated == GATED) {                                                          \
+    if (one)                                                                                     \
+      hipLaunchKernelGGL((grad_kernel<BF, GATED, kOneStripCols>), grid, th, 0, stream, a);       \
+    else                                                                                         \
+      hipLaunchKernelGGL((grad_kernel<BF, GATED, kGradCols>), grid, th, 0, stream, a);           \
+  }
+    W4_GRAD(true, true)
+    W4_GRAD(true, false)
+    W4_GRAD(false, true)
+    W4_GRAD(false, false)
+#undef W4_GRAD
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || one) return e;
   }
   const dim3 bg((unsigned)((d.N + 31) / 32)), th(256);
   if (d.db) hipLaunchKernelGGL(bias_kernel, bg, th, 0, stream, a.part, strips, d.N, static_cast<float *>(d.db));
