@@ -461,7 +461,7 @@ typedef struct w4a16_backward_term {
  * (EINVAL where two terms' dZ or dbias overlap, or a dZ or dX what another term
  * or the product reads).
  * workspace: w4a16_linear_backward_workspace_size() bytes (depends on M, K,
- * dtype and the terms' N, act, wbits and whether dbias is set; may be 0), 256-byte
+ * dtype and the terms' N, wbits and whether dbias is set; may be 0), 256-byte
  * aligned; EINVAL if smaller than this call needs.  Asynchronous on `stream`. */
 int w4a16_linear_backward_workspace_size(const w4a16_backward_term *terms, int count, int64_t M,
                                          int64_t K, int dtype, size_t *bytes);

@@ -796,8 +796,7 @@ size_t backward_bytes(const w4a16_backward_term *terms, int count, bool gated, b
   for (int i = 0; i < count; ++i) {
     const int sums = gated ? (terms[0].dbias ? 1 : 0) + (terms[1].dbias ? 1 : 0)
                            : (terms[i].dbias ? 1 : 0);
-    const size_t n = w4a16::grad_workspace_bytes((int)M, (int)terms[i].N, sums,
-                                                 gated || terms[i].act != W4A16_ACT_NONE);
+    const size_t n = w4a16::grad_workspace_bytes((int)M, (int)terms[i].N, sums);
     need = n > need ? n : need;
   }
   return need;

@@ -104,9 +104,9 @@ __global__ __launch_bounds__(256) void transpose_meta_kernel(const _Float16 *sca
 // meet in LDS, so the sums do not depend on scheduling.
 // Bound by HBM: one read of dY and the pre-activations, one write of dZ.
 // COLS columns per workgroup, 2048 / COLS rows at a time: 512 and 4, or, for
-// column sums of few rows (one_strip), 64 and 32, where one strip is all
+// column sums of few rows (one_strip), 32 and 64, where one strip is all
 // rows and its sums are the result: no partial sums and no second launch.
-constexpr int kGradCols = 512, kOneStripCols = 64;
+constexpr int kGradCols = 512, kOneStripCols = 32;
 struct GradArgs {
   const void *dY, *z, *u;      // z, u: pre-activations (null: dZ = dY, not written)
   void *dz, *du;
@@ -118,19 +118,36 @@ struct GradArgs {
 template <bool BF, bool GATED, int COLS>
 __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
   constexpr int kAcross = COLS / 8, kRows = 256 / kAcross;  // threads along a row, rows at a time
+  constexpr int kParts = COLS < 256 ? 256 / COLS : 1;       // of the rows, in the sum over row lanes
   const int strip = (int)blockIdx.x / a.col_blocks;
   const int col0 = ((int)blockIdx.x - strip * a.col_blocks) * COLS;
   const int x8 = (int)threadIdx.x % kAcross * 8, n = col0 + x8;
   const int lane_row = threadIdx.x / kAcross;
   const int m1 = min(a.M, (strip + 1) * a.rows);
   float s0[8] = {0, 0, 0, 0, 0, 0, 0, 0}, s1[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  if (n < a.N) {
+  if (n < a.N && !GATED && !a.dz) {  // column sums alone: up to eight loads in flight
+    constexpr int kAtOnce = 8;
+    for (int m = strip * a.rows + lane_row; m < m1; m += kAtOnce * kRows) {
+      u32x4 d[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        d[k] = u32x4{0, 0, 0, 0};
+        if (m + k * kRows < m1)
+          d[k] = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.dY) +
+                                                  (size_t)(m + k * kRows) * a.N + n);
+      }
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s0[j] += act_to_f32<BF>((uint16_t)(d[k][j / 2] >> (16 * (j & 1))));
+    }
+  } else if (n < a.N) {
 #pragma unroll 2
     for (int m = strip * a.rows + lane_row; m < m1; m += kRows) {
       const size_t at = (size_t)m * a.N + n;
       const u32x4 d = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.dY) + at);
-      u32x4 z = d, u = d, oz, ou;
-      if (a.z) z = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.z) + at);
+      u32x4 u = d, oz, ou;
+      const u32x4 z = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.z) + at);
       if (GATED) u = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.u) + at);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -139,7 +156,7 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
         for (int h = 0; h < 2; ++h) {
           const float dy = act_to_f32<BF>((uint16_t)(d[q] >> (16 * h)));
           const float zv = act_to_f32<BF>((uint16_t)(z[q] >> (16 * h)));
-          float dz = a.z ? dy * act_grad(zv, a.act) : dy;
+          float dz = dy * act_grad(zv, a.act);
           if (GATED) {
             const float du = dy * act_value(zv, a.act);
             dz *= act_to_f32<BF>((uint16_t)(u[q] >> (16 * h)));
@@ -152,7 +169,7 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
         oz[q] = wz;
         ou[q] = wu;
       }
-      if (a.dz) *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(a.dz) + at) = oz;
+      *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(a.dz) + at) = oz;
       if (GATED) *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(a.du) + at) = ou;
     }
   }
@@ -162,6 +179,14 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) red[lane_row][x8 + j] = s[j];
     __syncthreads();
+    if constexpr (kParts > 1) {  // kRows / kParts rows each, in order, into the first of them
+      const int x = (int)threadIdx.x % COLS, i0 = (int)threadIdx.x / COLS * (kRows / kParts);
+      float sum = red[i0][x];
+#pragma unroll
+      for (int i = 1; i < kRows / kParts; ++i) sum += red[i0 + i][x];
+      red[i0][x] = sum;
+      __syncthreads();
+    }
     for (int x = threadIdx.x; x < COLS; x += 256) {
       float sum;
       if constexpr (kRows == 4) {
@@ -169,7 +194,7 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
       } else {
         sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) sum += red[i][x];
+        for (int i = 0; i < kRows; i += kRows / kParts) sum += red[i][x];
       }
       if (col0 + x < a.N) part[(size_t)strip * a.N + col0 + x] = sum;
     }
@@ -546,10 +571,11 @@ __global__ __launch_bounds__(256) void dx_reduce_kernel(DxArgs P) {
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 // Column sums of few rows: one strip, without a second launch.  Measured in us
-// (bf16, 14336 columns), strips against one: no activation, M = 200 7.0 and 4.2,
-// M = 384 7.2 and 6.9, M = 512 7.1 and 9.5; SiLU, M = 128 8.8 and 6.4, M = 200 9.2
-// and 11.9; gated, M = 64 10.2 and 6.0, M = 128 11.7 and 11.1, M = 200 14.9 and 16.9.
-bool one_strip(int M, bool sums, bool act) { return sums && M <= (act ? 128 : 256); }
+// per call (bf16, 14336 columns), strips against one: no activation, M = 200 6.5
+// and 3.9, M = 512 6.8 and 6.4, M = 1024 8.3 and 10.8; SiLU, M = 128 6.8 and 5.3,
+// M = 256 8.4 and 7.8, M = 512 11.5 and 12.6; gated, M = 64 9.7 and 5.2, M = 256
+// 13.8 and 11.9, M = 512 19.6 and 20.7.
+bool one_strip(int M, bool sums) { return sums && M <= 256; }
 
 // Rows per strip of grad_kernel: 32, fewer while the launch has under 512
 // workgroups (each is 256 threads: two per CU), more where column sums are
@@ -651,14 +677,14 @@ hipError_t launch_transpose(const void *Wq, const void *scales, const void *zero
   return hipGetLastError();
 }
 
-size_t grad_workspace_bytes(int M, int N, int sums, bool act) {
-  if (!sums || one_strip(M, true, act)) return 0;
+size_t grad_workspace_bytes(int M, int N, int sums) {
+  if (!sums || one_strip(M, true)) return 0;
   return sums * align256((size_t)strips_of(M, N, true) * N * sizeof(float));
 }
 
 hipError_t launch_grad(const GradDesc &d, void *workspace, hipStream_t stream) {
   const bool gated = d.u != nullptr, sums = d.db || d.db2;
-  const bool one = d.M > 0 && one_strip(d.M, sums, d.z != nullptr);
+  const bool one = d.M > 0 && one_strip(d.M, sums);
   const int strips = d.M == 0 ? 0 : one ? 1 : strips_of(d.M, d.N, sums);
   GradArgs a = {d.dY, d.z, d.u, d.dz, d.du, nullptr, nullptr, d.M, d.N, 0, 0, d.act};
   char *ws = static_cast<char *>(workspace);

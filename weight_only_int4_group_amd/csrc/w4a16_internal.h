@@ -103,14 +103,14 @@ hipError_t launch_transpose(const void *Wq, const void *scales, const void *zero
 // Gradients of an epilogue: dz = dY * act'(z) and, when u is set, gated: dz =
 // dY * u * act'(z), du = dY * act(z).  z null: dz is dY (not written).  db, db2:
 // fp32 column sums of dz and du (null: not wanted), which take
-// grad_workspace_bytes(M, N, how many, whether z is set) of workspace.
+// grad_workspace_bytes(M, N, how many) of workspace.
 struct GradDesc {
   const void *dY, *z, *u;
   void *dz, *du, *db, *db2;
   int M, N, act;
   bool bf16;
 };
-size_t grad_workspace_bytes(int M, int N, int sums, bool act);
+size_t grad_workspace_bytes(int M, int N, int sums);
 hipError_t launch_grad(const GradDesc &d, void *workspace, hipStream_t stream);
 
 // dX = add + s * sum over the terms of dZ . D (M >= 1, validated by the caller;
