@@ -433,7 +433,7 @@ int w4a16_transpose(const void *Wq, const void *scales, const void *zeros, int64
 /* Backward of one linear layer with frozen (packed) weights:
  *   dZ = dY * act'(Z),   dbias = sum over rows of dZ.
  * dY [M][N]; Z = preact [M][N] as the forward kept it, and dZ [M][N] output
- * (it may be the same term's dY or preact, where no other term reads that),
+ * (it may be the same term's dY or preact, where nothing else reads that),
  * both required unless act is W4A16_ACT_NONE, where dZ is dY and both must be
  * NULL; dbias: fp32 [N], or NULL.  dZ is rounded once to the activations' type, and the product below
  * reads the rounded values; dbias sums the unrounded ones in fp32, in a fixed
@@ -457,9 +457,10 @@ typedef struct w4a16_backward_term {
  * W4A16_DTYPE_*); sums are fp32, s and add are applied in fp32, and dX is
  * rounded once.  Outlier weights have no transposed form.  All terms share
  * wbits (EUNSUPPORTED otherwise).  M >= 0, dX may be NULL to get only dZ and
- * dbias.  Outputs must not overlap each other or any input except as said
- * (EINVAL where two terms' dZ or dbias overlap, or a dZ or dX what another term
- * or the product reads).
+ * dbias.  The outputs (dX, every dZ and dbias) must not overlap each other or
+ * any input of the call, of whichever term (EINVAL), except that a dZ may start
+ * exactly where its own term's dY or preact does and dX where add does: dZ is
+ * not written into a dY that is also add, or that another term reads.
  * workspace: w4a16_linear_backward_workspace_size() bytes (depends on M, K,
  * dtype and the terms' N, wbits and whether dbias is set; may be 0), 256-byte
  * aligned; EINVAL if smaller than this call needs.  Asynchronous on `stream`. */
@@ -473,8 +474,8 @@ int w4a16_linear_backward(const w4a16_backward_term *terms, int count, const voi
  *   dG = dH * U * act'(G),  dU = dH * act(G),  dX = add + s * (dG . Dg + dU . Du),
  * dbias_gate and dbias_up the fp32 sums over rows of dG and dU.  gate and up carry
  * Wt, meta, N, wbits and dbias (or NULL) of the two weights, preact = G or U,
- * and dZ = the output for dG or dU (each may be the same term's preact); the
- * gate's act is the block's (act must be 0 in up) and both dY are ignored.
+ * and dZ = the output for dG or dU (each may be the same term's preact, or one
+ * of them dH where add is not dH); the gate's act is the block's (act must be 0 in up) and both dY are ignored.
  * Everything else as w4a16_linear_backward. */
 int w4a16_gated_backward_workspace_size(const w4a16_backward_term *gate,
                                         const w4a16_backward_term *up, int64_t M, int64_t K,

@@ -168,6 +168,66 @@ def test_gated_backward_refuses_outputs_over_what_is_still_read():
     assert gated_backward_rc(G, dict(preact=C, dZ=C), dH=D, dX=C) == -1
 
 
+# Every buffer of a call of two terms in a megabyte of its own; M = 4, N = 128 and 256, K = 256.
+AT = {n: (i + 8) << 20 for i, n in enumerate(
+    ("dY0", "preact0", "dZ0", "dbias0", "Wt0", "meta0", "dY1", "preact1", "dZ1", "dbias1", "Wt1", "meta1",
+     "s", "add", "dX", "ws"))}
+OUTPUTS = ("dZ0", "dbias0", "dZ1", "dbias1", "dX")
+IN_PLACE = {("dZ0", "dY0"), ("dZ0", "preact0"), ("dZ1", "dY1"), ("dZ1", "preact1"), ("dX", "add")}
+
+
+def two_terms(at, M=4, act=2):
+    n = {i: {f: at[f + str(i)] for f in ("dY", "preact", "dZ", "dbias", "Wt", "meta")} for i in (0, 1)}
+    return backward_rc(count=2, terms=[term(N=128, act=act, **n[0]), term(N=256, act=act, **n[1])], s=at["s"],
+                       add=at["add"], dX=at["dX"], M=M, K=256, ws=at["ws"])
+
+
+@pytest.mark.parametrize("out", OUTPUTS)
+@pytest.mark.parametrize("other", [n for n in AT if n != "ws"])
+def test_backward_refuses_every_overlap(out, other):
+    """An output at, inside or around another buffer of the call; only the named pairs may
+    share an address (those run on the GPU)."""
+    if out == other:
+        return
+    for offset in (0, 64, -64):
+        if offset == 0 and (out, other) in IN_PLACE:
+            continue
+        assert two_terms({**AT, out: AT[other] + offset}) == -1, offset
+
+
+def test_backward_refuses_a_dZ_into_a_dY_that_is_added():
+    """The gradient of Y = X + act(X . W^T + b): add is dY, so dZ may not replace it."""
+    assert backward_rc(dX=E, add=A, K=128, t=dict(dY=A, preact=B, dZ=A, N=128, Wt=C, meta=D)) == -1
+    assert two_terms({**AT, "dZ0": AT["dY0"], "add": AT["dY0"]}) == -1
+    assert two_terms({**AT, "dZ1": AT["preact1"], "add": AT["preact1"]}) == -1
+
+
+def test_backward_of_no_rows_refuses_sums_over_inputs():
+    """M = 0 still writes the bias gradients (zeros)."""
+    for other in ("s", "Wt0", "meta1", "dbias1"):
+        assert two_terms({**AT, "dbias0": AT[other]}, M=0) == -1
+
+
+def test_gated_backward_refuses_every_overlap():
+    at = {**AT, "dH": 64 << 20}
+
+    def rc(at):
+        g = term(dY=None, N=256, **{f: at[f + "0"] for f in ("preact", "dZ", "dbias", "Wt", "meta")})
+        u = term(dY=None, N=256, act=0, **{f: at[f + "1"] for f in ("preact", "dZ", "dbias", "Wt", "meta")})
+        return w4.lib().w4a16_gated_backward(at["dH"], ctypes.byref(g), ctypes.byref(u), at["s"], at["add"],
+                                             at["dX"], 4, 256, 0, at["ws"], 1 << 20, None)
+    for out in OUTPUTS:
+        for other in at:
+            if other in (out, "ws", "dY0", "dY1"):
+                continue
+            for offset in (0, 64, -64):
+                if offset == 0 and ((out, other) in IN_PLACE or (out[:2], other) == ("dZ", "dH")):
+                    continue
+                assert rc({**at, out: at[other] + offset}) == -1, (out, other, offset)
+    assert rc({**at, "dZ0": at["dH"], "add": at["dH"]}) == -1
+    assert rc({**at, "dZ0": at["dH"], "dZ1": at["dH"]}) == -1
+
+
 def test_backward_workspace_sizes():
     L, n = w4.lib(), ctypes.c_size_t()
 

@@ -497,6 +497,25 @@ def test_backward_in_place(M):
     run_gated_backward(M, 272, 640, "bf16", "gelu", bias=True, inplace=True)
 
 
+@pytest.mark.parametrize("M", [9, 130, 300])
+def test_gated_backward_into_dH(M):
+    """dG, or dU, written where dH is: the bits of the call with buffers of their own."""
+    torch = torch_cuda()
+    N, K = 272, 640
+    gt, ut = (w4.w4a16_transpose(weight(k, N, K).pw) for k in (6, 8))
+    G, Up = act_array("bf16", 12, M, N)[0], act_array("bf16", 14, M, N)[0]
+    dH = act_array("bf16", 11, M, N, 0.25)[0]
+    want = w4.w4a16_gated_backward(dH, G, Up, gt, ut, bias_grad=True)
+    for which in (0, 1):
+        d, other, dX = dH.clone(), torch.empty_like(dH), torch.empty_like(want[0])
+        db = [torch.empty(N, device="cuda") for _ in range(2)]
+        note(f"gated backward into dH M={M} output {which}")
+        outs = (d, other) if which == 0 else (other, d)
+        w4.GatedBackwardCall(d, G, Up, gt, ut, None, dX, *outs, w4.ACT_SILU, None, *db)()
+        for a, b in zip(want, (dX, *outs, *db)):
+            assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("M", [1, 3, 16, 17, 33, 65, 129, 300])
 def test_gated_backward_every_tile_height(M, dtype):

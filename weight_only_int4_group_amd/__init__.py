@@ -780,7 +780,8 @@ class BackwardTerm:
 class LinearBackwardCall(_PreparedCall):
     """A prepared w4a16_linear_backward call: dX = add + s * sum over the terms of dZ . D,
     and each term's dZ and dbias.  The terms (1 to 4 BackwardTerm) are the layers that read
-    the same X with the same s.  dX None: only dZ and dbias; add may be dX itself."""
+    the same X with the same s.  dX None: only dZ and dbias; add may be dX itself, and a dZ
+    its own term's dY or preact (where neither add nor another term is in that buffer)."""
 
     def __init__(self, terms, s, dX, add=None, stream=None, workspace=None):
         torch = _torch()
@@ -820,7 +821,8 @@ def w4a16_linear_backward(dY, wt: TransposedWeight, s=None, act=ACT_NONE, preact
 class GatedBackwardCall(_PreparedCall):
     """A prepared w4a16_gated_backward call: dG = dH * U * act'(G), dU = dH * act(G),
     dX = add + s * (dG . Dg + dU . Du), and the fp32 column sums of dG and dU.  dG may be G
-    and dU may be U; dX None: only dG, dU and the sums."""
+    and dU may be U, or one of them dH (where add is not dH); dX None: only dG, dU and the
+    sums."""
 
     def __init__(self, dH, G, U, gate: TransposedWeight, up: TransposedWeight, s, dX, dG, dU,
                  act=ACT_SILU, add=None, dbias_gate=None, dbias_up=None, stream=None,

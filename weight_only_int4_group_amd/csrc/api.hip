@@ -1,6 +1,7 @@
 // C-ABI front end: argument validation (host only, before any HIP call),
 // kernel choice by M, and launches on the caller's stream.
 #include <functional>
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 
@@ -818,38 +819,58 @@ int check_backward_pointers(const w4a16_backward_term &t, bool gated, bool dx, i
   return W4A16_OK;
 }
 
-bool overlap(const void *a, size_t na, const void *b, size_t nb) {
-  const char *x = static_cast<const char *>(a), *y = static_cast<const char *>(b);
-  return x && y && std::less<const char *>()(x, y + nb) && std::less<const char *>()(y, x + na);
+struct Range {
+  const void *p;
+  size_t n;
+};
+
+bool overlap(const Range &a, const Range &b) {
+  if (!a.p || !b.p || a.n == 0 || b.n == 0) return false;
+  const char *x = static_cast<const char *>(a.p), *y = static_cast<const char *>(b.p);
+  return std::less<const char *>()(x, y + b.n) && std::less<const char *>()(y, x + a.n);
 }
 
-// dX is formed after every dZ, from all of them, and the terms' dZ one after
-// the other: a dZ or dX over what another term or the product still reads would
-// give wrong sums.
-bool backward_overlaps(const w4a16_backward_term *terms, int count, const void *dX, int64_t M,
-                       int64_t K) {
+// An output that may also be exactly the input it replaces, element by element.
+bool overlap_but_same(const Range &out, const Range &in) { return out.p != in.p && overlap(out, in); }
+
+// The kernels of a call run in order (the terms' dZ and dbias one after the
+// other, then dX from all of them, s and add): an output over another output or
+// over an input that a workgroup, or a kernel after it, still reads would give
+// wrong sums.  Only an output at the very address of an input is safe, where
+// the same thread reads each element before it writes it: dZ at its own term's dY
+// (dH: of either) or preact, dX at add.  dH: of a gated call, or null.
+bool backward_overlaps(const w4a16_backward_term *terms, int count, const void *dH, const void *s,
+                       const void *add, const void *dX, int64_t M, int64_t K) {
+  const Range x = {dX, (size_t)(M * K) * 2}, r_add = {add, x.n}, r_s = {s, (size_t)K * 2};
+  if (overlap(x, r_s) || overlap_but_same(x, r_add)) return true;
   for (int i = 0; i < count; ++i) {
-    const size_t n = (size_t)(M * terms[i].N) * 2;
-    const void *read[2] = {terms[i].dY, terms[i].preact};
-    if (overlap(dX, (size_t)(M * K) * 2, terms[i].dZ, n)) return true;
-    for (const void *r : read)
-      if (overlap(dX, (size_t)(M * K) * 2, r, n)) return true;
-    for (int j = 0; j < count; ++j) {
-      if (i == j) continue;
-      const size_t nj = (size_t)(M * terms[j].N) * 2;
-      if (overlap(terms[j].dZ, nj, terms[i].dZ, n) ||
-          overlap(terms[j].dbias, (size_t)terms[j].N * 4, terms[i].dbias, (size_t)terms[i].N * 4))
-        return true;
-      for (const void *r : read)
-        if (overlap(terms[j].dZ, nj, r, n)) return true;
+    const int64_t N = terms[i].N, NG = (N + W4A16_GROUP - 1) / W4A16_GROUP;
+    const size_t mn = (size_t)(M * N) * 2;
+    const Range dz = {terms[i].dZ, mn}, db = {terms[i].dbias, (size_t)N * 4};
+    const Range dy = {dH ? dH : terms[i].dY, mn}, pre = {terms[i].preact, mn};
+    const Range wt = {terms[i].Wt, (size_t)(NG * W4A16_GROUP * K / (terms[i].wbits == 8 ? 1 : 2))};
+    const Range meta = {terms[i].meta, (size_t)(NG * (K / W4A16_GROUP) * 512)};
+    for (const Range &in : {dy, pre, wt, meta, dz, db})
+      if (overlap(x, in)) return true;
+    if (overlap(dz, r_s) || overlap(dz, r_add) || overlap(db, r_s) || overlap(db, r_add)) return true;
+    for (int j = 0; j < count; ++j) {  // term j's outputs against what term i reads and writes
+      const size_t mnj = (size_t)(M * terms[j].N) * 2;
+      const Range dzj = {terms[j].dZ, mnj}, dbj = {terms[j].dbias, (size_t)terms[j].N * 4};
+      for (const Range &in : {dy, pre, wt, meta, dz})
+        if (overlap(dbj, in)) return true;
+      if (overlap(dzj, wt) || overlap(dzj, meta)) return true;
+      if (i != j && (overlap(dzj, dz) || overlap(dbj, db) || overlap(dzj, pre))) return true;
+      if (i == j && overlap_but_same(dzj, pre)) return true;
+      if (i == j || dH ? overlap_but_same(dzj, dy) : overlap(dzj, dy)) return true;
     }
   }
   return false;
 }
 
-int check_backward_common(const w4a16_backward_term *terms, int count, bool gated, const void *s,
-                          const void *add, const void *dX, int64_t M, int64_t K, int dtype,
-                          const void *workspace, size_t workspace_bytes) {
+// dH: the gated call's (terms[].dY are ignored there), null for a linear call
+int check_backward_common(const w4a16_backward_term *terms, int count, bool gated, const void *dH,
+                          const void *s, const void *add, const void *dX, int64_t M, int64_t K,
+                          int dtype, const void *workspace, size_t workspace_bytes) {
   for (int i = 0; i < count; ++i) {
     const int rc = check_backward_pointers(terms[i], gated, dX != nullptr, M);
     if (rc) return rc;
@@ -859,7 +880,7 @@ int check_backward_common(const w4a16_backward_term *terms, int count, bool gate
   const size_t need = backward_bytes(terms, count, gated, dX != nullptr, M, K, dtype);
   if (need > 0 && (!workspace || workspace_bytes < need)) return W4A16_EINVAL;
   if (workspace && !aligned256(workspace)) return W4A16_EALIGN;
-  return M > 0 && backward_overlaps(terms, count, dX, M, K) ? W4A16_EINVAL : W4A16_OK;
+  return backward_overlaps(terms, count, dH, s, add, dX, M, K) ? W4A16_EINVAL : W4A16_OK;
 }
 
 }  // namespace
@@ -903,7 +924,8 @@ int w4a16_linear_backward(const w4a16_backward_term *terms, int count, const voi
                           void *workspace, size_t workspace_bytes, void *stream) {
   int rc = check_backward_shape(terms, count, M, K, dtype);
   if (rc) return rc;
-  rc = check_backward_common(terms, count, false, s, add, dX, M, K, dtype, workspace, workspace_bytes);
+  rc = check_backward_common(terms, count, false, nullptr, s, add, dX, M, K, dtype, workspace,
+                             workspace_bytes);
   if (rc) return rc;
   hipStream_t st = static_cast<hipStream_t>(stream);
   const void *dZ[w4a16::kMaxDxTerms] = {};
@@ -945,7 +967,7 @@ int w4a16_gated_backward(const void *dH, const w4a16_backward_term *gate,
   if (up->act != W4A16_ACT_NONE) return W4A16_EINVAL;
   if (!dH && M > 0) return W4A16_EINVAL;
   if (!aligned16(dH)) return W4A16_EALIGN;
-  rc = check_backward_common(terms, 2, true, s, add, dX, M, K, dtype, workspace, workspace_bytes);
+  rc = check_backward_common(terms, 2, true, dH, s, add, dX, M, K, dtype, workspace, workspace_bytes);
   if (rc) return rc;
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (M > 0 || gate->dbias || up->dbias) {
