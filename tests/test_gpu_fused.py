@@ -363,6 +363,74 @@ def test_extreme_pre_activations():
             assert (np.abs(got[:, down]) <= 1e-30).all()
 
 
+# Pre-activations from far in the lower tail on, where an activation is all tail: past them
+# its values leave the normal range of fp32 (and bf16).
+TAIL = {"silu": -80.0, "gelu": -12.5, "gelu_tanh": -9.4}
+
+
+def tail_points(dtype, act, n):
+    """n pre-activations from the tail to 6: (device tensor [n], fp64 values)."""
+    torch = torch_cuda()
+    z = np.linspace(TAIL[act], 6.0, n).astype(np.float32)
+    if dtype == "fp16":
+        return to_dev(z.astype(np.float16)), z.astype(np.float16).astype(np.float64)
+    b = to_bf16_bits(z)
+    return to_dev(b.view(np.int16)).view(torch.bfloat16), bf16_bits_to_f64(b)
+
+
+def tail_eps(z, act):
+    """Relative error of the activation's factor (sigmoid or normal distribution function) in
+    fp32: 2^-19 for its dozen roundings and the fits, reciprocal and exponential (at most
+    2^-21 each), and the exponential's argument a, which a relative rounding of k 2^-24 moves by
+    k |a| 2^-24: z^2 / 2 (one rounding, one more in the change of base), z (one), and
+    sqrt(8 / pi) (z + 0.044715 z^3) (four)."""
+    a = {"silu": np.abs(z), "gelu": z * z / 2,
+         "gelu_tanh": 1.6 * np.abs(z + 0.044715 * z ** 3)}[act]
+    return 2.0 ** -19 + a * (8 if act == "gelu_tanh" else 4) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("M", [3, 40])
+@pytest.mark.parametrize("act", list(TAIL))
+def test_activations_keep_their_relative_precision(act, M, dtype):
+    """X = 0, so Z is the bias without a rounding: Y (and H with U = 1) within one rounding of
+    act(Z), relative to act(Z) itself."""
+    torch = torch_cuda()
+    N, K = 1008, 128
+    note(f"tail of {act} M={M} {dtype}")
+    w = weight(1, N, K)
+    b, z = tail_points(dtype, act, N)
+    X = torch.zeros(M, K, dtype=b.dtype, device="cuda")
+    ref, u = of.act(z, act), U[dtype]
+    bound = (u + 2 * tail_eps(z, act)) * np.abs(ref) + (TINY if dtype == "fp16" else 0.0)
+    for got in (w4.w4a16_linear(X, w.pw, bias=b, act=ACT[act]),
+                w4.w4a16_gated(X, w.pw, w.pw, act=ACT[act], bias_gate=b, bias_up=torch.ones_like(b))):
+        bad = np.abs(values(got) - ref) > bound
+        assert not bad.any(), (z[np.nonzero(bad)[1][:4]], (np.abs(values(got) - ref) / np.abs(ref)).max())
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("act", list(TAIL))
+def test_derivatives_keep_their_relative_precision(act, dtype):
+    """dZ of dY = 1 in the tail: act' = f + z f' with the factor f and its derivative, each to
+    the factor's relative error (f' = f (1 - f) u' too, where 1 - f is within 2^-23)."""
+    torch = torch_cuda()
+    N, K, M = 1008, 128, 3
+    note(f"tail of {act}' {dtype}")
+    wt = w4.w4a16_transpose(weight(1, N, K).pw)
+    zt, z = tail_points(dtype, act, N)
+    Z = zt.expand(M, N).contiguous()
+    dZ, one = torch.empty_like(Z), torch.ones_like(Z)
+    w4.LinearBackwardCall([w4.BackwardTerm(one, wt, ACT[act], Z, dZ)], None, None)()
+    ref, u = of.act_grad(z, act), U[dtype]
+    f = of.act(z, act) / np.where(z == 0, 1.0, z)
+    size = f + np.abs(ref - f) + np.abs(z) * f * {"silu": 1.0, "gelu": 0.0, "gelu_tanh":
+                                                  1.6 * (1 + 3 * 0.044715 * z * z)}[act]
+    bound = u * np.abs(ref) + 2 * tail_eps(z, act) * size + (TINY if dtype == "fp16" else 0.0)
+    bad = np.abs(values(dZ) - ref) > bound
+    assert not bad.any(), (z[np.nonzero(bad)[1][:4]], (np.abs(values(dZ) - ref) / bound).max())
+
+
 # ---- backward -----------------------------------------------------------------------
 
 def eval_bound(dY, z, extra=0.0):
