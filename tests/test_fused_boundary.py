@@ -259,6 +259,22 @@ def test_binding_refusals():
     w4.LinearCall([])()                                             # nothing to do
 
 
+def test_binding_refuses_tensors_whose_gradient_would_be_lost():
+    import torch
+    x = torch.zeros(2, 128, dtype=torch.float16, requires_grad=True)
+    y = torch.zeros(2, 16, dtype=torch.float16, requires_grad=True)
+    pw, wt = w4.PackedWeight(None, None, None, 16, 128), w4.TransposedWeight(None, None, 16, 128)
+    calls = (lambda: w4.LinearCall([(x, pw, None, y, w4.Epilogue())]),
+             lambda: w4.GatedCall(x, pw, pw, None, y),
+             lambda: w4.LinearBackwardCall([w4.BackwardTerm(y, wt)], None, x),
+             lambda: w4.GatedBackwardCall(y, y, y, wt, wt, None, x, y, y))
+    for call in calls:
+        with pytest.raises(ValueError, match="requires grad"):
+            call()
+        with torch.no_grad(), pytest.raises(TypeError):              # not a device tensor
+            call()
+
+
 @pytest.mark.parametrize("source", ["backward.hip"])
 def test_backward_kernels_keep_everything_in_registers(source, tmp_path):
     kernels = _kernel_metadata(_device_asm(source, tmp_path))

@@ -738,6 +738,50 @@ def test_binding_refuses_views_types_and_shapes():
                       workspace=small)
 
 
+def test_tensors_that_require_grad():
+    """Refused in grad mode, whichever it is; taken under no_grad and inside an
+    autograd.Function, whose gradients are the formulas'."""
+    torch = torch_cuda()
+    N, K, M = 48, 384, 6
+    w = weight(1, N, K)
+    wt = w4.w4a16_transpose(w.pw)
+    t = lambda *shape: torch.randn(*shape, generator=torch.Generator().manual_seed(5)).half().cuda()
+    X, b, R, Y, s = t(M, K), t(N), t(M, N), t(M, N), t(K).abs() + 0.5
+    for name, base in (("bias", b), ("residual", R), ("preact", Y), ("out", Y), ("s", s)):
+        with pytest.raises(ValueError, match="requires grad"):
+            w4.w4a16_linear(X, w.pw, **{name: base.clone().requires_grad_()})
+    for name in ("bias_gate", "bias_up"):
+        with pytest.raises(ValueError, match="requires grad"):
+            w4.w4a16_gated(X, w.pw, w.pw, **{name: b.clone().requires_grad_()})
+    with pytest.raises(ValueError, match="requires grad"):
+        w4.w4a16_linear_backward(R, wt, act=w4.ACT_SILU, preact=Y.clone().requires_grad_())
+    with pytest.raises(ValueError, match="requires grad"):
+        w4.w4a16_gated_backward(R, Y, Y.clone().requires_grad_(), wt, wt)
+
+    class Layer(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, bias):
+            z = torch.empty(M, N, dtype=x.dtype, device="cuda")
+            ctx.save_for_backward(z)
+            return w4.w4a16_linear(x, w.pw, bias=bias, act=w4.ACT_SILU, preact=z)
+
+        @staticmethod
+        def backward(ctx, dy):
+            dX, _, db = w4.w4a16_linear_backward(dy.contiguous(), wt, act=w4.ACT_SILU,
+                                                 preact=ctx.saved_tensors[0], bias_grad=True)
+            return dX, db.half()
+    note("autograd.Function of a layer")
+    x, bias = X.clone().requires_grad_(), b.clone().requires_grad_()
+    Layer.apply(x, bias).backward(R)
+    with torch.no_grad():
+        assert torch.equal(Layer.apply(x, bias), w4.w4a16_linear(x, w.pw, bias=bias, act=w4.ACT_SILU))
+    z = values(X) @ w.W.T + values(b)
+    dz = of.linear_grad(values(R), z, "silu")
+    # z is rounded once before its derivative, dZ once before the product
+    assert errors(values(x.grad), of.input_grad([dz], [w.W]))[0] <= 5 * REL["fp16"]
+    assert errors(values(bias.grad), dz.sum(0))[0] <= 5 * REL["fp16"]
+
+
 # ---- together -----------------------------------------------------------------------
 
 @pytest.mark.parametrize("M", [5, 70])

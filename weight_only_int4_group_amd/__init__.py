@@ -538,11 +538,21 @@ def w4a16_spec_verify(p_target, p_draft, draft, u_accept, u_sample, out=None, wo
 
 # ---- fused linear layers and their backward passes -------------------------------------
 
+def _refuse_grad(t, name):
+    """These calls record no graph: a tensor whose gradient autograd expects would lose it
+    without a word.  (An autograd.Function's forward and backward run without grad mode.)"""
+    if t.requires_grad and _torch().is_grad_enabled():
+        raise ValueError(f"{name} requires grad, and the fused calls record no graph: call them "
+                         "from an autograd.Function (forward here, backward through the "
+                         "*_backward calls) or under torch.no_grad()")
+
+
 def _act_dtype(t, name):
     """The activations' type of tensor t: torch.float16 or torch.bfloat16."""
     torch = _torch()
     if not isinstance(t, torch.Tensor) or t.dtype not in (torch.float16, torch.bfloat16):
         raise TypeError(f"{name} must be a float16 or bfloat16 tensor")
+    _refuse_grad(t, name)
     return t.dtype
 
 
@@ -559,6 +569,7 @@ def _shaped_ptr(t, name, dtype, shape, device):
     p = _dev_ptr(t, name, dtype)
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
+    _refuse_grad(t, name)
     return p
 
 
@@ -673,7 +684,9 @@ class LinearCall(_PreparedCall):
 def w4a16_linear(X, pw: PackedWeight, s=None, bias=None, act=ACT_NONE, residual=None, out=None,
                  preact=None):
     """Y = residual + act(X . dequant(pw)^T + bias) on the current stream; X fp16 or bf16
-    [M][K].  preact, when given, receives the pre-activation for a backward pass."""
+    [M][K].  preact, when given, receives the pre-activation for a backward pass.  Like all
+    fused calls it is not differentiable by itself: in grad mode a tensor that requires grad
+    is refused (w4a16_linear_backward gives the gradients)."""
     if out is None:
         out = _torch().empty((X.shape[0], pw.N), dtype=X.dtype, device=X.device)
     LinearCall([(X, pw, s, out, Epilogue(bias, act, residual, preact))])()
