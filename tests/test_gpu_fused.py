@@ -326,6 +326,79 @@ def test_linear_group_of_layers(M, K):
         close(values(Y), ref, bound, f"group M={M}", 5 * REL[dtype])
 
 
+def run_problems(specs, workspace=True):
+    """One w4a16_linear call over (M, N, K, dtype, bits, outliers) problems, each with an
+    activation, bias, residual and pre-activation output of its own, each checked."""
+    torch = torch_cuda()
+    items, checks = [], []
+    for i, (M, N, K, dtype, bits, count) in enumerate(specs):
+        act, w = of.ACTS[(i + 1) % 5], weight(60 + i, N, K, i % 2 == 0, bits, count)
+        X, Xv = act_array(dtype, 100 + i, M, K)
+        b, bv = act_array(dtype, 120 + i, 1, N, 0.5)
+        R, Rv = act_array(dtype, 140 + i, M, N) if i % 3 != 1 else (None, None)
+        (Y, buf), (Z, zbuf) = guarded(dtype, M, N), guarded(dtype, M, N)
+        b, bv = (b.reshape(N), bv.reshape(N)) if i % 4 != 2 else (None, None)
+        items.append((X, w.pw, w.sd, Y, w4.Epilogue(b, ACT[act], R, Z if i % 2 else None)))
+        checks.append((w, Xv, bv, act, Rv, buf, zbuf if i % 2 else None))
+    note(f"problems {specs} ws={workspace}")
+    call = w4.LinearCall(items)
+    if not workspace:
+        call.args = (*call.args[:-2], None, 0)
+    call()
+    for (X, _, _, Y, e), (w, Xv, bv, act, Rv, buf, zbuf), (M, N, K, dtype, bits, count) in zip(
+            items, checks, specs):
+        u, tag = U[dtype], f"problem {M}x{N}x{K} {dtype} {bits} {count} {act}"
+        ref, z = of.linear(Xv, w.W, bv, act, Rv)
+        ez = product_bound(Xv, w.W, u, K)
+        ey = act_bound(z, ez) if act != "none" else ez
+        check_guard(buf, M)
+        close(values(Y), ref, ey + u * np.abs(ref) + u * ey + TINY, tag, 5 * REL[dtype])
+        if zbuf is not None:
+            check_guard(zbuf, M)
+            close(values(e.preact), z, ez + u * np.abs(z) + u * ez + TINY, tag + " Z", REL[dtype])
+
+
+@pytest.mark.parametrize("workspace", [True, False])
+@pytest.mark.parametrize("specs", [
+    # rows of different lengths in one launch, the longest last: cut into ranges of K beside a
+    # problem that is stored directly, and (without a workspace, or too long for ranges) windows
+    [(5, 48, 640, "fp16", 4, 0), (5, 272, 4224, "fp16", 4, 0), (5, 48, 14464, "fp16", 4, 0)],
+    [(5, 48, 640, "bf16", 4, 0), (5, 272, 4224, "bf16", 4, 0), (5, 48, 14464, "bf16", 4, 0)],
+    [(16, 48, 640, "bf16", 4, 0), (16, 80, 4224, "bf16", 4, 0)],
+    [(16, 48, 640, "fp16", 8, 0), (16, 80, 4224, "fp16", 8, 0), (3, 16, 14464, "fp16", 8, 0)],
+    # a problem with outliers beside one without
+    [(5, 48, 640, "fp16", 4, 300), (5, 272, 4224, "fp16", 4, 0)],
+    [(16, 48, 640, "bf16", 4, 300), (16, 48, 4224, "bf16", 4, 0), (16, 48, 640, "bf16", 4, 0)],
+    # both activation types and code widths in one call: four launches share the workspace
+    [(16, 48, 4224, "fp16", 4, 0), (16, 48, 4224, "bf16", 4, 0), (16, 48, 4224, "fp16", 8, 0),
+     (16, 48, 4224, "bf16", 8, 0), (7, 272, 640, "fp16", 4, 0)],
+])
+def test_problems_of_different_kinds_streamed(specs, workspace):
+    run_problems(specs, workspace)
+
+
+@pytest.mark.parametrize("workspace", [True, False])
+@pytest.mark.parametrize("specs", [
+    # both paths in one call
+    [(3, 272, 640, "bf16", 4, 0), (40, 272, 640, "bf16", 4, 0), (16, 48, 640, "bf16", 4, 0),
+     (130, 48, 1152, "bf16", 4, 0)],
+    # tiled launches with a problem that is split beside one that is not (one group of K)
+    [(40, 48, 4224, "fp16", 4, 0), (130, 272, 128, "fp16", 4, 0), (17, 16, 4224, "fp16", 4, 0)],
+    [(40, 48, 4224, "bf16", 8, 0), (130, 272, 128, "bf16", 8, 0), (17, 16, 4224, "bf16", 8, 0)],
+    # outliers in one problem of a tiled launch, and a change of type and width in the middle
+    [(40, 48, 640, "fp16", 4, 0), (40, 272, 640, "fp16", 4, 900), (70, 48, 640, "fp16", 4, 0),
+     (70, 48, 640, "bf16", 4, 0), (40, 48, 640, "fp16", 8, 0), (40, 48, 640, "fp16", 4, 0)],
+])
+def test_problems_of_different_kinds_tiled(specs, workspace):
+    run_problems(specs, workspace)
+
+
+@pytest.mark.parametrize("M", [3, 40])
+def test_more_problems_than_a_launch_holds(M):
+    """Eleven problems: a second launch takes the last three, with their own epilogues."""
+    run_problems([(M, 16 * (i + 1), 128 * (1 + i % 4), "fp16", 4, 0) for i in range(11)])
+
+
 def test_empty_batch():
     torch = torch_cuda()
     w = weight(1, 48, 384)
@@ -429,6 +502,54 @@ def test_derivatives_keep_their_relative_precision(act, dtype):
     bound = u * np.abs(ref) + 2 * tail_eps(z, act) * size + (TINY if dtype == "fp16" else 0.0)
     bad = np.abs(values(dZ) - ref) > bound
     assert not bad.any(), (z[np.nonzero(bad)[1][:4]], (np.abs(values(dZ) - ref) / bound).max())
+
+
+EXTREMES = np.array([1e38, -1e38, 1e20, -1e20, 300.0, -300.0, 90.0, -90.0, 16.1, -16.1, 15.9, -15.9,
+                     np.inf, -np.inf, np.nan, 0.0], np.float32)
+
+
+def extreme_values(dtype, n):
+    """n values that cycle through EXTREMES (fp16: large ones become infinite)."""
+    torch = torch_cuda()
+    z = np.resize(EXTREMES, n)
+    if dtype == "fp16":
+        with np.errstate(over="ignore"):
+            h = z.astype(np.float16)
+        return to_dev(h), h.astype(np.float64)
+    b = to_bf16_bits(z)
+    return to_dev(b.view(np.int16)).view(torch.bfloat16), bf16_bits_to_f64(b)
+
+
+def check_extreme_act(got, z, dtype, act):
+    """act(z) at its limits: z or 0 to either side of 15; NaN stays NaN.  At minus infinity the
+    formulas are infinity times 0: 0 or NaN (relu: 0)."""
+    assert np.isnan(got[:, np.isnan(z)]).all()
+    up, down = z > 15, (z < -15) & np.isfinite(z)
+    # products with U = 1, sums with X = 0: one rounding of z, past the limit 1e-6 from gelu_tanh's factor
+    with np.errstate(invalid="ignore"):
+        near = np.abs(got[:, up] - z[up]) <= (U[dtype] + 1e-6) * np.abs(z[up])
+    assert (near | (got[:, up] == z[up])).all()
+    assert (np.abs(got[:, down]) <= (5e-6 if act == "silu" else 1e-30)).all()
+    assert (got[:, z == 0] == 0).all()
+    low = got[:, z == -np.inf]
+    assert ((low == 0) | (np.isnan(low) & (act != "relu"))).all()
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("M,K", [(3, 384), (20, 384), (5, 14464), (20, 4224)])
+@pytest.mark.parametrize("act", of.ACTS[1:])
+def test_activations_at_their_limits(act, M, K, dtype):
+    """Large, infinite and NaN pre-activations (X = 0 and such a bias), direct and out of K
+    ranges and split sums, in a linear and in a gated call."""
+    torch = torch_cuda()
+    N = 48
+    w = weight(1, N, K)
+    b, z = extreme_values(dtype, N)
+    X = torch.zeros(M, K, dtype=b.dtype, device="cuda")
+    note(f"limits of {act} M={M} K={K} {dtype}")
+    check_extreme_act(values(w4.w4a16_linear(X, w.pw, bias=b, act=ACT[act])), z, dtype, act)
+    check_extreme_act(values(w4.w4a16_gated(X, w.pw, w.pw, act=ACT[act], bias_gate=b,
+                                            bias_up=torch.ones_like(b))), z, dtype, act)
 
 
 # ---- backward -----------------------------------------------------------------------
@@ -563,6 +684,35 @@ def test_backward_in_place(M):
     run_linear_backward(M, 272, 640, "bf16", "silu", add=True, inplace=True)
     run_linear_backward(M, 1040, 256, "fp16", "gelu", add=True, bias=True, inplace=True)
     run_gated_backward(M, 272, 640, "bf16", "gelu", bias=True, inplace=True)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("M", [3, 300])
+@pytest.mark.parametrize("act", of.ACTS[1:])
+def test_derivatives_at_their_limits(act, M, dtype):
+    """act' is 1 above and 0 below the middle, without a NaN from a vanishing factor times an
+    overflowed one; NaN stays NaN, and at the infinities silu's and gelu's formulas are infinity
+    times 0 (1, 0 or NaN)."""
+    torch = torch_cuda()
+    N, K = 48, 128
+    wt = w4.w4a16_transpose(weight(1, N, K).pw)
+    zt, z = extreme_values(dtype, N)
+    Z = zt.expand(M, N).contiguous()
+    one = torch.ones_like(Z)
+    note(f"limits of {act}' M={M} {dtype}")
+    dZ, dG, dU = torch.empty_like(Z), torch.empty_like(Z), torch.empty_like(Z)
+    w4.LinearBackwardCall([w4.BackwardTerm(one, wt, ACT[act], Z, dZ)], None, None)()
+    w4.GatedBackwardCall(one, Z, one, wt, wt, None, None, dG, dU, ACT[act])()
+    got = values(dZ)
+    assert np.array_equal(got, values(dG), equal_nan=True)
+    check_extreme_act(values(dU), z, dtype, act)                 # dU = dH act(G)
+    assert np.isnan(got[:, np.isnan(z)]).all()
+    up, down = (z > 15) & np.isfinite(z), (z < -15) & np.isfinite(z)
+    assert (np.abs(got[:, up] - 1) <= U[dtype] + 1e-5).all()
+    assert (np.abs(got[:, down]) <= (5e-6 if act == "silu" else 1e-30)).all()
+    for inf, limit in ((np.inf, 1.0), (-np.inf, 0.0)):
+        at = got[:, z == inf]
+        assert ((at == limit) | (np.isnan(at) & (act in ("silu", "gelu")))).all()
 
 
 @pytest.mark.parametrize("M", [9, 130, 300])
