@@ -367,7 +367,11 @@ int w4a16_spec_verify(const void *p_target, const void *p_draft, const void *dra
  * them before they are stored, in the same kernels and on the same paths:
  *   Z = X . W_hat^T + bias,   Y = residual + act(Z).
  * The fp32 sums get bias, activation and residual in fp32 and Y is rounded to
- * the activations' type once.  An epilogue belongs to each problem: */
+ * the activations' type once.  The sums themselves round what w4a16_gemm's do: X * s
+ * once, and on the tiled path (M > 16) each dequantized weight once, both to the
+ * activations' type.  The activations are evaluated in fp32 with a relative error
+ * of at most 2^-14, in the lower tails too, down to where they leave fp32's normal
+ * range.  An epilogue belongs to each problem: */
 enum {
   W4A16_ACT_NONE = 0,
   W4A16_ACT_RELU = 1,      /* max(z, 0); derivative 0 at z = 0                   */
@@ -404,7 +408,8 @@ int w4a16_linear(const w4a16_problem *problems, const w4a16_epilogue *epilogues,
  * gate and up are the two products: same X, s, M, N, K, dtype and wbits (EINVAL
  * otherwise).  Their Y receive G and U, each rounded once, for a backward pass:
  * both set or both NULL.  H [M][N] is formed in fp32 from the unrounded sums
- * and rounded once.  H, the Y and the biases ([N] or NULL) are of the
+ * and rounded once; as a product of two sums it carries the roundings of both
+ * (relative L2 error against exact arithmetic about 1.7 times one rounding's).  H, the Y and the biases ([N] or NULL) are of the
  * activations' type and 16-byte aligned; outputs must not overlap each other
  * or any input.  The workspace is optional, as for w4a16_gemm_grouped_ws.
  * Asynchronous on `stream`. */

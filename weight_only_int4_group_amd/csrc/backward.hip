@@ -256,7 +256,10 @@ struct DxArgs {
 // A weight's dequantization: (q - z) exact in fp16, times the scale, rounded
 // once to fp16; bf16 takes the product in fp32 (v_fma_mix, exact: 8 + 11 bits)
 // and rounds it once: 5 instructions for two weights, where converting code
-// and scale to fp32 first would take 7.
+// and scale to fp32 first would take 7.  Both operands are rounded to the
+// activations' type because the MFMA takes 16-bit ones: dZ as it is stored, and D
+// with its scale, which varies along the contraction here and so cannot
+// multiply the fp32 sums instead.
 // N is split across workgroups when the output blocks leave CUs idle: fp32
 // partials, added in a fixed order by dx_reduce_kernel.
 // KS = 2: two slices of four waves each walk every other stage of the
@@ -570,11 +573,17 @@ __global__ __launch_bounds__(256) void dx_reduce_kernel(DxArgs P) {
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Column sums of few rows: one strip, without a second launch.  Measured in us
-// per call (bf16, 14336 columns), strips against one: no activation, M = 200 6.5
-// and 3.9, M = 512 6.8 and 6.4, M = 1024 8.3 and 10.8; SiLU, M = 128 6.8 and 5.3,
-// M = 256 8.4 and 7.8, M = 512 11.5 and 12.6; gated, M = 64 9.7 and 5.2, M = 256
-// 13.8 and 11.9, M = 512 19.6 and 20.7.
+// Column sums of few rows: one strip, without a second launch.  One limit for every
+// width and activation, below each of their crossovers.  Measured in us per call
+// (bf16), strips against one, with 14336 columns: no activation, M = 200 6.5 and 3.9,
+// M = 256 6.6 and 4.3; SiLU, M = 128 6.8 and 5.3, M = 256 8.4 and 7.8; gated, M = 64
+// 9.7 and 5.2, M = 256 13.8 and 11.9.  At the limit one strip is 0.2-2.8 us ahead in
+// all nine sweeps (4096, 14336 and 18944 columns; M = 200 of 18944 SiLU columns alone is
+// behind, 9.7 against 9.4).  Past it the sides part: no activation, 4096 columns,
+// M = 1024 6.5 and 5.2, 14336 columns, M = 512 6.8 and 6.4, 18944 columns 7.5 and 8.2;
+// SiLU, 4096 columns, M = 384 7.0 and 8.1, 14336 columns 10.7 and 10.2; gated, 18944
+// columns, M = 384 20.5 and 23.3.  The one limit leaves up to 2.8 us there (plain sums
+// of 4096 columns, M = 384: 6.9 and 4.0).
 bool one_strip(int M, bool sums) { return sums && M <= 256; }
 
 // Rows per strip of grad_kernel: 32, fewer while the launch has under 512
@@ -612,7 +621,7 @@ constexpr int kDxMaxSplit = 32;
 // a model of the launch: rounds of at most two workgroups per CU, each as long
 // as its steps, plus the partials' traffic and the second launch.  Measured, in
 // us: M = 2048, N = 14336, K = 4096: 128 x 256 split in two 211, 64 x 128 289;
-// M = 200, N = K = 3584: 128 x 256 split in four 27.2, 64 x 128 split in four
+// M = 200, N = K = 3584: 128 x 256 split in four 27.2, 64 x 128 split in two
 // 16.7 (one slice: 17.4); M = 64, N = 2 x 14336, K = 4096: 42.6 and 29.2 (34.4).
 DxPlan plan_dx(const DxDesc &d) {
   static const DxShape large = {8, 4, 1, 2.9, 3.5}, large8 = {6, 4, 1, 2.5, 3.1};

@@ -57,6 +57,11 @@ __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t b
 
 // Eight codes of one word -> (q_j - z) * scale in fp16, j = 0..7: (q - z) is
 // formed exactly (see the streaming kernel), then rounded once by the scale.
+// The rounding to the activations' type puts the whole weight into one 16-bit MFMA
+// operand.  Multiplying each group's fp32 sums by the scale instead would need no
+// rounding, but TM x TN x 4 FMAs per lane and group and the B operands of a whole
+// group (16 TN registers) at once, which the 128-row blocks do not have.  Plain and
+// fused launches round alike.
 __device__ __forceinline__ half8 dequant_word(uint32_t w, half2v bias_lo, half2v bias_hi,
                                               half2v scale) {
   const half2v sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
