@@ -369,7 +369,8 @@ int w4a16_spec_verify(const void *p_target, const void *p_draft, const void *dra
  * The fp32 sums get bias, activation and residual in fp32 and Y is rounded to
  * the activations' type once.  The sums themselves round what w4a16_gemm's do: X * s
  * once, and on the tiled path (M > 16) each dequantized weight once, both to the
- * activations' type.  The activations are evaluated in fp32 with a relative error
+ * activations' type: they are the operands of MFMAs that take 16-bit types, and
+ * sum in fp32.  The activations are evaluated in fp32 with a relative error
  * of at most 2^-14, in the lower tails too, down to where they leave fp32's normal
  * range.  An epilogue belongs to each problem: */
 enum {
