@@ -491,6 +491,122 @@ int w4a16_gated_backward(const void *dH, const w4a16_backward_term *gate,
                          int64_t M, int64_t K, int dtype, void *workspace, size_t workspace_bytes,
                          void *stream);
 
+/* ---- The expert feed-forward block: norms, routing, experts ------------------------- */
+
+/* Norms before and after a block, with the block's gate and residual scale:
+ *   r = alpha * x + gate * post(y),   h = pre(r),
+ * y [T][D] the block's output, x [T][D] the residual stream.  A norm is
+ *   W4A16_NORM_NONE   v (weight and bias must be NULL)
+ *   W4A16_NORM_RMS    v * weight / sqrt(mean(v^2) + eps) + bias
+ *   W4A16_NORM_LAYER  (v - mean(v)) * weight / sqrt(mean((v - mean(v))^2) + eps) + bias
+ * over the D columns of a row, weight and bias [D] or NULL (1 and 0), eps >= 0 and
+ * finite.  gate [ceil(T / gate_rows)][D] or NULL (1): row t / gate_rows belongs to token
+ * t (one gate for all tokens, one a sequence, one a token).  Everything is of the
+ * activations' type (dtype, W4A16_DTYPE_F16 or _BF16); a row is computed in fp32, h
+ * from the unrounded r, and r and h are rounded once.
+ * y may be NULL (then post is NONE and gate NULL: a plain norm).  r may be NULL where it
+ * is not wanted; h is NULL just where pre is NONE.  r and h may each start exactly where
+ * x or y does; otherwise outputs must not overlap each other or any input (EINVAL).
+ * 0 <= T < 2^22, 1 <= D <= 16384, any D.  Asynchronous on `stream`. */
+enum { W4A16_NORM_NONE = 0, W4A16_NORM_RMS = 1, W4A16_NORM_LAYER = 2 };
+
+typedef struct w4a16_norm {
+  const void *weight;
+  const void *bias;
+  float eps;
+  int32_t kind;          /* W4A16_NORM_*, else EUNSUPPORTED                      */
+} w4a16_norm;
+
+typedef struct w4a16_norm_call {
+  const void *x;
+  const void *y;
+  const void *gate;
+  w4a16_norm post;
+  w4a16_norm pre;
+  void *r;
+  void *h;
+  int64_t T, D, gate_rows;
+  float alpha;
+  int32_t dtype;
+} w4a16_norm_call;
+
+int w4a16_norm_block(const w4a16_norm_call *call, void *stream);
+
+/* Backward of w4a16_norm_block from dr (the gradient of r from elsewhere, or NULL) and
+ * dh (required just where pre is not NONE), with the forward's y and r (r only where
+ * pre is not NONE; y may be NULL as there):
+ *   R = dr + (gradient of pre at r)(dh),   dx = alpha * R,
+ *   dy = (gradient of post at y)(gate * R),
+ * both [T][D] of the activations' type, rounded once, or NULL.  Statistics are taken
+ * again from y and r, so nothing else is kept by the forward.  The fp32 gradients dgate
+ * (the gate's shape) and dpost_weight, dpost_bias, dpre_weight, dpre_bias [D], each or
+ * NULL, are sums over rows in a fixed order; one of an absent gate or norm is EINVAL.
+ * Outputs must not overlap each other or any input.  workspace:
+ * w4a16_norm_block_backward_workspace_size() bytes for the same call (it depends on T, D,
+ * gate_rows and which gradients are wanted; may be 0), 256-byte aligned; EINVAL if
+ * smaller.  Asynchronous on `stream`. */
+typedef struct w4a16_norm_backward_call {
+  const void *dr;
+  const void *dh;
+  const void *y;
+  const void *r;
+  const void *gate;
+  w4a16_norm post;
+  w4a16_norm pre;
+  void *dx;
+  void *dy;
+  void *dgate;
+  void *dpost_weight;
+  void *dpost_bias;
+  void *dpre_weight;
+  void *dpre_bias;
+  int64_t T, D, gate_rows;
+  float alpha;
+  int32_t dtype;
+} w4a16_norm_backward_call;
+
+int w4a16_norm_block_backward_workspace_size(const w4a16_norm_backward_call *call, size_t *bytes);
+int w4a16_norm_block_backward(const w4a16_norm_backward_call *call, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/* Routing of T tokens to k of E experts by logits [T][E] (dtype: W4A16_DTYPE_F16, _BF16
+ * or _F32):
+ *   score   softmax over the experts, or 1 / (1 + exp(-logit))
+ *   choice  the k largest of score + bias (bias fp32 [E], or NULL), with groups > 1 among
+ *           the experts of the topk_groups groups (of E / groups consecutive experts)
+ *           with the largest values, a group's value being the sum of its two largest
+ *           score + bias; ties go to the lower index
+ *   weight  scale * score, divided by the sum of the k chosen scores if renormalize
+ * ids int32 [T][k], in the order of the choice, and weights fp32 [T][k].  Choices are made
+ * as exact arithmetic would make them (to 2^-50 of a score where a bias or groups
+ * are given).  An expert whose logit is -inf or NaN is never chosen, whatever its bias
+ * (finite); where fewer than k are left to choose, the last slots have id -1 and weight 0.
+ * +inf counts as the largest finite fp32 value.
+ * 0 <= T <= 2^22, 1 <= E <= 1024, 1 <= k <= 64, 1 <= groups <= 64 dividing E,
+ * 1 <= topk_groups <= groups, k <= topk_groups * (E / groups), scale finite (EINVAL).
+ * Outputs must not overlap each other or an input.  Asynchronous on `stream`. */
+enum { W4A16_SCORE_SOFTMAX = 0, W4A16_SCORE_SIGMOID = 1 };
+enum { W4A16_DTYPE_F32 = 2 };  /* logits only */
+
+typedef struct w4a16_routing {
+  int64_t T, E, k;
+  int32_t score;         /* W4A16_SCORE_*, else EUNSUPPORTED                     */
+  int32_t groups, topk_groups;
+  int32_t renormalize;
+  float scale;
+  int32_t dtype;
+} w4a16_routing;
+
+int w4a16_route(const w4a16_routing *routing, const void *logits, const void *bias, void *ids,
+                void *weights, void *stream);
+
+/* Gradient of the logits (dlogits [T][E], of their type, fully written) from dweights
+ * fp32 [T][k] and the ids that w4a16_route gave; ids outside 0..E-1 contribute nothing.  The
+ * choice has no gradient.  dlogits must not overlap an input.  Asynchronous on
+ * `stream`. */
+int w4a16_route_backward(const w4a16_routing *routing, const void *dweights, const void *logits,
+                         const void *ids, void *dlogits, void *stream);
+
 /* Which path AUTO takes for this shape (host only; no GPU call). */
 int w4a16_select_path(int64_t M, int64_t N, int64_t K);
 

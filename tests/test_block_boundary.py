@@ -1,0 +1,163 @@
+"""Refusals of the expert block's entry points (host validation, no GPU) and the registers of
+its kernels."""
+import ctypes
+
+import pytest
+
+import weight_only_int4_group_amd as w4
+from tests.test_kernel_sources import _device_asm, _kernel_metadata
+from weight_only_int4_group_amd import experts as ex
+
+ODD = (1 << 20) + 2
+
+
+def at(i):
+    """Aligned stand-in addresses, 64 MB apart (never dereferenced)."""
+    return (1 + i) << 26
+
+
+def norm(kind=1, weight=None, bias=None, eps=1e-6):
+    return ex.NormStruct(weight, bias, eps, kind)
+
+
+NONE = (0, None, None, 0.0)
+
+
+def norm_call(**kw):
+    f = dict(x=at(0), y=at(1), gate=at(2), post=norm(), pre=norm(2, at(3), at(4)), r=at(5), h=at(6), T=4, D=64,
+             gate_rows=2, alpha=1.0, dtype=0)
+    f.update(kw)
+    return ex.NormCallStruct(*f.values())
+
+
+def norm_rc(**kw):
+    return w4.lib().w4a16_norm_block(ctypes.byref(norm_call(**kw)), None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(T=-1), -1), (dict(T=1 << 22), -1), (dict(D=0), -1), (dict(D=16385), -1), (dict(dtype=2), -3),
+    (dict(x=None), -1), (dict(r=None, h=None), -1), (dict(h=None), -1), (dict(pre=norm(*NONE)), -1),
+    (dict(post=norm(3)), -3), (dict(pre=norm(-1)), -3), (dict(post=norm(0, at(3))), -1),
+    (dict(post=norm(0, None, at(3))), -1), (dict(pre=norm(1, eps=-1.0)), -1),
+    (dict(pre=norm(1, eps=float("nan"))), -1), (dict(pre=norm(1, eps=float("inf"))), -1),
+    (dict(gate_rows=0), -1), (dict(y=None), -1), (dict(y=None, gate=None), -1),
+    (dict(y=None, post=norm(*NONE)), -1), (dict(x=ODD), -2), (dict(y=ODD), -2), (dict(gate=ODD), -2),
+    (dict(r=ODD), -2), (dict(h=ODD), -2), (dict(post=norm(1, ODD)), -2), (dict(pre=norm(1, None, ODD)), -2),
+    (dict(r=at(0) + 496), -1), (dict(h=at(1) + 16), -1), (dict(r=at(6)), -1), (dict(h=at(2)), -1),
+    (dict(r=at(3)), -1), (dict(T=0, x=None), 0),
+])
+def test_norm_refusals(kw, code):
+    assert norm_rc(**kw) == code
+
+
+def norm_backward(**kw):
+    f = dict(dr=at(0), dh=at(1), y=at(2), r=at(3), gate=at(4), post=norm(1, at(5)), pre=norm(2, at(6), at(7)),
+             dx=at(8), dy=at(9), dgate=at(10), dpost_weight=at(11), dpost_bias=at(12), dpre_weight=at(13),
+             dpre_bias=at(14), T=4, D=64, gate_rows=2, alpha=1.0, dtype=0)
+    f.update(kw)
+    return ex.NormBackwardStruct(*f.values())
+
+
+def norm_backward_rc(ws=at(20), nbytes=1 << 20, **kw):
+    return w4.lib().w4a16_norm_block_backward(ctypes.byref(norm_backward(**kw)), ws, nbytes, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(T=-1), -1), (dict(D=0), -1), (dict(D=20000), -1), (dict(dtype=7), -3), (dict(post=norm(5)), -3),
+    (dict(dh=None), -1), (dict(r=None), -1), (dict(y=None), -1), (dict(gate=None), -1), (dict(gate_rows=-2), -1),
+    (dict(pre=norm(*NONE)), -1), (dict(post=norm(*NONE)), -1),
+    (dict(pre=norm(*NONE), dpre_weight=None, dpre_bias=None), -1),
+    (dict(pre=norm(*NONE), dpre_weight=None, dpre_bias=None, dh=None, dr=None), -1),
+    (dict(ws=None), -1), (dict(nbytes=16), -1), (dict(ws=at(20) + 16), -2), (dict(dx=ODD), -2), (dict(dgate=ODD), -2),
+    (dict(dpre_bias=ODD), -2), (dict(dx=at(0)), -1), (dict(dy=at(2)), -1), (dict(dx=at(9) + 128), -1),
+    (dict(dgate=at(4)), -1), (dict(dpost_weight=at(11), dpost_bias=at(11) + 128), -1), (dict(dx=at(20)), -1),
+    (dict(dpre_weight=at(6)), -1),
+])
+def test_norm_backward_refusals(kw, code):
+    assert norm_backward_rc(**kw) == code
+
+
+def test_norm_backward_sizes():
+    n = ctypes.c_size_t()
+    size = w4.lib().w4a16_norm_block_backward_workspace_size
+    none = dict.fromkeys(("dgate", "dpost_weight", "dpost_bias", "dpre_weight", "dpre_bias"))
+    assert size(ctypes.byref(norm_backward(T=4096, D=4096, **none)), ctypes.byref(n)) == 0 and n.value == 0
+    assert size(ctypes.byref(norm_backward(T=0)), ctypes.byref(n)) == 0 and n.value == 0
+    assert size(ctypes.byref(norm_backward(T=4096, D=4096)), ctypes.byref(n)) == 0 and n.value > 0
+    assert size(ctypes.byref(norm_backward(D=0)), ctypes.byref(n)) == -1
+    assert size(ctypes.byref(norm_backward()), None) == -1 and size(None, ctypes.byref(n)) == -1
+    assert w4.lib().w4a16_norm_block(None, None) == -1
+    assert w4.lib().w4a16_norm_block_backward(None, None, 0, None) == -1
+
+
+def routing(**kw):
+    f = dict(T=4, E=64, k=8, score=0, groups=1, topk_groups=1, renormalize=1, scale=1.0, dtype=2)
+    f.update(kw)
+    return ex.RoutingStruct(*f.values())
+
+
+ROUTING_REFUSALS = [
+    (dict(T=-1), -1), (dict(T=(1 << 22) + 1), -1), (dict(E=0), -1), (dict(E=1025), -1), (dict(k=0), -1), (dict(k=65), -1),
+    (dict(E=4), -1), (dict(score=2), -3), (dict(score=-1), -3), (dict(dtype=3), -3), (dict(scale=float("inf")), -1),
+    (dict(scale=float("nan")), -1), (dict(groups=0), -1), (dict(groups=3), -1), (dict(groups=128, E=256), -1),
+    (dict(groups=8, topk_groups=9), -1), (dict(groups=8, topk_groups=0), -1), (dict(groups=16, topk_groups=1), -1),
+]
+
+
+@pytest.mark.parametrize("kw,code", ROUTING_REFUSALS)
+def test_routing_refusals(kw, code):
+    r = routing(**kw)
+    L = w4.lib()
+    assert L.w4a16_route(ctypes.byref(r), at(0), at(1), at(2), at(3), None) == code
+    assert L.w4a16_route_backward(ctypes.byref(r), at(0), at(1), at(2), at(3), None) == code
+
+
+def test_route_pointers():
+    L, r = w4.lib(), routing()
+    good = [at(0), at(1), at(2), at(3)]
+    for i in range(4):
+        for value, code in ((None, -1), (ODD, -2)):
+            args = list(good)
+            args[i] = value
+            if not (i == 1 and value is None):     # (no bias)
+                assert L.w4a16_route(ctypes.byref(r), *args, None) == code
+            assert L.w4a16_route_backward(ctypes.byref(r), *args, None) == code
+    assert L.w4a16_route(ctypes.byref(r), at(0), at(1), at(2), at(2), None) == -1
+    assert L.w4a16_route(ctypes.byref(r), at(0), at(1), at(0) + 64, at(2), None) == -1
+    assert L.w4a16_route(ctypes.byref(r), at(0), at(1), at(2), at(1) + 128, None) == -1
+    for i in range(3):
+        args = list(good)
+        args[3] = args[i]
+        assert L.w4a16_route_backward(ctypes.byref(r), *args, None) == -1
+    assert L.w4a16_route(None, *good, None) == -1
+    r = routing(T=0)
+    assert L.w4a16_route(ctypes.byref(r), None, None, None, None, None) == 0
+    assert L.w4a16_route_backward(ctypes.byref(r), None, None, None, None, None) == 0
+
+
+def test_binding_refuses_what_is_not_a_device_tensor():
+    import torch
+    x = torch.zeros(4, 8, dtype=torch.float16)
+    with pytest.raises(TypeError):
+        w4.w4a16_norm_block(x, pre=w4.Norm())
+    with pytest.raises(TypeError):
+        w4.w4a16_norm_block(x.float(), pre=w4.Norm())
+    with pytest.raises(TypeError):
+        w4.w4a16_route(x, w4.Routing(2))
+    with pytest.raises(TypeError):
+        w4.w4a16_route(x.int(), w4.Routing(2))
+    with pytest.raises(ValueError):
+        w4.w4a16_norm_block_backward(None, None)
+    g = torch.zeros(4, 8, requires_grad=True)
+    with pytest.raises(ValueError):
+        w4.w4a16_route(g, w4.Routing(2))
+    with pytest.raises(ValueError):
+        w4.w4a16_norm_block(g.half(), pre=w4.Norm())
+
+
+@pytest.mark.parametrize("source", ["norm.hip", "route.hip"])
+def test_block_kernels_keep_everything_in_registers(source, tmp_path):
+    kernels = _kernel_metadata(_device_asm(source, tmp_path))
+    assert kernels
+    bad = [k for k in kernels if k[1] or k[2] or k[3]]
+    assert not bad, f"{source}: (kernel, private bytes, VGPR spills, SGPR spills): {bad}"

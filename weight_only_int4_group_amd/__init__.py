@@ -62,7 +62,9 @@ EXPORTED_SYMBOLS = ("w4a16_packed_sizes", "w4a16_packed_sizes_mode", "w4a16_quan
                     "w4a16_linear", "w4a16_linear_workspace_size", "w4a16_gated",
                     "w4a16_gated_workspace_size", "w4a16_transposed_sizes", "w4a16_transpose",
                     "w4a16_linear_backward", "w4a16_linear_backward_workspace_size",
-                    "w4a16_gated_backward", "w4a16_gated_backward_workspace_size")
+                    "w4a16_gated_backward", "w4a16_gated_backward_workspace_size",
+                    "w4a16_norm_block", "w4a16_norm_block_backward_workspace_size",
+                    "w4a16_norm_block_backward", "w4a16_route", "w4a16_route_backward")
 
 
 class Problem(ctypes.Structure):
@@ -157,6 +159,7 @@ def lib() -> ctypes.CDLL:
                  "w4a16_gated_backward_workspace_size", "w4a16_gated_backward",
                  "w4a16_version"):
         getattr(L, name).restype = ctypes.c_int
+    experts._declare(L)
     _lib = L
     return L
 
@@ -870,3 +873,9 @@ def w4a16_gated_backward(dH, G, U, gate: TransposedWeight, up: TransposedWeight,
           for _ in range(2)]
     GatedBackwardCall(dH, G, U, gate, up, s, dX, dG, dU, act, add, *db)()
     return dX, dG, dU, db[0], db[1]
+
+
+from . import experts  # noqa: E402  (it takes the pieces above)
+from .experts import *  # noqa: E402,F401,F403
+
+__all__ += experts.__all__

@@ -1,25 +1,22 @@
 // C-ABI front end: argument validation (host only, before any HIP call),
 // kernel choice by M, and launches on the caller's stream.
-#include <functional>
 #include <initializer_list>
 #include <mutex>
 #include <vector>
 
 #include "../../include/w4a16.h"
+#include "checks.h"
 #include "w4a16_device.h"
 #include "w4a16_internal.h"
 
 namespace {
 
+using namespace w4a16::checks;
+
 constexpr int64_t kMaxDim = int64_t(1) << 24;  // rows / columns per operand
-constexpr int64_t kMaxM = int64_t(1) << 22;    // batch rows per call
-// Packed codes of one matrix are addressed with 32-bit byte offsets.
-constexpr int64_t kMaxPackedBytes = (int64_t(1) << 31) - (int64_t(1) << 20);
 
 // Largest M the streaming kernel takes in one pass (its A operand is 16 rows).
 constexpr int64_t kSkinnyMaxM = 16;
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int check_shape(int64_t N, int64_t K) {
   if (N <= 0 || K <= 0 || N > kMaxDim || K > kMaxDim) return W4A16_EINVAL;
@@ -450,7 +447,6 @@ int w4a16_gemm_grouped_ws(const w4a16_problem *problems, int count, void *worksp
 
 namespace {
 
-bool known_act(int act) { return act >= W4A16_ACT_NONE && act <= W4A16_ACT_GELU_TANH; }
 static_assert(W4A16_ACT_RELU == (int)w4a16::kActRelu && W4A16_ACT_SILU == (int)w4a16::kActSilu &&
                   W4A16_ACT_GELU == (int)w4a16::kActGelu &&
                   W4A16_ACT_GELU_TANH == (int)w4a16::kActGeluTanh,
@@ -735,8 +731,6 @@ int w4a16_gemm(const void *X, const void *Wq, const void *scales, const void *ze
 
 namespace {
 
-bool aligned256(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
-
 // Rows of a transposed weight are addressed from a block's first row with
 // 32-bit byte offsets (128 rows of dZ).
 constexpr int64_t kMaxBackwardN = int64_t(1) << 22;
@@ -818,20 +812,6 @@ int check_backward_pointers(const w4a16_backward_term &t, bool gated, bool dx, i
     return W4A16_EALIGN;
   return W4A16_OK;
 }
-
-struct Range {
-  const void *p;
-  size_t n;
-};
-
-bool overlap(const Range &a, const Range &b) {
-  if (!a.p || !b.p || a.n == 0 || b.n == 0) return false;
-  const char *x = static_cast<const char *>(a.p), *y = static_cast<const char *>(b.p);
-  return std::less<const char *>()(x, y + b.n) && std::less<const char *>()(y, x + a.n);
-}
-
-// An output that may also be exactly the input it replaces, element by element.
-bool overlap_but_same(const Range &out, const Range &in) { return out.p != in.p && overlap(out, in); }
 
 // The kernels of a call run in order (the terms' dZ and dbias one after the
 // other, then dX from all of them, s and add): an output over another output or

@@ -128,6 +128,52 @@ struct DxDesc {
 size_t dx_workspace_bytes(const DxDesc &d);
 hipError_t launch_dx(const DxDesc &d, void *workspace, hipStream_t stream);
 
+// Norms before and after a block: r = alpha x + gate post(y), h = pre(r).  y, gate,
+// r and h null where absent; kinds are W4A16_NORM_*.
+struct NormSpec {
+  int kind;
+  float eps;
+  const void *weight, *bias;
+};
+struct NormDesc {
+  const void *x, *y, *gate;
+  NormSpec post, pre;
+  float alpha;
+  void *r, *h;
+  int T, D, gate_rows;  // gate row m / gate_rows of token m
+  bool bf16;
+};
+hipError_t launch_norm(const NormDesc &d, hipStream_t stream);
+
+// Its backward; sums: the fp32 gradients of the gate, post's weight and bias and
+// pre's weight and bias, each null when not wanted.
+constexpr int kNormSums = 5;
+struct NormGradDesc {
+  const void *dr, *dh, *y, *r, *gate;
+  NormSpec post, pre;
+  float alpha;
+  void *dx, *dy;
+  void *sums[kNormSums];
+  int T, D, gate_rows;
+  bool bf16;
+};
+size_t norm_grad_workspace_bytes(const NormGradDesc &d);
+hipError_t launch_norm_grad(const NormGradDesc &d, void *workspace, hipStream_t stream);
+
+// Routing of T tokens to k of E experts (E <= 1024, k <= 64), or its backward (reads
+// ids and dweights, writes dlogits).  type: 0 fp16, 1 bf16, 2 fp32 logits.
+struct RouteDesc {
+  const void *logits;
+  const float *bias, *dweights;
+  int32_t *ids;
+  float *weights;
+  void *dlogits;
+  int T, E, k, type;
+  int sigmoid, groups, topk_groups, renormalize;
+  float scale;
+};
+hipError_t launch_route(const RouteDesc &d, bool grad, hipStream_t stream);
+
 // Speculative-sampling verification of B sequences (validated by the caller):
 // the vocabulary is cut into spec_verify_chunks(V) chunks, and the workspace
 // (spec_verify_workspace_bytes(B, V) bytes, 256-byte aligned) holds the
