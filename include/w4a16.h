@@ -607,6 +607,90 @@ int w4a16_route(const w4a16_routing *routing, const void *logits, const void *bi
 int w4a16_route_backward(const w4a16_routing *routing, const void *dweights, const void *logits,
                          const void *ids, void *dlogits, void *stream);
 
+/* The experts' gated feed-forward blocks over packed INT4 weights.  For token t and slot j, with
+ * e = ids[t][j] (int32) and w = weights[t][j] (fp32), as w4a16_route gives them:
+ *   G = (X[t] * s) . Wg_e^T,  U = (X[t] * s) . Wu_e^T,  H = act(G) * U * s_down[e],
+ *   Y[t] = residual[t] + sum over j of w * (H . Wd_e^T).
+ * An id outside 0..E-1 names no expert: the slot adds nothing (experts held elsewhere,
+ * padded tokens).  A token may name an expert twice.  A weight is E packed weights of one
+ * shape, one after the other in each of its three buffers (w4a16_packed_sizes bytes per
+ * expert): gate and up [N][D], down [D][N], (q - z) * scale; s fp16 [D] (one for all
+ * experts, which read the same X) and s_down fp16 [E][N], or NULL (1).
+ * X, residual (or NULL; may be Y) and Y [T][D], and G and U [T][k][N] are of the
+ * activations' type.  G and U are both set, for a backward pass, or both NULL; those of a
+ * slot that names no expert are not written.
+ * X * s is rounded to the activations' type once (not without s), and so are H, G, U and
+ * Y; weights and sums are not rounded: codes are multiplied exactly, scales and
+ * zero points applied to the fp32 sums of their group.
+ * 0 <= T <= 2^22, 1 <= E <= 1024, 1 <= k <= 64, D and N multiples of 128 up to 2^20 with
+ * N * D / 2 < 2^31 - 2^20 (EINVAL).  workspace: w4a16_experts_workspace_size() bytes
+ * (it depends on T, E, k, D, N and whether s is set), 256-byte aligned; EINVAL if smaller.
+ * Calls that share one must not overlap in time.  All pointers 16-byte aligned (EALIGN);
+ * outputs and workspace must not overlap each other or an input (EINVAL), but Y may be
+ * residual.  The same call always gives the same bits.  Asynchronous on `stream`. */
+typedef struct w4a16_expert_weight {
+  const void *Wq;
+  const void *scales;
+  const void *zeros;
+} w4a16_expert_weight;
+
+typedef struct w4a16_experts_call {
+  const void *X;
+  const void *ids;
+  const void *weights;
+  w4a16_expert_weight gate, up, down;
+  const void *s;
+  const void *s_down;
+  const void *residual;
+  void *G;
+  void *U;
+  void *Y;
+  int64_t T, E, k, D, N;
+  int32_t act;           /* W4A16_ACT_*, else EUNSUPPORTED                       */
+  int32_t dtype;
+} w4a16_experts_call;
+
+int w4a16_experts_workspace_size(const w4a16_experts_call *call, size_t *bytes);
+int w4a16_experts(const w4a16_experts_call *call, void *workspace, size_t workspace_bytes,
+                  void *stream);
+
+/* Backward of w4a16_experts with frozen weights, from dY [T][D] and the G and U that its forward
+ * kept:
+ *   dH = (dY[t] . Wd_e) * s_down[e],   dweights[t][j] = <dH, act(G) * U>,
+ *   dG = w * dH * U * act'(G),  dU = w * dH * act(G),
+ *   dX[t] = add[t] + s * sum over j of (dG . Wg_e + dU . Wu_e).
+ * gate, up and down are the transposed copies (w4a16_transpose) of the E weights, one after
+ * the other in each buffer.  dX and add (or NULL; may be dX) [T][D] and dweights [T][k] are
+ * of the activations' type: the products round each weight, and dG and dU, to it once, as
+ * w4a16_gated_backward's do.  dX or dweights may be NULL; add needs dX.  A slot that names
+ * no expert has dweights 0, and its G and U are not read.  Limits, errors and workspace
+ * (w4a16_experts_backward_workspace_size() bytes) as for w4a16_experts. */
+typedef struct w4a16_expert_transposed {
+  const void *Wt;
+  const void *meta;
+} w4a16_expert_transposed;
+
+typedef struct w4a16_experts_backward_call {
+  const void *dY;
+  const void *ids;
+  const void *weights;
+  const void *G;
+  const void *U;
+  w4a16_expert_transposed gate, up, down;
+  const void *s;
+  const void *s_down;
+  const void *add;
+  void *dX;
+  void *dweights;
+  int64_t T, E, k, D, N;
+  int32_t act;
+  int32_t dtype;
+} w4a16_experts_backward_call;
+
+int w4a16_experts_backward_workspace_size(const w4a16_experts_backward_call *call, size_t *bytes);
+int w4a16_experts_backward(const w4a16_experts_backward_call *call, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
 /* Which path AUTO takes for this shape (host only; no GPU call). */
 int w4a16_select_path(int64_t M, int64_t N, int64_t K);
 

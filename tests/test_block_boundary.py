@@ -135,6 +135,77 @@ def test_route_pointers():
     assert L.w4a16_route_backward(ctypes.byref(r), None, None, None, None, None) == 0
 
 
+def experts_call(**kw):
+    weight = [ex.ExpertWeightStruct(at(40 + 3 * i), at(41 + 3 * i), at(42 + 3 * i)) for i in range(3)]
+    f = dict(X=at(0), ids=at(1), weights=at(2), gate=weight[0], up=weight[1], down=weight[2], s=at(3), s_down=at(4),
+             residual=at(5), G=at(6), U=at(7), Y=at(8), T=4, E=8, k=2, D=256, N=128, act=2, dtype=0)
+    f.update(kw)
+    return ex.ExpertsStruct(*f.values())
+
+
+def experts_rc(ws=at(20), nbytes=1 << 25, **kw):
+    return w4.lib().w4a16_experts(ctypes.byref(experts_call(**kw)), ws, nbytes, None)
+
+
+EXPERT_SHAPES = [
+    (dict(T=-1), -1), (dict(T=(1 << 22) + 1), -1), (dict(E=0), -1), (dict(E=1025), -1), (dict(k=0), -1), (dict(k=65), -1),
+    (dict(D=0), -1), (dict(D=64), -1), (dict(D=200), -1), (dict(N=192), -1), (dict(N=1 << 21), -1),
+    (dict(D=1 << 16, N=1 << 16), -1), (dict(act=5), -3), (dict(act=-1), -3), (dict(dtype=2), -3),
+]
+
+
+@pytest.mark.parametrize("kw,code", EXPERT_SHAPES + [
+    (dict(X=None), -1), (dict(ids=None), -1), (dict(weights=None), -1), (dict(Y=None), -1), (dict(G=None), -1),
+    (dict(U=None), -1), (dict(gate=ex.ExpertWeightStruct(at(1), None, at(2))), -1),
+    (dict(down=ex.ExpertWeightStruct(at(1), at(2), ODD)), -2), (dict(X=ODD), -2), (dict(ids=ODD), -2),
+    (dict(weights=ODD), -2), (dict(s=ODD), -2), (dict(s_down=ODD), -2), (dict(residual=ODD), -2), (dict(G=ODD), -2),
+    (dict(Y=ODD), -2), (dict(ws=None), -1), (dict(nbytes=64), -1), (dict(ws=at(20) + 16), -2), (dict(Y=at(0)), -1),
+    (dict(Y=at(5) + 16), -1), (dict(G=at(7)), -1), (dict(Y=at(20)), -1), (dict(U=at(40)), -1), (dict(Y=at(4)), -1),
+    (dict(ws=at(0)), -1), (dict(G=at(5)), -1), (dict(T=0, X=None), 0),
+])
+def test_experts_refusals(kw, code):
+    assert experts_rc(**kw) == code
+
+
+def experts_backward(**kw):
+    weight = [ex.ExpertTransposedStruct(at(40 + 2 * i), at(41 + 2 * i)) for i in range(3)]
+    f = dict(dY=at(0), ids=at(1), weights=at(2), G=at(3), U=at(4), gate=weight[0], up=weight[1], down=weight[2], s=at(5),
+             s_down=at(6), add=at(7), dX=at(8), dweights=at(9), T=4, E=8, k=2, D=256, N=128, act=2, dtype=0)
+    f.update(kw)
+    return ex.ExpertsBackwardStruct(*f.values())
+
+
+def experts_backward_rc(ws=at(20), nbytes=1 << 25, **kw):
+    return w4.lib().w4a16_experts_backward(ctypes.byref(experts_backward(**kw)), ws, nbytes, None)
+
+
+@pytest.mark.parametrize("kw,code", EXPERT_SHAPES + [
+    (dict(dY=None), -1), (dict(ids=None), -1), (dict(weights=None), -1), (dict(G=None), -1), (dict(U=None), -1),
+    (dict(dX=None), -1), (dict(dX=None, add=None, dweights=None), -1),
+    (dict(up=ex.ExpertTransposedStruct(None, at(2))), -1), (dict(gate=ex.ExpertTransposedStruct(at(1), ODD)), -2),
+    (dict(dY=ODD), -2), (dict(G=ODD), -2), (dict(add=ODD), -2), (dict(dX=ODD), -2), (dict(dweights=ODD), -2),
+    (dict(ws=None), -1), (dict(nbytes=64), -1), (dict(ws=at(20) + 128), -2), (dict(dX=at(0)), -1), (dict(dX=at(3)), -1),
+    (dict(dweights=at(8)), -1), (dict(dX=at(7) + 32), -1), (dict(dweights=at(7)), -1), (dict(dX=at(20)), -1),
+    (dict(T=0, dY=None), 0),
+])
+def test_experts_backward_refusals(kw, code):
+    assert experts_backward_rc(**kw) == code
+
+
+def test_experts_sizes():
+    L, n = w4.lib(), ctypes.c_size_t()
+    for size, call in ((L.w4a16_experts_workspace_size, experts_call),
+                       (L.w4a16_experts_backward_workspace_size, experts_backward)):
+        assert size(ctypes.byref(call(T=0)), ctypes.byref(n)) == 0 and n.value == 0
+        assert size(ctypes.byref(call()), ctypes.byref(n)) == 0 and 0 < n.value < 1 << 20
+        # bounded whatever the number of tokens: at most 2^17 slots a round
+        assert size(ctypes.byref(call(T=1 << 22, D=4096, N=1024)), ctypes.byref(n)) == 0
+        assert n.value < (1 << 17) * (4 * 4096 + 4 * 1024 + 256) + (1 << 30)
+        assert size(ctypes.byref(call(D=100)), ctypes.byref(n)) == -1
+        assert size(ctypes.byref(call()), None) == -1 and size(None, ctypes.byref(n)) == -1
+    assert L.w4a16_experts(None, None, 0, None) == -1 and L.w4a16_experts_backward(None, None, 0, None) == -1
+
+
 def test_binding_refuses_what_is_not_a_device_tensor():
     import torch
     x = torch.zeros(4, 8, dtype=torch.float16)
@@ -155,7 +226,15 @@ def test_binding_refuses_what_is_not_a_device_tensor():
         w4.w4a16_norm_block(g.half(), pre=w4.Norm())
 
 
-@pytest.mark.parametrize("source", ["norm.hip", "route.hip"])
+def test_stacking_refuses_unlike_weights():
+    a, b = w4.PackedWeight(None, None, None, 128, 128), w4.PackedWeight(None, None, None, 128, 256)
+    c = w4.PackedWeight(None, None, None, 128, 128, wbits=8)
+    for bad in ([], [a, b], [a, c], [c]):
+        with pytest.raises(ValueError):
+            w4.w4a16_stack_experts(bad)
+
+
+@pytest.mark.parametrize("source", ["norm.hip", "route.hip", "experts.hip"])
 def test_block_kernels_keep_everything_in_registers(source, tmp_path):
     kernels = _kernel_metadata(_device_asm(source, tmp_path))
     assert kernels

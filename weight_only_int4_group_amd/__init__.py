@@ -64,7 +64,9 @@ EXPORTED_SYMBOLS = ("w4a16_packed_sizes", "w4a16_packed_sizes_mode", "w4a16_quan
                     "w4a16_linear_backward", "w4a16_linear_backward_workspace_size",
                     "w4a16_gated_backward", "w4a16_gated_backward_workspace_size",
                     "w4a16_norm_block", "w4a16_norm_block_backward_workspace_size",
-                    "w4a16_norm_block_backward", "w4a16_route", "w4a16_route_backward")
+                    "w4a16_norm_block_backward", "w4a16_route", "w4a16_route_backward",
+                    "w4a16_experts_workspace_size", "w4a16_experts",
+                    "w4a16_experts_backward_workspace_size", "w4a16_experts_backward")
 
 
 class Problem(ctypes.Structure):

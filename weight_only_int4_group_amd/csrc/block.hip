@@ -131,6 +131,69 @@ w4a16::RouteDesc route_desc(const w4a16_routing &r) {
 
 size_t logit_bytes(const w4a16_routing &r) { return (size_t)(r.T * r.E) * (r.dtype == W4A16_DTYPE_F32 ? 4 : 2); }
 
+// ---- experts -------------------------------------------------------------------------
+
+constexpr int64_t kMaxExpertDim = int64_t(1) << 20;
+
+int check_experts_shape(int64_t T, int64_t E, int64_t k, int64_t D, int64_t N, int act, int dtype) {
+  if (T < 0 || T > kMaxM || E < 1 || E > kMaxExperts || k < 1 || k > kMaxTopK) return W4A16_EINVAL;
+  if (D < W4A16_GROUP || N < W4A16_GROUP || D > kMaxExpertDim || N > kMaxExpertDim || D % W4A16_GROUP ||
+      N % W4A16_GROUP || N * D / 2 > kMaxPackedBytes)
+    return W4A16_EINVAL;
+  return known_act(act) && act_type(dtype) ? W4A16_OK : W4A16_EUNSUPPORTED;
+}
+
+w4a16::ExpertsDesc experts_desc(const w4a16_experts_call &c) {
+  auto weight = [](const w4a16_expert_weight &w) { return w4a16::ExpertWeight{w.Wq, w.scales, w.zeros}; };
+  w4a16::ExpertsDesc d = {};
+  d.X = c.X;
+  d.ids = static_cast<const int32_t *>(c.ids);
+  d.weights = static_cast<const float *>(c.weights);
+  d.gate = weight(c.gate);
+  d.up = weight(c.up);
+  d.down = weight(c.down);
+  d.s = c.s;
+  d.s_down = c.s_down;
+  d.residual = c.residual;
+  d.G = c.G;
+  d.U = c.U;
+  d.Y = c.Y;
+  d.T = (int)c.T;
+  d.E = (int)c.E;
+  d.k = (int)c.k;
+  d.D = (int)c.D;
+  d.N = (int)c.N;
+  d.act = c.act;
+  d.bf16 = c.dtype == W4A16_DTYPE_BF16;
+  return d;
+}
+
+w4a16::ExpertsGradDesc experts_grad_desc(const w4a16_experts_backward_call &c) {
+  auto weight = [](const w4a16_expert_transposed &w) { return w4a16::ExpertTransposed{w.Wt, w.meta}; };
+  w4a16::ExpertsGradDesc d = {};
+  d.dY = c.dY;
+  d.ids = static_cast<const int32_t *>(c.ids);
+  d.weights = static_cast<const float *>(c.weights);
+  d.G = c.G;
+  d.U = c.U;
+  d.gate = weight(c.gate);
+  d.up = weight(c.up);
+  d.down = weight(c.down);
+  d.s = c.s;
+  d.s_down = c.s_down;
+  d.add = c.add;
+  d.dX = c.dX;
+  d.dweights = c.dweights;
+  d.T = (int)c.T;
+  d.E = (int)c.E;
+  d.k = (int)c.k;
+  d.D = (int)c.D;
+  d.N = (int)c.N;
+  d.act = c.act;
+  d.bf16 = c.dtype == W4A16_DTYPE_BF16;
+  return d;
+}
+
 }  // namespace
 
 extern "C" {
@@ -216,6 +279,79 @@ int w4a16_route_backward(const w4a16_routing *r, const void *dweights, const voi
   d.ids = const_cast<int32_t *>(static_cast<const int32_t *>(ids));
   d.dlogits = dlogits;
   return status(w4a16::launch_route(d, true, static_cast<hipStream_t>(stream)));
+}
+
+int w4a16_experts_workspace_size(const w4a16_experts_call *c, size_t *bytes) {
+  if (!c || !bytes) return W4A16_EINVAL;
+  if (int rc = check_experts_shape(c->T, c->E, c->k, c->D, c->N, c->act, c->dtype)) return rc;
+  *bytes = w4a16::experts_workspace_bytes(experts_desc(*c));
+  return W4A16_OK;
+}
+
+int w4a16_experts(const w4a16_experts_call *c, void *workspace, size_t workspace_bytes, void *stream) {
+  if (!c) return W4A16_EINVAL;
+  if (int rc = check_experts_shape(c->T, c->E, c->k, c->D, c->N, c->act, c->dtype)) return rc;
+  if (c->T == 0) return W4A16_OK;
+  if (!c->X || !c->ids || !c->weights || !c->Y || (c->G != nullptr) != (c->U != nullptr)) return W4A16_EINVAL;
+  for (const w4a16_expert_weight *w : {&c->gate, &c->up, &c->down}) {
+    if (!w->Wq || !w->scales || !w->zeros) return W4A16_EINVAL;
+    if (!aligned16({w->Wq, w->scales, w->zeros})) return W4A16_EALIGN;
+  }
+  if (!aligned16({c->X, c->ids, c->weights, c->s, c->s_down, c->residual, c->G, c->U, c->Y})) return W4A16_EALIGN;
+  const w4a16::ExpertsDesc d = experts_desc(*c);
+  const size_t need = w4a16::experts_workspace_bytes(d);
+  if (!workspace || workspace_bytes < need) return W4A16_EINVAL;
+  if (!aligned256(workspace)) return W4A16_EALIGN;
+  const size_t rows = (size_t)(c->T * c->D) * 2, slots = (size_t)(c->T * c->k), kept = slots * c->N * 2;
+  const size_t codes = (size_t)(c->E * (c->N * c->D / 2)), E = (size_t)c->E;
+  const size_t meta_in = E * c->N * (size_t)((c->D / W4A16_GROUP + 3) / 4 * 4) * 2;
+  const size_t meta_down = E * c->D * (size_t)((c->N / W4A16_GROUP + 3) / 4 * 4) * 2;
+  if (overlaps({{c->Y, rows}, {c->G, kept}, {c->U, kept}, {workspace, need}},
+               {{c->X, rows}, {c->ids, slots * 4}, {c->weights, slots * 4}, {c->gate.Wq, codes}, {c->up.Wq, codes},
+                {c->down.Wq, codes}, {c->gate.scales, meta_in}, {c->gate.zeros, meta_in}, {c->up.scales, meta_in},
+                {c->up.zeros, meta_in}, {c->down.scales, meta_down}, {c->down.zeros, meta_down},
+                {c->s, (size_t)c->D * 2}, {c->s_down, E * c->N * 2}}, 0) ||
+      overlaps({{c->G, kept}, {c->U, kept}, {workspace, need}}, {{c->residual, rows}}, 0) ||
+      overlaps({{c->Y, rows}}, {{c->residual, rows}}, 1))
+    return W4A16_EINVAL;
+  return status(w4a16::launch_experts(d, workspace, static_cast<hipStream_t>(stream)));
+}
+
+int w4a16_experts_backward_workspace_size(const w4a16_experts_backward_call *c, size_t *bytes) {
+  if (!c || !bytes) return W4A16_EINVAL;
+  if (int rc = check_experts_shape(c->T, c->E, c->k, c->D, c->N, c->act, c->dtype)) return rc;
+  *bytes = w4a16::experts_grad_workspace_bytes(experts_grad_desc(*c));
+  return W4A16_OK;
+}
+
+int w4a16_experts_backward(const w4a16_experts_backward_call *c, void *workspace, size_t workspace_bytes,
+                           void *stream) {
+  if (!c) return W4A16_EINVAL;
+  if (int rc = check_experts_shape(c->T, c->E, c->k, c->D, c->N, c->act, c->dtype)) return rc;
+  if (c->T == 0) return W4A16_OK;
+  if (!c->dY || !c->ids || !c->weights || !c->G || !c->U || (!c->dX && (!c->dweights || c->add)))
+    return W4A16_EINVAL;
+  for (const w4a16_expert_transposed *w : {&c->gate, &c->up, &c->down}) {
+    if (!w->Wt || !w->meta) return W4A16_EINVAL;
+    if (!aligned16({w->Wt, w->meta})) return W4A16_EALIGN;
+  }
+  if (!aligned16({c->dY, c->ids, c->weights, c->G, c->U, c->s, c->s_down, c->add, c->dX, c->dweights}))
+    return W4A16_EALIGN;
+  const w4a16::ExpertsGradDesc d = experts_grad_desc(*c);
+  const size_t need = w4a16::experts_grad_workspace_bytes(d);
+  if (!workspace || workspace_bytes < need) return W4A16_EINVAL;
+  if (!aligned256(workspace)) return W4A16_EALIGN;
+  const size_t rows = (size_t)(c->T * c->D) * 2, slots = (size_t)(c->T * c->k), kept = slots * c->N * 2;
+  const size_t codes = (size_t)(c->E * (c->N * c->D / 2)), E = (size_t)c->E;
+  const size_t meta = (size_t)(c->E * (c->N / W4A16_GROUP) * (c->D / W4A16_GROUP) * 512);
+  if (overlaps({{c->dX, rows}, {c->dweights, slots * 2}, {workspace, need}},
+               {{c->dY, rows}, {c->ids, slots * 4}, {c->weights, slots * 4}, {c->G, kept}, {c->U, kept},
+                {c->gate.Wt, codes}, {c->up.Wt, codes}, {c->down.Wt, codes}, {c->gate.meta, meta}, {c->up.meta, meta},
+                {c->down.meta, meta}, {c->s, (size_t)c->D * 2}, {c->s_down, E * c->N * 2}}, 0) ||
+      overlaps({{c->dweights, slots * 2}, {workspace, need}}, {{c->add, rows}}, 0) ||
+      overlaps({{c->dX, rows}}, {{c->add, rows}}, 1))
+    return W4A16_EINVAL;
+  return status(w4a16::launch_experts_grad(d, workspace, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,1027 @@
+// The experts' gated feed-forward blocks over packed INT4 weights, and their backward.
+//
+//   forward   G = X . Wg_e^T,  U = X . Wu_e^T,  H = act(G) * U * s_down,
+//             Y = residual + sum over a token's slots of w * (H . Wd_e^T)
+//   backward  dH = (dY . Wd_e) * s_down,  dw = <dH, act(G) * U>,
+//             dG = w dH U act'(G),  dU = w dH act(G),
+//             dX = add + s * sum over the slots of (dG . Wg_e + dU . Wu_e)
+//
+// A slot is one of a token's k choices.  plan_kernel sorts the slots by expert and cuts each
+// expert's run into tiles of rows; a product's workgroup takes one tile and a strip of the
+// expert's outputs.  How many tiles there are is known on the GPU alone: the grids cover
+// the most there can be, and workgroups past the last tile end at once.  The order of an
+// expert's rows is whatever the sort's atomics give; no result depends on it, since a
+// row of a product does not depend on the rows beside it.
+//
+// Each slot's contribution to Y (or dX) is kept in fp32, weighted, in the slot's own row;
+// combine_kernel adds a token's k rows in their order.  (Atomic adds into Y would save
+// that pass, and give other bits every time.)
+#include <algorithm>
+
+#include "epilogue.h"
+#include "w4a16_device.h"
+#include "w4a16_internal.h"
+
+namespace w4a16 {
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kRsrcWord3 = 0x00020000;  // raw buffer resource, 32-bit data format
+constexpr int kMetaBytes = 512;         // transposed weights: metadata of 128 rows and one group
+constexpr int kOutOfRange = 0x7ffffff0; // a buffer offset past every resource: loads read 0
+
+__device__ __forceinline__ int uniform_int(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t bits) {
+  uint32_t r;
+  asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(mask), "s"(bits));
+  return r;
+}
+
+template <bool BF>
+__device__ __forceinline__ float4v mfma(u32x4 a, u32x4 b, float4v c) {
+  if constexpr (BF)
+    return mfma16_bf16(a, b, c);
+  else
+    return mfma16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), c);
+}
+
+// Eight codes of one word as an exact MFMA operand, c + q with c = 128 (bf16) or 64
+// (fp16): an OR into the mantissa of c, whose last bit that holds 1 lies at the
+// bottom (bf16) or at bit 4 (fp16).  Seven instructions, and nothing rounded; with
+// xs the sum of a row's activations over the group, its dot product with (q - z) is
+// the MFMA's sum minus (c + z) xs, in fp32.
+template <bool BF>
+constexpr float kCodeBase = BF ? 128.f : 64.f;
+template <bool BF>
+__device__ __forceinline__ u32x4 code_operand(uint32_t w) {
+  if constexpr (BF)
+    return (u32x4){and_or(w, 0x000F000Fu, kMagicBF), and_or(w >> 4, 0x000F000Fu, kMagicBF),
+                   and_or(w >> 8, 0x000F000Fu, kMagicBF), and_or(w >> 12, 0x000F000Fu, kMagicBF)};
+  else
+    return (u32x4){and_or(w << 4, 0x00F000F0u, 0x54005400u), and_or(w, 0x00F000F0u, 0x54005400u),
+                   and_or(w >> 4, 0x00F000F0u, 0x54005400u), and_or(w >> 8, 0x00F000F0u, 0x54005400u)};
+}
+template <bool BF>
+__device__ __forceinline__ u32x4 ones_operand() {
+  const uint32_t one = BF ? 0x3F803F80u : 0x3C003C00u;
+  return (u32x4){one, one, one, one};
+}
+
+// ---- the plan -------------------------------------------------------------------------
+
+struct ExpertTile {
+  int expert, row0, rows, unused;  // sorted rows row0 .. row0 + rows - 1
+};
+struct Plan {
+  const int32_t *order;      // [S] slots, sorted by expert (those that name one)
+  const ExpertTile *tiles;
+  const int32_t *count;      // tiles there are
+};
+
+constexpr int kPlanThreads = 1024;  // and the most experts
+
+// One workgroup: counts per expert, their prefix sums (and those of their tiles), then
+// each slot to its place.
+__global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int32_t *ids, int S, int E, int tile_rows,
+                                                            int32_t *order, ExpertTile *tiles,
+                                                            int32_t *tile_count) {
+  __shared__ int count[kPlanThreads], at[kPlanThreads];
+  __shared__ int2 part[kPlanThreads / 64];
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  count[t] = 0;
+  __syncthreads();
+  for (int i = t; i < S; i += kPlanThreads) {
+    const int e = ids[i];
+    if (e >= 0 && e < E) atomicAdd(&count[e], 1);
+  }
+  __syncthreads();
+  const int rows = count[t], mine = (rows + tile_rows - 1) / tile_rows;
+  int a = rows, b = mine;  // inclusive sums over the wave, then over the waves
+#pragma unroll
+  for (int o = 1; o < 64; o *= 2) {
+    const int pa = __shfl_up(a, o), pb = __shfl_up(b, o);
+    if (lane >= o) {
+      a += pa;
+      b += pb;
+    }
+  }
+  if (lane == 63) part[wave] = make_int2(a, b);
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) {
+    a += part[w].x;
+    b += part[w].y;
+  }
+  const int first = a - rows;
+  at[t] = first;
+  for (int i = 0; i < mine; ++i)
+    tiles[b - mine + i] = {t, first + i * tile_rows, min(tile_rows, rows - i * tile_rows), 0};
+  if (t == kPlanThreads - 1) *tile_count = b;
+  __syncthreads();
+  for (int i = t; i < S; i += kPlanThreads) {
+    const int e = ids[i];
+    if (e >= 0 && e < E) order[atomicAdd(&at[e], 1)] = i;
+  }
+}
+
+// ---- operands and epilogues shared by the products -------------------------------------------
+
+enum { kGatedOut = 0, kRowsOut = 1 };
+
+struct ExpertArgs {
+  Plan plan;
+  const void *A;          // gathered: [tokens][K] rows; else [sorted rows][K]
+  const uint8_t *Wq[2];   // expert 0's weights (gated: gate and up)
+  const _Float16 *scales[2], *zeros[2];
+  size_t code_bytes, meta_count;  // from one expert to the next
+  int K, N;               // of one weight: outputs are N wide
+  int k, tokens;          // slots per token; tokens of A when gathered
+  const float *weights;   // [slots]
+  const _Float16 *s_down; // [E][N] or null (gated)
+  void *G, *U;            // [slots][N] or null (gated)
+  void *H;                // gated: [sorted rows][N]
+  float *part;            // rows: [slots][N], weighted
+  int act, columns;       // columns: workgroups along the outputs
+};
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void *p, size_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((void *)p, (short)0, (int)min((size_t)0x7fffffff, bytes), kRsrcWord3);
+}
+
+// (tile, column block) of workgroup `block`: the active workgroups are renumbered so that
+// each XCD (they go round the eight) takes one run of them, whose neighbours share an
+// expert's weights and rows in its L2.  false: past the last tile.
+__device__ __forceinline__ bool place(const Plan &plan, int columns, int block, int &tile, int &column) {
+  const int total = uniform_int(*plan.count) * columns, run = (total + 7) >> 3;
+  const int local = (block & 7) * run + (block >> 3);
+  if ((block >> 3) >= run || local >= total) return false;
+  tile = local / columns;
+  column = local - tile * columns;
+  return true;
+}
+
+__device__ __forceinline__ ExpertTile tile_at(const Plan &plan, int tile) {
+  const ExpertTile t = plan.tiles[tile];
+  return {uniform_int(t.expert), uniform_int(t.row0), uniform_int(t.rows), 0};
+}
+
+// Stores a 16 x 16 block of G and U: row 4 c + v of rows row .. of the tile, column n.
+template <bool BF>
+__device__ __forceinline__ void store_gated(const ExpertArgs &P, const ExpertTile &tile, int row, int n, float4v g,
+                                            float4v u) {
+  const float sd = P.s_down ? (float)P.s_down[(size_t)tile.expert * P.N + n] : 1.f;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    if (row + v >= tile.rows) continue;
+    const size_t at = (size_t)(tile.row0 + row + v);
+    if (P.G) {
+      const size_t slot = (size_t)P.plan.order[at] * P.N + n;
+      static_cast<uint16_t *>(P.G)[slot] = f32_to_act<BF>(g[v]);
+      static_cast<uint16_t *>(P.U)[slot] = f32_to_act<BF>(u[v]);
+    }
+    static_cast<uint16_t *>(P.H)[at * P.N + n] = f32_to_act<BF>(act_value(g[v], P.act) * u[v] * sd);
+  }
+}
+
+__device__ __forceinline__ void store_rows(const ExpertArgs &P, const ExpertTile &tile, int row, int n, float4v y) {
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    if (row + v >= tile.rows) continue;
+    const int slot = P.plan.order[tile.row0 + row + v];
+    P.part[(size_t)slot * P.N + n] = y[v] * P.weights[slot];
+  }
+}
+
+// ---- few rows per expert: streaming -----------------------------------------------------------
+
+// A tile of up to 16 rows, TN 16-row blocks of the weights (gated: alternating gate and
+// up), KS waves that each take a KS-th of the contraction and meet in LDS at the end (in
+// order).  Bound by HBM: every weight is read once per tile.  Codes and activations
+// come straight into registers, DEPTH groups of 128 ahead, with no barrier until the end;
+// rows past the tile's are not loaded (their offset lies past the resource).
+template <int TN, int KS, int EPI, bool GATHER, bool BF>
+__global__ __launch_bounds__(64 * KS) void expert_stream_kernel(ExpertArgs P) {
+  constexpr int DEPTH = TN == 2 ? 4 : 2;
+  constexpr int STEP = EPI == kGatedOut ? 2 : 1;
+  __shared__ float4v red[KS][TN][64];
+  int tile_i, column;
+  if (!place(P.plan, P.columns, blockIdx.x, tile_i, column)) return;
+  const ExpertTile tile = tile_at(P.plan, tile_i);
+  const int lane = threadIdx.x & 63, wave = uniform_int(threadIdx.x >> 6), c = lane >> 4, r = lane & 15;
+  const int K = P.K, N = P.N, G = K / kGroup, NB = N / kTileRows;
+  const int vb0 = column * TN;  // first row block (gated: of the alternating ones)
+
+  const __amdgpu_buffer_rsrc_t ars =
+      GATHER ? resource(P.A, (size_t)P.tokens * K * 2)
+             : resource(static_cast<const uint16_t *>(P.A) + (size_t)tile.row0 * K, (size_t)tile.rows * K * 2);
+  int aoff = kOutOfRange;
+  if (r < tile.rows) aoff = ((GATHER ? P.plan.order[tile.row0 + r] / P.k : r) * K + 8 * c) * 2;
+  __amdgpu_buffer_rsrc_t wrs[STEP], srs[STEP], zrs[STEP];
+  const size_t code0 = tile.expert * P.code_bytes, meta0 = tile.expert * P.meta_count;
+#pragma unroll
+  for (int i = 0; i < STEP; ++i) {
+    wrs[i] = resource(P.Wq[i] + code0, P.code_bytes);
+    srs[i] = resource(P.scales[i] + meta0, P.meta_count * 2);
+    zrs[i] = resource(P.zeros[i] + meta0, P.meta_count * 2);
+  }
+  const int tile_stride = NB * kTileBytes, meta_stride = NB * kTileRows * kMetaQuad * 2;
+  const int g0 = G * wave / KS, g1 = G * (wave + 1) / KS;
+
+  struct Stage {
+    u32x4 a[4], code[TN];
+    uint32_t sc[TN], zp[TN];
+  } st[DEPTH];
+  auto load = [&](int g, Stage &s) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      const int rb = min(vb0 + j, STEP * NB - 1) / STEP;  // (blocks past N: the last again, not stored)
+      s.code[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                wrs[j % STEP], lane * 16, g * tile_stride + rb * kTileBytes, 0));
+      const int qo = (g / kMetaQuad) * meta_stride + (rb * kTileRows * kMetaQuad + g % kMetaQuad) * 2;
+      s.sc[j] = __builtin_amdgcn_raw_buffer_load_b16(srs[j % STEP], r * kMetaQuad * 2, qo, 0);
+      s.zp[j] = __builtin_amdgcn_raw_buffer_load_b16(zrs[j % STEP], r * kMetaQuad * 2, qo, 0);
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      s.a[t] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ars, aoff, g * kGroup * 2 + 64 * t, 0));
+  };
+  float4v acc[TN];
+#pragma unroll
+  for (int j = 0; j < TN; ++j) acc[j] = float4v{0.f, 0.f, 0.f, 0.f};
+  auto compute = [&](const Stage &s) {
+    float4v xs = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int t = 0; t < 4; ++t) xs = mfma<BF>(s.a[t], ones_operand<BF>(), xs);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      float4v p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int t = 0; t < 4; ++t) p = mfma<BF>(s.a[t], code_operand<BF>(s.code[j][t]), p);
+      const float sc = (float)__builtin_bit_cast(_Float16, (uint16_t)s.sc[j]);
+      const float z = kCodeBase<BF> + (float)__builtin_bit_cast(_Float16, (uint16_t)s.zp[j]);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[j][v] = __builtin_fmaf(sc, __builtin_fmaf(-z, xs[v], p[v]), acc[j][v]);
+    }
+  };
+#pragma unroll
+  for (int d = 0; d < DEPTH; ++d)
+    if (g0 + d < g1) load(g0 + d, st[d]);
+  for (int g = g0; g < g1; g += DEPTH) {
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) {
+      if (g + d >= g1) break;
+      compute(st[d]);
+      if (g + d + DEPTH < g1) load(g + d + DEPTH, st[d]);
+    }
+  }
+
+#pragma unroll
+  for (int j = 0; j < TN; ++j) red[wave][j][lane] = acc[j];
+  __syncthreads();
+  for (int p = wave; p < TN / STEP; p += KS) {
+    float4v y[STEP];
+#pragma unroll
+    for (int i = 0; i < STEP; ++i) {
+      y[i] = red[0][STEP * p + i][lane];
+#pragma unroll
+      for (int w = 1; w < KS; ++w) y[i] += red[w][STEP * p + i][lane];
+    }
+    const int n = (vb0 / STEP + p) * kTileRows + r;
+    if (n >= N) continue;
+    if constexpr (EPI == kGatedOut)
+      store_gated<BF>(P, tile, 4 * c, n, y[0], y[STEP - 1]);
+    else
+      store_rows(P, tile, 4 * c, n, y[0]);
+  }
+}
+
+// ---- many rows per expert: LDS tiles -----------------------------------------------------------
+
+// A tile of 16 TM rows and 256 outputs (gated: 128 of G and of U), four waves of 16 TM x
+// 64, a group of 128 of the contraction per stage: the rows go into LDS with DMA loads
+// (double-buffered, XOR-swizzled 16-byte chunks, one barrier a stage), the wave's code
+// tiles into registers one stage ahead.
+//
+// The codes are multiplied as they are (code_operand) and the group's scale and zero
+// point applied to its fp32 sums, so no weight is rounded and the decoding costs 7
+// instructions per 8 weights; it is the sums that cost two FMAs per element and group,
+// half of what their four MFMAs take.  The sums of a group's activations, which the zero
+// points multiply, are MFMAs with ones: wave i takes those of row block i, and they reach
+// the other waves through LDS a stage later.
+template <int TM, int EPI, bool GATHER, bool BF>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void expert_tile_kernel(ExpertArgs P) {
+  constexpr int TN = 4, BM = 16 * TM, STEP = EPI == kGatedOut ? 2 : 1;
+  constexpr int kRowChunks = kGroup / 8, kDma = BM * kRowChunks / 256;  // DMA loads per wave and stage (TM)
+  __shared__ __attribute__((aligned(16))) _Float16 As[2][BM * kGroup];
+  __shared__ float4v Xs[2][BM / 4];
+  int tile_i, column;
+  if (!place(P.plan, P.columns, blockIdx.x, tile_i, column)) return;
+  const ExpertTile tile = tile_at(P.plan, tile_i);
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform_int(tid >> 6), c = lane >> 4, r = lane & 15;
+  const int K = P.K, N = P.N, G = K / kGroup, NB = N / kTileRows;
+
+  // wave load u fills LDS chunks p = (u * 4 + wave) * 64 + lane: row p / 16 = 16 u + 4 wave +
+  // lane / 16, physical chunk p % 16, holding logical chunk lc = (p % 16) ^ (row % 16), the same
+  // for every u.  Rows past the tile's lie past the resource and read zeros.
+  const __amdgpu_buffer_rsrc_t ars =
+      GATHER ? resource(P.A, (size_t)P.tokens * K * 2)
+             : resource(static_cast<const uint16_t *>(P.A) + (size_t)tile.row0 * K, (size_t)tile.rows * K * 2);
+  const int arow = 4 * wave + c, lc = r ^ arow;
+  int aoff[GATHER ? kDma : 1];
+  aoff[0] = (arow * K + 8 * lc) * 2;
+  if constexpr (GATHER) {
+#pragma unroll
+    for (int u = 0; u < kDma; ++u) {
+      aoff[u] = kOutOfRange;
+      if (16 * u + arow < tile.rows)
+        aoff[u] = (P.plan.order[tile.row0 + 16 * u + arow] / P.k * K + 8 * lc) * 2;
+    }
+  }
+  auto load_a = [&](int g, int buf) {
+#pragma unroll
+    for (int u = 0; u < kDma; ++u) {
+      const int vo = GATHER ? aoff[GATHER ? u : 0] : aoff[0] + 32 * u * K;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          ars, (__attribute__((address_space(3))) void *)(&As[buf][(u * 4 + wave) * 64 * 8]), 16, vo,
+          g * kGroup * 2, 0, 0);
+    }
+  };
+  __amdgpu_buffer_rsrc_t wrs[STEP], srs[STEP], zrs[STEP];
+  const size_t code0 = tile.expert * P.code_bytes, meta0 = tile.expert * P.meta_count;
+#pragma unroll
+  for (int i = 0; i < STEP; ++i) {
+    wrs[i] = resource(P.Wq[i] + code0, P.code_bytes);
+    srs[i] = resource(P.scales[i] + meta0, P.meta_count * 2);
+    zrs[i] = resource(P.zeros[i] + meta0, P.meta_count * 2);
+  }
+  const int vb0 = (column * 4 + wave) * TN;
+  const int tile_stride = NB * kTileBytes, meta_stride = NB * kTileRows * kMetaQuad * 2;
+  struct BStage {
+    u32x4 code[TN];
+    uint32_t sc[TN], zp[TN];
+  };
+  auto load_b = [&](int g, BStage &b) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      const int rb = min(vb0 + j, STEP * NB - 1) / STEP;
+      b.code[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                wrs[j % STEP], lane * 16, g * tile_stride + rb * kTileBytes, 0));
+      const int qo = (g / kMetaQuad) * meta_stride + (rb * kTileRows * kMetaQuad + g % kMetaQuad) * 2;
+      b.sc[j] = __builtin_amdgcn_raw_buffer_load_b16(srs[j % STEP], r * kMetaQuad * 2, qo, 0);
+      b.zp[j] = __builtin_amdgcn_raw_buffer_load_b16(zrs[j % STEP], r * kMetaQuad * 2, qo, 0);
+    }
+  };
+
+  float4v acc[TM][TN];
+#pragma unroll
+  for (int j = 0; j < TN; ++j)
+#pragma unroll
+    for (int i = 0; i < TM; ++i) acc[i][j] = float4v{0.f, 0.f, 0.f, 0.f};
+  // a group's zero points, from its stage b and the row sums in LDS
+  auto take_zero_points = [&](const BStage &b, int buf) {
+    float zs[TN];
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+      zs[j] = (float)__builtin_bit_cast(_Float16, (uint16_t)b.sc[j]) *
+              (kCodeBase<BF> + (float)__builtin_bit_cast(_Float16, (uint16_t)b.zp[j]));
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const float4v xs = Xs[buf][4 * i + c];
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(-zs[j], xs[v], acc[i][j][v]);
+    }
+  };
+  auto compute = [&](const BStage &b, int buf) {
+    float4v p[TM][TN], xs = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int tt = 0; tt < 4; ++tt) {
+      const int pc = (4 * tt + c) ^ r;
+      u32x4 bop[TN];
+#pragma unroll
+      for (int j = 0; j < TN; ++j) bop[j] = code_operand<BF>(b.code[j][tt]);
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        const u32x4 a = *reinterpret_cast<const u32x4 *>(&As[buf][(16 * i + r) * kGroup + 8 * pc]);
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+          p[i][j] = mfma<BF>(a, bop[j], tt ? p[i][j] : float4v{0.f, 0.f, 0.f, 0.f});
+      }
+      if (TM == 4 || wave < TM) {
+        const u32x4 a = *reinterpret_cast<const u32x4 *>(&As[buf][(16 * wave + r) * kGroup + 8 * pc]);
+        xs = mfma<BF>(a, ones_operand<BF>(), xs);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      const float sc = (float)__builtin_bit_cast(_Float16, (uint16_t)b.sc[j]);
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(sc, p[i][j][v], acc[i][j][v]);
+    }
+    if ((TM == 4 || wave < TM) && r == 0) Xs[buf][4 * wave + c] = xs;
+  };
+  // One group per step: wait until this group's loads (issued a step ago) and the sums of
+  // the group before are in LDS and every wave is past the previous step, issue the
+  // next group's loads, compute.  Past the range they re-read the last group.
+  BStage b0, b1;
+  auto step = [&](int g, BStage &cur, BStage &nxt, int buf) {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    const int gn = min(g + 1, G - 1);
+    load_a(gn, buf ^ 1);
+    if (g > 0) take_zero_points(nxt, buf ^ 1);  // (nxt still holds the group before)
+    load_b(gn, nxt);
+    compute(cur, buf);
+  };
+  load_a(0, 0);
+  load_b(0, b0);
+  for (int g = 0; g < G; g += 2) {
+    step(g, b0, b1, 0);
+    if (g + 1 < G) step(g + 1, b1, b0, 1);
+  }
+  // (the last step's DMA must land before the workgroup's LDS is released)
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  take_zero_points(b0, (G - 1) & 1);  // (both stages hold the last group)
+
+  // (the lane's place again, rather than in registers through the loop)
+  const int at = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    if (16 * i >= tile.rows) break;
+#pragma unroll
+    for (int j = 0; j < TN; j += STEP) {
+      const int n = (vb0 + j) / STEP * kTileRows + (at & 15);
+      if (n >= N) continue;
+      if constexpr (EPI == kGatedOut)
+        store_gated<BF>(P, tile, 16 * i + 4 * (at >> 4), n, acc[i][j], acc[i][j + STEP - 1]);
+      else
+        store_rows(P, tile, 16 * i + 4 * (at >> 4), n, acc[i][j]);
+    }
+  }
+}
+
+// ---- backward products -------------------------------------------------------------------------
+
+enum { kActGradOut = 0, kGradRowsOut = 1 };
+
+struct ExpertGradArgs {
+  Plan plan;
+  const void *A[2];              // gathered: [tokens][R] rows of dY; else [sorted rows][R]
+  const uint8_t *Wt[2], *meta[2];  // expert 0's transposed weights
+  size_t code_bytes, meta_bytes; // from one expert to the next
+  int R, C;                      // contraction per term, outputs
+  int k, tokens;
+  const float *weights;          // [slots]
+  const _Float16 *s_down;        // [E][C] or null
+  const void *G, *U;             // [slots][C]
+  void *dG, *dU;                 // [sorted rows][C]
+  float *dw_part;                // [slots][4 columns]
+  float *part;                   // [slots][C]
+  int act, columns;
+};
+
+// A tile of 16 TM rows and 256 outputs of the sum over the terms of A . D, D [R][C] the
+// experts' (q - z) * scale: four waves of 16 TM x 64, 128 rows of one term's D per
+// stage.  Rows of A and the stage's scales and zero points (1 KB for 256 outputs) go into LDS
+// with DMA loads, the wave's code tiles into registers, all one stage ahead.  The scale
+// varies along the contraction here, so it cannot multiply the sums: each weight is
+// rounded once to the activations' type, which the MFMA takes, as in the dense layers'
+// backward.
+template <int TM, int EPI, bool GATHER, bool BF>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void expert_grad_kernel(ExpertGradArgs P) {
+  constexpr int TN = 4, BM = 16 * TM, TERMS = EPI == kActGradOut ? 1 : 2;
+  __shared__ __attribute__((aligned(16))) _Float16 As[2][BM * kGroup];
+  __shared__ __attribute__((aligned(16))) unsigned char Ms[2][1024];
+  int tile_i, column;
+  if (!place(P.plan, P.columns, blockIdx.x, tile_i, column)) return;
+  const ExpertTile tile = tile_at(P.plan, tile_i);
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform_int(tid >> 6), c = lane >> 4, r = lane & 15;
+  const int R = P.R, C = P.C, KB = C / kTileRows, CG = C / kGroup, NG = R / kGroup;
+
+  __amdgpu_buffer_rsrc_t ars[TERMS], wrs[TERMS], mrs[TERMS];
+#pragma unroll
+  for (int i = 0; i < TERMS; ++i) {
+    ars[i] = GATHER ? resource(P.A[i], (size_t)P.tokens * R * 2)
+                    : resource(static_cast<const uint16_t *>(P.A[i]) + (size_t)tile.row0 * R, (size_t)tile.rows * R * 2);
+    wrs[i] = resource(P.Wt[i] + tile.expert * P.code_bytes, P.code_bytes);
+    mrs[i] = resource(P.meta[i] + tile.expert * P.meta_bytes, P.meta_bytes);
+  }
+  // rows of A: as in expert_tile_kernel
+  const int arow = 4 * wave + c, lc = r ^ arow;
+  int aoff[GATHER ? TM : 1];
+  aoff[0] = (arow * R + 8 * lc) * 2;
+  if constexpr (GATHER) {
+#pragma unroll
+    for (int u = 0; u < TM; ++u) {
+      aoff[u] = kOutOfRange;
+      if (16 * u + arow < tile.rows)
+        aoff[u] = (P.plan.order[tile.row0 + 16 * u + arow] / P.k * R + 8 * lc) * 2;
+    }
+  }
+  auto load_a = [&](int stage, int buf) {
+    const int ti = TERMS > 1 && stage >= NG ? 1 : 0, g = stage - ti * NG;
+    // (an array element passed straight to the builtin keeps the kernel from being
+    // instantiated in the host compilation)
+    const __amdgpu_buffer_rsrc_t rs = ti ? ars[TERMS - 1] : ars[0], ms = ti ? mrs[TERMS - 1] : mrs[0];
+#pragma unroll
+    for (int u = 0; u < TM; ++u) {
+      const int vo = GATHER ? aoff[GATHER ? u : 0] : aoff[0] + 32 * u * R;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rs, (__attribute__((address_space(3))) void *)(&As[buf][(u * 4 + wave) * 64 * 8]), 16, vo,
+          g * kGroup * 2, 0, 0);
+    }
+    // scales and zero points of the block's two quantization groups (or its one, twice): 256 bytes a wave
+    const int mo = ((column * 2 + 1 < CG ? wave : wave & 1) * 64 + lane) * 4;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        ms, (__attribute__((address_space(3))) void *)(&Ms[buf][wave * 256]), 4, mo,
+        (g * CG + column * 2) * kMetaBytes, 0, 0);
+  };
+  const int kb0 = (column * 4 + wave) * TN, tile_stride = KB * kTileBytes;
+  struct BStage {
+    u32x4 code[TN];
+  };
+  auto load_b = [&](int stage, BStage &b) {
+    const int ti = TERMS > 1 && stage >= NG ? 1 : 0, g = stage - ti * NG;
+    const __amdgpu_buffer_rsrc_t rs = ti ? wrs[TERMS - 1] : wrs[0];
+#pragma unroll
+    for (int j = 0; j < TN; ++j)  // (column blocks past C: the last again, not stored)
+      b.code[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                rs, lane * 16,
+                                                g * tile_stride + min(kb0 + j, KB - 1) * kTileBytes, 0));
+  };
+  const int ul = wave >> 1;  // the wave's quantization group among the block's two
+
+  float4v acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = float4v{0.f, 0.f, 0.f, 0.f};
+
+  auto compute = [&](const BStage &b, int buf) {
+    const _Float16 *ms = reinterpret_cast<const _Float16 *>(&Ms[buf][ul * kMetaBytes]) + 8 * c;
+    struct Meta {
+      half8 scale, bias;
+    };
+    auto meta_at = [&](int tt) -> Meta {
+      return {*reinterpret_cast<const half8 *>(ms + 32 * tt), *reinterpret_cast<const half8 *>(ms + kGroup + 32 * tt)};
+    };
+    auto dequant = [&](int j, int tt, const Meta &m) -> u32x4 {
+      const uint32_t w = b.code[j][tt], w8 = w >> 8;
+      const half2v sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
+      const half2v e[4] = {as_half2(and_or(w, 0x000F000Fu, kMagic2)),
+                           as_half2(and_or(w, 0x00F000F0u, kMagic2)) * sixteenth,
+                           as_half2(and_or(w8, 0x000F000Fu, kMagic2)),
+                           as_half2(and_or(w8, 0x00F000F0u, kMagic2)) * sixteenth};
+      u32x4 out;
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const half2v bias = {m.bias[2 * p], m.bias[2 * p + 1]}, scale = {m.scale[2 * p], m.scale[2 * p + 1]};
+        const half2v v = e[p] - bias;  // q - z, exact
+        if constexpr (BF)
+          out[p] = pack_bf16x2(__builtin_fmaf((float)v[0], (float)scale[0], 0.f),
+                               __builtin_fmaf((float)v[1], (float)scale[1], 0.f));
+        else
+          out[p] = __builtin_bit_cast(uint32_t, v * scale);
+      }
+      return out;
+    };
+    // k step tt + 1's weights are dequantized while k step tt's MFMAs run
+    u32x4 bop[TN];
+    Meta m = meta_at(0);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) bop[j] = dequant(j, 0, m);
+#pragma unroll
+    for (int tt = 0; tt < 4; ++tt) {
+      u32x4 bnx[TN];
+      if (tt < 3) {
+        m = meta_at(tt + 1);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) bnx[j] = dequant(j, tt + 1, m);
+      }
+      const int pc = (4 * tt + c) ^ r;
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        const u32x4 a = *reinterpret_cast<const u32x4 *>(&As[buf][(16 * i + r) * kGroup + 8 * pc]);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = mfma<BF>(a, bop[j], acc[i][j]);
+      }
+      if (tt < 3) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) bop[j] = bnx[j];
+      }
+    }
+  };
+  BStage b0, b1;
+  const int stages = TERMS * NG;
+  auto step = [&](int i, BStage &cur, BStage &nxt, int buf) {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    const int next = min(i + 1, stages - 1);  // (past the range: the last again, into what nobody reads)
+    load_a(next, buf ^ 1);
+    load_b(next, nxt);
+    compute(cur, buf);
+  };
+  load_a(0, 0);
+  load_b(0, b0);
+  for (int i = 0; i < stages; i += 2) {
+    step(i, b0, b1, 0);
+    if (i + 1 < stages) step(i + 1, b1, b0, 1);
+  }
+  // the last step's DMA must land before the workgroup's LDS is released
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+
+  const int at = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+  const int ec = at >> 4, er = at & 15;
+  if (kb0 >= KB) return;  // (C is a multiple of 128: a wave's 64 outputs are all there or none)
+  float sd[TN];
+  if constexpr (EPI == kActGradOut) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+      sd[j] = P.s_down ? (float)P.s_down[(size_t)tile.expert * C + (kb0 + j) * kTileRows + er] : 1.f;
+  }
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    if (16 * i >= tile.rows) break;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int row = 16 * i + 4 * ec + v;
+      const bool in = row < tile.rows;
+      const size_t sorted = (size_t)(tile.row0 + (in ? row : 0));
+      const int slot = P.plan.order[sorted];
+      const size_t from = (size_t)slot * C + kb0 * kTileRows + er;
+      if constexpr (EPI == kGradRowsOut) {
+        if (!in) continue;
+#pragma unroll
+        for (int j = 0; j < TN; ++j) P.part[from + j * kTileRows] = acc[i][j][v];
+      } else {
+        const float w = P.weights[slot];
+        const size_t to = sorted * C + kb0 * kTileRows + er;
+        float dw = 0.f;
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          const float g = act_to_f32<BF>(static_cast<const uint16_t *>(P.G)[from + j * kTileRows]);
+          const float u = act_to_f32<BF>(static_cast<const uint16_t *>(P.U)[from + j * kTileRows]);
+          const float dh = acc[i][j][v] * sd[j], a = act_value(g, P.act);
+          dw = __builtin_fmaf(dh, a * u, dw);
+          if (in) {
+            static_cast<uint16_t *>(P.dG)[to + j * kTileRows] = f32_to_act<BF>(w * dh * u * act_grad(g, P.act));
+            static_cast<uint16_t *>(P.dU)[to + j * kTileRows] = f32_to_act<BF>(w * dh * a);
+          }
+        }
+#pragma unroll
+        for (int o = 1; o < 16; o *= 2) dw += __shfl_xor(dw, o);
+        if (in && er == 0) P.dw_part[(size_t)slot * (4 * P.columns) + column * 4 + wave] = dw;
+      }
+    }
+  }
+}
+
+// dw of each slot: its partial sums over the first `parts` of `stride`, one wave per slot, in a
+// fixed order; 0 for a slot that names no expert.
+template <bool BF>
+__global__ __launch_bounds__(256) void weight_grad_kernel(const int32_t *ids, const float *part, int stride, int parts,
+                                                          int S, int E, uint16_t *dw) {
+  const int slot = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  if (slot >= S) return;
+  const int e = ids[slot];
+  float s = 0.f;
+  if (e >= 0 && e < E)
+    for (int i = lane; i < parts; i += 64) s += part[(size_t)slot * stride + i];
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+  if (lane == 0) dw[slot] = f32_to_act<BF>(s);
+}
+
+// ---- joining a token's slots ---------------------------------------------------------------------
+
+struct CombineArgs {
+  const int32_t *ids;
+  const float *part;         // [slots][D]
+  const void *add;           // [T][D] or null
+  const _Float16 *s;         // [D] or null (backward)
+  void *out;                 // [T][D]
+  int T, D, k, E;
+};
+
+// out[t] = add[t] + s * sum of the token's rows, in the order of its slots; four columns
+// per thread.
+template <bool BF>
+__global__ __launch_bounds__(256) void combine_kernel(CombineArgs P) {
+  const int quads = P.D / 4;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= (long long)P.T * quads) return;
+  const int t = (int)(i / quads), d = (int)(i - (long long)t * quads) * 4;
+  const int32_t *ids = P.ids + (size_t)t * P.k;
+  const float *rows = P.part + (size_t)t * P.k * P.D + d;
+  float4v y = {0.f, 0.f, 0.f, 0.f};
+  for (int j0 = 0; j0 < P.k; j0 += 4) {
+    float4v x[4];
+    bool in[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int e = j0 + j < P.k ? ids[j0 + j] : -1;
+      in[j] = e >= 0 && e < P.E;
+      x[j] = float4v{0.f, 0.f, 0.f, 0.f};
+      if (in[j]) x[j] = *reinterpret_cast<const float4v *>(rows + (size_t)(j0 + j) * P.D);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y += x[j];
+  }
+  if (P.s) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) y[v] *= (float)P.s[d + v];
+  }
+  const size_t at = (size_t)t * P.D + d;
+  if (P.add) {
+    const u16x4 a = *reinterpret_cast<const u16x4 *>(static_cast<const uint16_t *>(P.add) + at);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) y[v] += act_to_f32<BF>(a[v]);
+  }
+  u16x4 out;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) out[v] = f32_to_act<BF>(y[v]);
+  *reinterpret_cast<u16x4 *>(static_cast<uint16_t *>(P.out) + at) = out;
+}
+
+// X * s, rounded once, eight columns per thread.
+template <bool BF>
+__global__ __launch_bounds__(256) void expert_prescale_kernel(const uint16_t *X, const _Float16 *s, uint16_t *out,
+                                                              int K, long long octets) {
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= octets) return;
+  const u32x4 x = *reinterpret_cast<const u32x4 *>(X + 8 * i);
+  const half8 f = load_half8(s + (8 * i) % K);
+  u32x4 y;
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    y[q] = (uint32_t)f32_to_act<BF>(act_to_f32<BF>((uint16_t)x[q]) * (float)f[2 * q]) |
+           (uint32_t)f32_to_act<BF>(act_to_f32<BF>((uint16_t)(x[q] >> 16)) * (float)f[2 * q + 1]) << 16;
+  *reinterpret_cast<u32x4 *>(out + 8 * i) = y;
+}
+
+// ---- launches -----------------------------------------------------------------------------------
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+// A call runs in rounds of at most this many slots, and of rows that 32-bit offsets reach,
+// so that its workspace stays bounded.
+constexpr long long kMaxSlots = 1 << 17;
+
+int round_tokens(int T, int k, int D) {
+  const long long by_slots = std::max<long long>(1, kMaxSlots / k);
+  const long long by_bytes = std::max<long long>(1, ((1ll << 31) - 1) / (2ll * D));
+  return (int)std::min<long long>(T, std::min(by_slots, by_bytes));
+}
+
+int max_tiles(int S, int E, int rows) { return std::min(S, S / rows + std::min(E, S)); }
+
+// Rows per tile: 16 where an expert that is chosen at all gets that many or fewer on
+// average (streaming), else 32 or 64.
+int tile_rows(const ExpertsDesc &d, int S) {
+  const double mean = (double)S / std::min(d.E, S);
+  return mean <= 16 ? 16 : mean <= 32 ? 32 : 64;
+}
+
+// The workspace of one round.
+struct Layout {
+  int tokens, slots, rows, tiles;  // rows: per tile
+  size_t order, list, count, xs, h, part, total;
+};
+Layout layout(const ExpertsDesc &d) {
+  Layout l = {};
+  l.tokens = round_tokens(d.T, d.k, d.D);
+  l.slots = l.tokens * d.k;
+  l.rows = tile_rows(d, l.slots);
+  l.tiles = max_tiles(l.slots, d.E, l.rows);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += align256(bytes);
+    return here;
+  };
+  l.order = take((size_t)l.slots * 4);
+  l.list = take((size_t)l.tiles * sizeof(ExpertTile));
+  l.count = take(4);
+  l.xs = take(d.s ? (size_t)l.tokens * d.D * 2 : 0);
+  l.h = take((size_t)l.slots * d.N * 2);
+  l.part = take((size_t)l.slots * d.D * 4);
+  l.total = at;
+  return l;
+}
+
+template <int EPI, bool GATHER, bool BF>
+hipError_t launch_product(ExpertArgs a, int rows, int tiles, hipStream_t stream) {
+  const int blocks = (EPI == kGatedOut ? 2 : 1) * (a.N / kTileRows);
+  if (rows == 16) {
+    constexpr int TN = EPI == kGatedOut ? 4 : 2, KS = EPI == kGatedOut ? 4 : 8;
+    a.columns = (blocks + TN - 1) / TN;
+    hipLaunchKernelGGL((expert_stream_kernel<TN, KS, EPI, GATHER, BF>), dim3((unsigned)((tiles * a.columns + 7) / 8 * 8)),
+                       dim3(64 * KS), 0, stream, a);
+  } else {
+    a.columns = (blocks + 15) / 16;
+    const dim3 grid((unsigned)((tiles * a.columns + 7) / 8 * 8));
+    if (rows == 32)
+      hipLaunchKernelGGL((expert_tile_kernel<2, EPI, GATHER, BF>), grid, dim3(256), 0, stream, a);
+    else
+      hipLaunchKernelGGL((expert_tile_kernel<4, EPI, GATHER, BF>), grid, dim3(256), 0, stream, a);
+  }
+  return hipGetLastError();
+}
+
+template <bool BF>
+hipError_t launch_experts_typed(const ExpertsDesc &d, char *ws, hipStream_t stream) {
+  const Layout l = layout(d);
+  const size_t slot_n = (size_t)d.k * d.N * 2;
+  for (int t0 = 0; t0 < d.T; t0 += l.tokens) {
+    const int T = std::min(l.tokens, d.T - t0), S = T * d.k;
+    const int32_t *ids = d.ids + (size_t)t0 * d.k;
+    int32_t *order = reinterpret_cast<int32_t *>(ws + l.order), *count = reinterpret_cast<int32_t *>(ws + l.count);
+    ExpertTile *list = reinterpret_cast<ExpertTile *>(ws + l.list);
+    hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, ids, S, d.E, l.rows, order, list, count);
+    const char *X = static_cast<const char *>(d.X) + (size_t)t0 * d.D * 2;
+    if (d.s) {
+      const long long octets = (long long)T * d.D / 8;
+      hipLaunchKernelGGL(expert_prescale_kernel<BF>, dim3((unsigned)((octets + 255) / 256)), dim3(256), 0, stream,
+                         reinterpret_cast<const uint16_t *>(X), static_cast<const _Float16 *>(d.s),
+                         reinterpret_cast<uint16_t *>(ws + l.xs), d.D, octets);
+      X = ws + l.xs;
+    }
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int tiles = max_tiles(S, d.E, l.rows);
+    ExpertArgs a = {};
+    a.plan = {order, list, count};
+    a.k = d.k;
+    a.tokens = T;
+    a.weights = d.weights + (size_t)t0 * d.k;
+    a.act = d.act;
+    auto weight = [&](int i, const ExpertWeight &w) {
+      a.Wq[i] = static_cast<const uint8_t *>(w.Wq);
+      a.scales[i] = static_cast<const _Float16 *>(w.scales);
+      a.zeros[i] = static_cast<const _Float16 *>(w.zeros);
+    };
+    auto shape = [&](int N, int K) {
+      a.N = N;
+      a.K = K;
+      a.code_bytes = (size_t)N * K / 2;
+      a.meta_count = (size_t)N * meta_groups(K / kGroup);
+    };
+    weight(0, d.gate);
+    weight(1, d.up);
+    shape(d.N, d.D);
+    a.A = X;
+    a.s_down = static_cast<const _Float16 *>(d.s_down);
+    a.G = d.G ? static_cast<char *>(d.G) + t0 * slot_n : nullptr;
+    a.U = d.U ? static_cast<char *>(d.U) + t0 * slot_n : nullptr;
+    a.H = ws + l.h;
+    if ((e = launch_product<kGatedOut, true, BF>(a, l.rows, tiles, stream)) != hipSuccess) return e;
+    weight(0, d.down);
+    shape(d.D, d.N);
+    a.A = ws + l.h;
+    a.part = reinterpret_cast<float *>(ws + l.part);
+    if ((e = launch_product<kRowsOut, false, BF>(a, l.rows, tiles, stream)) != hipSuccess) return e;
+    const size_t row = (size_t)t0 * d.D * 2;
+    CombineArgs c = {};
+    c.ids = ids;
+    c.part = a.part;
+    c.add = d.residual ? static_cast<const char *>(d.residual) + row : nullptr;
+    c.out = static_cast<char *>(d.Y) + row;
+    c.T = T;
+    c.D = d.D;
+    c.k = d.k;
+    c.E = d.E;
+    hipLaunchKernelGGL(combine_kernel<BF>, dim3((unsigned)(((long long)T * d.D / 4 + 255) / 256)), dim3(256), 0, stream, c);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+// ---- backward launches
+
+struct GradLayout {
+  int tokens, slots, rows, tiles, columns;
+  size_t order, list, count, dg, du, dw, part, total;
+};
+GradLayout grad_layout(const ExpertsGradDesc &d) {
+  GradLayout l = {};
+  l.tokens = round_tokens(d.T, d.k, d.D);
+  l.slots = l.tokens * d.k;
+  const double mean = (double)l.slots / std::min(d.E, l.slots);
+  l.rows = mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : 128;
+  l.tiles = max_tiles(l.slots, d.E, l.rows);
+  l.columns = (d.N + 255) / 256;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += align256(bytes);
+    return here;
+  };
+  l.order = take((size_t)l.slots * 4);
+  l.list = take((size_t)l.tiles * sizeof(ExpertTile));
+  l.count = take(4);
+  l.dg = take((size_t)l.slots * d.N * 2);
+  l.du = take((size_t)l.slots * d.N * 2);
+  l.dw = take((size_t)l.slots * l.columns * 16);
+  l.part = take((size_t)l.slots * d.D * 4);
+  l.total = at;
+  return l;
+}
+
+template <int EPI, bool GATHER, bool BF>
+hipError_t launch_grad_product(ExpertGradArgs a, int rows, int tiles, hipStream_t stream) {
+  a.columns = (a.C + 255) / 256;
+  const dim3 grid((unsigned)((tiles * a.columns + 7) / 8 * 8));
+#define W4_GRAD(TM)                                                                              \
+  if (rows == 16 * TM)                                                                           \
+  hipLaunchKernelGGL((expert_grad_kernel<TM, EPI, GATHER, BF>), grid, dim3(256), 0, stream, a)
+  W4_GRAD(1);
+  W4_GRAD(2);
+  W4_GRAD(4);
+  W4_GRAD(8);
+#undef W4_GRAD
+  return hipGetLastError();
+}
+
+template <bool BF>
+hipError_t launch_experts_grad_typed(const ExpertsGradDesc &d, char *ws, hipStream_t stream) {
+  const GradLayout l = grad_layout(d);
+  for (int t0 = 0; t0 < d.T; t0 += l.tokens) {
+    const int T = std::min(l.tokens, d.T - t0), S = T * d.k;
+    const int32_t *ids = d.ids + (size_t)t0 * d.k;
+    int32_t *order = reinterpret_cast<int32_t *>(ws + l.order), *count = reinterpret_cast<int32_t *>(ws + l.count);
+    ExpertTile *list = reinterpret_cast<ExpertTile *>(ws + l.list);
+    hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, ids, S, d.E, l.rows, order, list, count);
+    const int tiles = max_tiles(S, d.E, l.rows);
+    const size_t row = (size_t)t0 * d.D * 2, slot_n = (size_t)t0 * d.k * d.N * 2;
+    ExpertGradArgs a = {};
+    a.plan = {order, list, count};
+    a.k = d.k;
+    a.tokens = T;
+    a.weights = d.weights + (size_t)t0 * d.k;
+    a.act = d.act;
+    a.code_bytes = (size_t)d.N * d.D / 2;
+    a.meta_bytes = (size_t)(d.N / kGroup) * (d.D / kGroup) * kMetaBytes;
+    a.A[0] = static_cast<const char *>(d.dY) + row;
+    a.Wt[0] = static_cast<const uint8_t *>(d.down.Wt);
+    a.meta[0] = static_cast<const uint8_t *>(d.down.meta);
+    a.R = d.D;
+    a.C = d.N;
+    a.s_down = static_cast<const _Float16 *>(d.s_down);
+    a.G = static_cast<const char *>(d.G) + slot_n;
+    a.U = static_cast<const char *>(d.U) + slot_n;
+    a.dG = ws + l.dg;
+    a.dU = ws + l.du;
+    a.dw_part = reinterpret_cast<float *>(ws + l.dw);
+    hipError_t e = launch_grad_product<kActGradOut, true, BF>(a, l.rows, tiles, stream);
+    if (e != hipSuccess) return e;
+    if (d.dweights)
+      hipLaunchKernelGGL(weight_grad_kernel<BF>, dim3((unsigned)((S + 3) / 4)), dim3(256), 0, stream, ids, a.dw_part,
+                         4 * l.columns, d.N / 64, S, d.E, static_cast<uint16_t *>(d.dweights) + (size_t)t0 * d.k);
+    if (d.dX) {
+      a.A[0] = a.dG;
+      a.A[1] = a.dU;
+      a.Wt[0] = static_cast<const uint8_t *>(d.gate.Wt);
+      a.Wt[1] = static_cast<const uint8_t *>(d.up.Wt);
+      a.meta[0] = static_cast<const uint8_t *>(d.gate.meta);
+      a.meta[1] = static_cast<const uint8_t *>(d.up.meta);
+      a.R = d.N;
+      a.C = d.D;
+      a.part = reinterpret_cast<float *>(ws + l.part);
+      if ((e = launch_grad_product<kGradRowsOut, false, BF>(a, l.rows, tiles, stream)) != hipSuccess) return e;
+      CombineArgs c = {};
+      c.ids = ids;
+      c.part = a.part;
+      c.add = d.add ? static_cast<const char *>(d.add) + row : nullptr;
+      c.s = static_cast<const _Float16 *>(d.s);
+      c.out = static_cast<char *>(d.dX) + row;
+      c.T = T;
+      c.D = d.D;
+      c.k = d.k;
+      c.E = d.E;
+      hipLaunchKernelGGL(combine_kernel<BF>, dim3((unsigned)(((long long)T * d.D / 4 + 255) / 256)), dim3(256), 0, stream, c);
+    }
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+size_t experts_grad_workspace_bytes(const ExpertsGradDesc &d) { return d.T == 0 ? 0 : grad_layout(d).total; }
+
+hipError_t launch_experts_grad(const ExpertsGradDesc &d, void *workspace, hipStream_t stream) {
+  char *ws = static_cast<char *>(workspace);
+  return d.bf16 ? launch_experts_grad_typed<true>(d, ws, stream) : launch_experts_grad_typed<false>(d, ws, stream);
+}
+
+size_t experts_workspace_bytes(const ExpertsDesc &d) { return d.T == 0 ? 0 : layout(d).total; }
+
+hipError_t launch_experts(const ExpertsDesc &d, void *workspace, hipStream_t stream) {
+  char *ws = static_cast<char *>(workspace);
+  return d.bf16 ? launch_experts_typed<true>(d, ws, stream) : launch_experts_typed<false>(d, ws, stream);
+}
+
+}  // namespace w4a16

@@ -174,6 +174,44 @@ struct RouteDesc {
 };
 hipError_t launch_route(const RouteDesc &d, bool grad, hipStream_t stream);
 
+// The experts' gated feed-forward blocks of T tokens with k slots each (validated by the
+// caller; D and N multiples of 128, E <= 1024).  A weight holds its E experts one after
+// the other: gate and up [N][D], down [D][N].
+struct ExpertWeight {
+  const void *Wq, *scales, *zeros;
+};
+struct ExpertsDesc {
+  const void *X;
+  const int32_t *ids;
+  const float *weights;
+  ExpertWeight gate, up, down;
+  const void *s, *s_down, *residual;
+  void *G, *U, *Y;
+  int T, E, k, D, N, act;
+  bool bf16;
+};
+size_t experts_workspace_bytes(const ExpertsDesc &d);
+hipError_t launch_experts(const ExpertsDesc &d, void *workspace, hipStream_t stream);
+
+// Their backward, from G and U [T][k][N], over the transposed copies of the weights, an
+// expert's after the other.  dX and dweights may each be null.
+struct ExpertTransposed {
+  const void *Wt, *meta;
+};
+struct ExpertsGradDesc {
+  const void *dY;
+  const int32_t *ids;
+  const float *weights;
+  const void *G, *U;
+  ExpertTransposed gate, up, down;
+  const void *s, *s_down, *add;
+  void *dX, *dweights;
+  int T, E, k, D, N, act;
+  bool bf16;
+};
+size_t experts_grad_workspace_bytes(const ExpertsGradDesc &d);
+hipError_t launch_experts_grad(const ExpertsGradDesc &d, void *workspace, hipStream_t stream);
+
 // Speculative-sampling verification of B sequences (validated by the caller):
 // the vocabulary is cut into spec_verify_chunks(V) chunks, and the workspace
 // (spec_verify_workspace_bytes(B, V) bytes, 256-byte aligned) holds the

@@ -10,7 +10,7 @@ rest of the package does.
 from __future__ import annotations
 
 import ctypes
-from dataclasses import dataclass, field
+from dataclasses import dataclass
 
 from . import (ACT_SILU, DTYPE_BF16, DTYPE_F16, GROUP, PackedWeight, W4A16Error, _act_dtype,
                _dev_ptr, _dtype_code, _PreparedCall, _refuse_grad, _shaped_ptr, _stream_handle, _torch,
@@ -19,7 +19,9 @@ from . import (ACT_SILU, DTYPE_BF16, DTYPE_F16, GROUP, PackedWeight, W4A16Error,
 __all__ = [
     "NORM_NONE", "NORM_RMS", "NORM_LAYER", "Norm", "NormBlockCall", "w4a16_norm_block", "NormGrads",
     "NormBlockBackwardCall", "w4a16_norm_block_backward", "SCORE_SOFTMAX", "SCORE_SIGMOID", "DTYPE_F32",
-    "Routing", "RouteCall", "w4a16_route", "RouteBackwardCall", "w4a16_route_backward",
+    "Routing", "RouteCall", "w4a16_route", "RouteBackwardCall", "w4a16_route_backward", "PackedExperts",
+    "w4a16_stack_experts", "ExpertsCall", "w4a16_experts", "TransposedExperts", "w4a16_transpose_experts",
+    "ExpertsBackwardCall", "w4a16_experts_backward",
 ]
 
 NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
@@ -56,6 +58,33 @@ class RoutingStruct(ctypes.Structure):
                 ("topk_groups", _I32), ("renormalize", _I32), ("scale", _F32), ("dtype", _I32)]
 
 
+class ExpertWeightStruct(ctypes.Structure):
+    """Mirror of the C struct w4a16_expert_weight."""
+    _fields_ = [("Wq", _VP), ("scales", _VP), ("zeros", _VP)]
+
+
+class ExpertsStruct(ctypes.Structure):
+    """Mirror of the C struct w4a16_experts_call."""
+    _fields_ = [("X", _VP), ("ids", _VP), ("weights", _VP), ("gate", ExpertWeightStruct),
+                ("up", ExpertWeightStruct), ("down", ExpertWeightStruct), ("s", _VP), ("s_down", _VP),
+                ("residual", _VP), ("G", _VP), ("U", _VP), ("Y", _VP), ("T", _I64), ("E", _I64), ("k", _I64),
+                ("D", _I64), ("N", _I64), ("act", _I32), ("dtype", _I32)]
+
+
+class ExpertTransposedStruct(ctypes.Structure):
+    """Mirror of the C struct w4a16_expert_transposed."""
+    _fields_ = [("Wt", _VP), ("meta", _VP)]
+
+
+class ExpertsBackwardStruct(ctypes.Structure):
+    """Mirror of the C struct w4a16_experts_backward_call."""
+    _fields_ = [("dY", _VP), ("ids", _VP), ("weights", _VP), ("G", _VP), ("U", _VP),
+                ("gate", ExpertTransposedStruct), ("up", ExpertTransposedStruct),
+                ("down", ExpertTransposedStruct), ("s", _VP), ("s_down", _VP), ("add", _VP), ("dX", _VP),
+                ("dweights", _VP), ("T", _I64), ("E", _I64), ("k", _I64), ("D", _I64), ("N", _I64),
+                ("act", _I32), ("dtype", _I32)]
+
+
 def _declare(L):
     """Argument types of this module's entry points (called once the library is loaded)."""
     ref, sz, cs, ci = ctypes.POINTER, ctypes.POINTER(ctypes.c_size_t), ctypes.c_size_t, ctypes.c_int
@@ -64,7 +93,11 @@ def _declare(L):
             ("w4a16_norm_block_backward_workspace_size", [ref(NormBackwardStruct), sz]),
             ("w4a16_norm_block_backward", [ref(NormBackwardStruct), _VP, cs, _VP]),
             ("w4a16_route", [ref(RoutingStruct), _VP, _VP, _VP, _VP, _VP]),
-            ("w4a16_route_backward", [ref(RoutingStruct), _VP, _VP, _VP, _VP, _VP])):
+            ("w4a16_route_backward", [ref(RoutingStruct), _VP, _VP, _VP, _VP, _VP]),
+            ("w4a16_experts_workspace_size", [ref(ExpertsStruct), sz]),
+            ("w4a16_experts", [ref(ExpertsStruct), _VP, cs, _VP]),
+            ("w4a16_experts_backward_workspace_size", [ref(ExpertsBackwardStruct), sz]),
+            ("w4a16_experts_backward", [ref(ExpertsBackwardStruct), _VP, cs, _VP])):
         getattr(L, name).argtypes = args
         getattr(L, name).restype = ci
 
@@ -297,3 +330,175 @@ def w4a16_route_backward(dweights, logits, ids, routing):
     dlogits = _torch().empty_like(logits)
     RouteBackwardCall(dweights, logits, ids, routing, dlogits)()
     return dlogits
+
+
+# ---- experts ---------------------------------------------------------------------------------
+
+@dataclass
+class PackedExperts:
+    """E packed INT4 weights [N][K] of one shape, one after the other in each buffer (the buffers
+    of PackedWeight, E times as long)."""
+    wq: "object"
+    scales: "object"
+    zeros: "object"
+    E: int
+    N: int
+    K: int
+
+
+def w4a16_stack_experts(weights) -> PackedExperts:
+    """PackedExperts of a list of PackedWeight (INT4 codes, one shape, no fp16 outliers)."""
+    torch = _torch()
+    weights = list(weights)
+    if not weights:
+        raise ValueError("at least one expert")
+    first = weights[0]
+    for w in weights:
+        if (w.N, w.K, w.wbits) != (first.N, first.K, 4):
+            raise ValueError("experts must be INT4 weights of one shape")
+        if w.outlier_ptrs()[0] is not None:
+            raise ValueError("experts take no fp16 outliers")
+    return PackedExperts(*(torch.cat([getattr(w, n) for w in weights]) for n in ("wq", "scales", "zeros")),
+                         len(weights), first.N, first.K)
+
+
+def _expert_struct(w, name, shape, device):
+    torch = _torch()
+    if (w.E, w.N, w.K) != shape:
+        raise ValueError(f"{name} must be {shape[0]} experts of [{shape[1]}][{shape[2]}]")
+    meta = (w.E * w.N * (-(-(w.K // GROUP) // 4) * 4),)
+    return ExpertWeightStruct(
+        _shaped_ptr(w.wq, f"{name}.wq", torch.uint8, (w.E * w.N * w.K // 2,), device),
+        _shaped_ptr(w.scales, f"{name}.scales", torch.float16, meta, device),
+        _shaped_ptr(w.zeros, f"{name}.zeros", torch.float16, meta, device))
+
+
+def _slots_ptrs(ids, weights, T, device):
+    torch = _torch()
+    if ids.dim() != 2:
+        raise ValueError("ids must be [T][k]")
+    k = ids.shape[1]
+    return k, (_shaped_ptr(ids, "ids", torch.int32, (T, k), device),
+               _shaped_ptr(weights, "weights", torch.float32, (T, k), device))
+
+
+class ExpertsCall(_PreparedCall):
+    """A prepared w4a16_experts call: Y = residual + the weighted sum of each token's experts,
+    act(G) * U through down, G and U the products of X * s with gate and up.
+
+    X, Y and residual (or None; may be Y) [T][D] are fp16 or bf16; ids int32 and weights fp32
+    [T][k] as w4a16_route gives them (an id outside 0..E-1: the slot adds nothing); gate, up
+    [N][D] and down [D][N] PackedExperts; s fp16 [D] and s_down fp16 [E][N] or None; preact: a
+    pair of [T][k][N] tensors that receive G and U, or None."""
+
+    def __init__(self, X, ids, weights, gate, up, down, Y, s=None, s_down=None, act=ACT_SILU, residual=None,
+                 preact=None, stream=None, workspace=None):
+        torch = _torch()
+        dt, device = _act_dtype(X, "X"), X.device
+        if X.dim() != 2:
+            raise ValueError("X must be [T][D]")
+        (T, D), E, N = X.shape, gate.E, gate.N
+        k, slots = _slots_ptrs(ids, weights, T, device)
+        G, U = preact if preact is not None else (None, None)
+        self.keep = (X, ids, weights, gate, up, down, Y, s, s_down, residual, G, U)
+        self.call = ExpertsStruct(
+            _dev_ptr(X, "X", dt), *slots, _expert_struct(gate, "gate", (E, N, D), device),
+            _expert_struct(up, "up", (E, N, D), device), _expert_struct(down, "down", (E, D, N), device),
+            _shaped_ptr(s, "s", torch.float16, (D,), device),
+            _shaped_ptr(s_down, "s_down", torch.float16, (E, N), device),
+            _shaped_ptr(residual, "residual", dt, (T, D), device),
+            _shaped_ptr(G, "preact[0]", dt, (T, k, N), device), _shaped_ptr(U, "preact[1]", dt, (T, k, N), device),
+            _shaped_ptr(Y, "Y", dt, (T, D), device), T, E, k, D, N, act, _dtype_code(dt))
+        nbytes = self._size("w4a16_experts_workspace_size", ctypes.byref(self.call))
+        self._prepare(device, nbytes, workspace, stream)
+        self._bind("w4a16_experts", ctypes.byref(self.call))
+
+
+def w4a16_experts(X, ids, weights, gate, up, down, s=None, s_down=None, act=ACT_SILU, residual=None, out=None,
+                  preact=None):
+    """The weighted sum of each token's experts on the current stream.  Arguments as for
+    ExpertsCall."""
+    if out is None:
+        out = _torch().empty_like(X)
+    ExpertsCall(X, ids, weights, gate, up, down, out, s, s_down, act, residual, preact)()
+    return out
+
+
+@dataclass
+class TransposedExperts:
+    """Transposed copies of PackedExperts for the backward pass, one expert after the other in
+    each buffer (layout: w4a16_transpose in include/w4a16.h)."""
+    wt: "object"
+    meta: "object"
+    E: int
+    N: int
+    K: int
+
+
+def w4a16_transpose_experts(w: PackedExperts) -> TransposedExperts:
+    """The transposed copies that w4a16_experts_backward reads, made once per weight (on the
+    current stream)."""
+    torch = _torch()
+    a, b = ctypes.c_size_t(), ctypes.c_size_t()
+    rc = lib().w4a16_transposed_sizes(w.N, w.K, 4, ctypes.byref(a), ctypes.byref(b))
+    if rc:
+        raise W4A16Error(rc, "w4a16_transposed_sizes")
+    dev = w.wq.device
+    src = _expert_struct(w, "experts", (w.E, w.N, w.K), dev)
+    out = TransposedExperts(torch.empty(w.E * a.value, dtype=torch.uint8, device=dev),
+                            torch.empty(w.E * b.value, dtype=torch.uint8, device=dev), w.E, w.N, w.K)
+    codes, meta = w.N * w.K // 2, w.N * (-(-(w.K // GROUP) // 4) * 4) * 2
+    with torch.cuda.device(dev):
+        for e in range(w.E):
+            rc = lib().w4a16_transpose(src.Wq + e * codes, src.scales + e * meta, src.zeros + e * meta, w.N, w.K,
+                                       4, out.wt.data_ptr() + e * a.value, out.meta.data_ptr() + e * b.value,
+                                       _stream_handle(dev))
+            if rc:
+                raise W4A16Error(rc, "w4a16_transpose")
+    return out
+
+
+def _transposed_struct(w, name, shape, device):
+    torch = _torch()
+    if (w.E, w.N, w.K) != shape:
+        raise ValueError(f"{name} must be {shape[0]} transposed experts of [{shape[1]}][{shape[2]}]")
+    rows = -(-w.N // GROUP)
+    return ExpertTransposedStruct(
+        _shaped_ptr(w.wt, f"{name}.wt", torch.uint8, (w.E * rows * GROUP * w.K // 2,), device),
+        _shaped_ptr(w.meta, f"{name}.meta", torch.uint8, (w.E * rows * (w.K // GROUP) * 512,), device))
+
+
+class ExpertsBackwardCall(_PreparedCall):
+    """A prepared w4a16_experts_backward call: dX [T][D] (or None) and dweights [T][k] (or None), of
+    the activations' type, from dY, the routing and the G and U of the forward; gate, up and
+    down TransposedExperts; add [T][D] (or None; may be dX) is added to dX."""
+
+    def __init__(self, dY, ids, weights, G, U, gate, up, down, dX, dweights, s=None, s_down=None, act=ACT_SILU,
+                 add=None, stream=None, workspace=None):
+        torch = _torch()
+        dt, device = _act_dtype(dY, "dY"), dY.device
+        if dY.dim() != 2:
+            raise ValueError("dY must be [T][D]")
+        (T, D), E, N = dY.shape, gate.E, gate.N
+        k, slots = _slots_ptrs(ids, weights, T, device)
+        self.keep = (dY, ids, weights, G, U, gate, up, down, dX, dweights, s, s_down, add)
+        self.call = ExpertsBackwardStruct(
+            _dev_ptr(dY, "dY", dt), *slots, _shaped_ptr(G, "G", dt, (T, k, N), device),
+            _shaped_ptr(U, "U", dt, (T, k, N), device), _transposed_struct(gate, "gate", (E, N, D), device),
+            _transposed_struct(up, "up", (E, N, D), device), _transposed_struct(down, "down", (E, D, N), device),
+            _shaped_ptr(s, "s", torch.float16, (D,), device),
+            _shaped_ptr(s_down, "s_down", torch.float16, (E, N), device),
+            _shaped_ptr(add, "add", dt, (T, D), device), _shaped_ptr(dX, "dX", dt, (T, D), device),
+            _shaped_ptr(dweights, "dweights", dt, (T, k), device), T, E, k, D, N, act, _dtype_code(dt))
+        nbytes = self._size("w4a16_experts_backward_workspace_size", ctypes.byref(self.call))
+        self._prepare(device, nbytes, workspace, stream)
+        self._bind("w4a16_experts_backward", ctypes.byref(self.call))
+
+
+def w4a16_experts_backward(dY, ids, weights, G, U, gate, up, down, s=None, s_down=None, act=ACT_SILU, add=None):
+    """Backward of w4a16_experts on the current stream: (dX, dweights).  Arguments as for
+    ExpertsBackwardCall."""
+    torch = _torch()
+    dX, dw = torch.empty_like(dY), torch.empty(ids.shape, dtype=dY.dtype, device=dY.device)
+    ExpertsBackwardCall(dY, ids, weights, G, U, gate, up, down, dX, dw, s, s_down, act, add)()
+    return dX, dw
