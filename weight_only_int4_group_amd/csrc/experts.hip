@@ -55,14 +55,20 @@ __device__ __forceinline__ float4v mfma(u32x4 a, u32x4 b, float4v c) {
 // the MFMA's sum minus (c + z) xs, in fp32.
 template <bool BF>
 constexpr float kCodeBase = BF ? 128.f : 64.f;
+// (No inline assembly here: an MFMA may read a register only two wait states after a
+// vector instruction wrote it, and the compiler sees to that for its own instructions alone.)
+// Part p of it: columns 2p and 2p + 1.
+template <bool BF>
+__device__ __forceinline__ uint32_t code_part(uint32_t w, int p) {
+  constexpr uint32_t mask = BF ? 0x000F000Fu : 0x00F000F0u, base = BF ? kMagicBF : 0x54005400u;
+  const uint32_t x = BF ? w >> (4 * p) : p ? w >> (4 * p - 4) : w << 4;
+  // (x & mask) | base as one instruction (bit by bit, 0xEA is the truth table); written with
+  // operators it becomes two
+  return (uint32_t)__builtin_amdgcn_bitop3_b32(x, mask, base, 0xEA);
+}
 template <bool BF>
 __device__ __forceinline__ u32x4 code_operand(uint32_t w) {
-  if constexpr (BF)
-    return (u32x4){and_or(w, 0x000F000Fu, kMagicBF), and_or(w >> 4, 0x000F000Fu, kMagicBF),
-                   and_or(w >> 8, 0x000F000Fu, kMagicBF), and_or(w >> 12, 0x000F000Fu, kMagicBF)};
-  else
-    return (u32x4){and_or(w << 4, 0x00F000F0u, 0x54005400u), and_or(w, 0x00F000F0u, 0x54005400u),
-                   and_or(w >> 4, 0x00F000F0u, 0x54005400u), and_or(w >> 8, 0x00F000F0u, 0x54005400u)};
+  return (u32x4){code_part<BF>(w, 0), code_part<BF>(w, 1), code_part<BF>(w, 2), code_part<BF>(w, 3)};
 }
 template <bool BF>
 __device__ __forceinline__ u32x4 ones_operand() {
@@ -73,7 +79,9 @@ __device__ __forceinline__ u32x4 ones_operand() {
 // ---- the plan -------------------------------------------------------------------------
 
 struct ExpertTile {
-  int expert, row0, rows, unused;  // sorted rows row0 .. row0 + rows - 1
+  int expert, row0, rows;  // sorted rows row0 .. row0 + rows - 1
+  int first, count;        // the expert's tiles
+  int pad[3];
 };
 struct Plan {
   const int32_t *order;      // [S] slots, sorted by expert (those that name one)
@@ -117,7 +125,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int32_t *ids, 
   const int first = a - rows;
   at[t] = first;
   for (int i = 0; i < mine; ++i)
-    tiles[b - mine + i] = {t, first + i * tile_rows, min(tile_rows, rows - i * tile_rows), 0};
+    tiles[b - mine + i] = {t, first + i * tile_rows, min(tile_rows, rows - i * tile_rows), b - mine, mine, {}};
   if (t == kPlanThreads - 1) *tile_count = b;
   __syncthreads();
   for (int i = t; i < S; i += kPlanThreads) {
@@ -150,48 +158,105 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void *p, size_t
   return __builtin_amdgcn_make_buffer_rsrc((void *)p, (short)0, (int)min((size_t)0x7fffffff, bytes), kRsrcWord3);
 }
 
-// (tile, column block) of workgroup `block`: the active workgroups are renumbered so that
-// each XCD (they go round the eight) takes one run of them, whose neighbours share an
-// expert's weights and rows in its L2.  false: past the last tile.
-__device__ __forceinline__ bool place(const Plan &plan, int columns, int block, int &tile, int &column) {
+// The tile and column block of workgroup `block` (false: past the last).  The active
+// workgroups are renumbered so that each XCD (they go round the eight) takes one run of them,
+// and within an expert the tiles of one column block are neighbours, which share its
+// weights in the XCD's L2.
+__device__ __forceinline__ bool place(const Plan &plan, int columns, int block, ExpertTile &tile, int &column) {
   const int total = uniform_int(*plan.count) * columns, run = (total + 7) >> 3;
   const int local = (block & 7) * run + (block >> 3);
   if ((block >> 3) >= run || local >= total) return false;
-  tile = local / columns;
-  column = local - tile * columns;
+  const ExpertTile &any = plan.tiles[local / columns];  // (of the same expert)
+  const int first = uniform_int(any.first), count = uniform_int(any.count), at = local - first * columns;
+  column = at / count;
+  const ExpertTile &t = plan.tiles[first + at - column * count];
+  tile = {uniform_int(t.expert), uniform_int(t.row0), uniform_int(t.rows), first, count, {}};
   return true;
 }
 
-__device__ __forceinline__ ExpertTile tile_at(const Plan &plan, int tile) {
-  const ExpertTile t = plan.tiles[tile];
-  return {uniform_int(t.expert), uniform_int(t.row0), uniform_int(t.rows), 0};
+// A wave's 16 x 64 fp32 sums go through 4 KB of its own LDS on their way out, so that a
+// lane has neighbouring columns of one row and stores 16 bytes of them: straight from
+// the MFMA's layout, 16 columns of 4 bytes at a time, the down product of 32768 slots of
+// 4096 (1024 deep) took 700 us, and 390 us this way.  Column blocks of 16 are swapped by row
+// (XOR with row / 4 % 4), so that the four rows that a write touches lie in different banks.
+__device__ __forceinline__ int staged(int row, int col) { return row * 64 + (col ^ ((row >> 2 & 3) * 16)); }
+__device__ __forceinline__ void stage_block(float *stage, int j, int c, int r, float4v x) {
+#pragma unroll
+  for (int v = 0; v < 4; ++v) stage[staged(4 * c + v, 16 * j + r)] = x[v];
 }
+// (the lanes of a wave write, then read: their LDS operations stay in order)
+__device__ __forceinline__ void stage_done() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 
-// Stores a 16 x 16 block of G and U: row 4 c + v of rows row .. of the tile, column n.
 template <bool BF>
-__device__ __forceinline__ void store_gated(const ExpertArgs &P, const ExpertTile &tile, int row, int n, float4v g,
-                                            float4v u) {
-  const float sd = P.s_down ? (float)P.s_down[(size_t)tile.expert * P.N + n] : 1.f;
+__device__ __forceinline__ u32x4 pack8(const float4v &a, const float4v &b) {
+  u32x4 o;
 #pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    if (row + v >= tile.rows) continue;
-    const size_t at = (size_t)(tile.row0 + row + v);
-    if (P.G) {
-      const size_t slot = (size_t)P.plan.order[at] * P.N + n;
-      static_cast<uint16_t *>(P.G)[slot] = f32_to_act<BF>(g[v]);
-      static_cast<uint16_t *>(P.U)[slot] = f32_to_act<BF>(u[v]);
-    }
-    static_cast<uint16_t *>(P.H)[at * P.N + n] = f32_to_act<BF>(act_value(g[v], P.act) * u[v] * sd);
+  for (int q = 0; q < 2; ++q) {
+    o[q] = (uint32_t)f32_to_act<BF>(a[2 * q]) | (uint32_t)f32_to_act<BF>(a[2 * q + 1]) << 16;
+    o[2 + q] = (uint32_t)f32_to_act<BF>(b[2 * q]) | (uint32_t)f32_to_act<BF>(b[2 * q + 1]) << 16;
   }
+  return o;
 }
 
-__device__ __forceinline__ void store_rows(const ExpertArgs &P, const ExpertTile &tile, int row, int n, float4v y) {
+// The wave's 16 x 32 block of 16-bit values (two 16-column blocks of x in fp32) of rows row0 ..
+// of the tile, columns n0 ..: each lane 8 columns of one row.  ROW(row) is the row's address.
+template <bool BF, typename ROW>
+__device__ __forceinline__ void store_16x32(float *stage, int lane, int row0, int rows, const float4v (&x)[2], ROW &&row) {
+  const int c = lane >> 4, r = lane & 15;
+  stage_block(stage, 0, c, r, x[0]);
+  stage_block(stage, 1, c, r, x[1]);
+  stage_done();
+  const int m = lane >> 2, n = 8 * (lane & 3);
+  const float4v a = *reinterpret_cast<const float4v *>(stage + staged(m, n));
+  const float4v b = *reinterpret_cast<const float4v *>(stage + staged(m, n + 4));
+  stage_done();
+  if (row0 + m < rows) *reinterpret_cast<u32x4 *>(row(row0 + m) + n) = pack8<BF>(a, b);
+}
+
+// 16 rows of G and U (and H from them), 32 columns from n0: g and u hold two 16-column
+// blocks each.
+template <bool BF>
+__device__ __forceinline__ void store_gated(const ExpertArgs &P, const ExpertTile &tile, float *stage, int lane, int row0,
+                                            int n0, const float4v (&g)[2], const float4v (&u)[2]) {
+  const int r = lane & 15;
+  float4v h[2];
 #pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    if (row + v >= tile.rows) continue;
-    const int slot = P.plan.order[tile.row0 + row + v];
-    P.part[(size_t)slot * P.N + n] = y[v] * P.weights[slot];
+  for (int j = 0; j < 2; ++j) {
+    const float sd = P.s_down ? (float)P.s_down[(size_t)tile.expert * P.N + n0 + 16 * j + r] : 1.f;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) h[j][v] = act_value(g[j][v], P.act) * u[j][v] * sd;
   }
+  store_16x32<BF>(stage, lane, row0, tile.rows, h, [&](int m) {
+    return static_cast<uint16_t *>(P.H) + (size_t)(tile.row0 + m) * P.N + n0;
+  });
+  if (!P.G) return;
+  auto slot = [&](void *p) {
+    return [=, &P](int m) { return static_cast<uint16_t *>(p) + (size_t)P.plan.order[tile.row0 + m] * P.N + n0; };
+  };
+  store_16x32<BF>(stage, lane, row0, tile.rows, g, slot(P.G));
+  store_16x32<BF>(stage, lane, row0, tile.rows, u, slot(P.U));
+}
+
+// 16 rows of a slot's contribution, 16 BLOCKS columns from n0, times the slot's weight (or as
+// they are: weights null), in fp32.
+template <int BLOCKS>
+__device__ __forceinline__ void store_rows(const Plan &plan, const float *weights, float *part, int N, const ExpertTile &tile,
+                                           float *stage, int lane, int row0, int n0, const float4v (&y)[BLOCKS]) {
+  constexpr int kLanes = 4 * BLOCKS, kRows = 64 / kLanes;  // lanes along a row, rows at a time
+#pragma unroll
+  for (int j = 0; j < BLOCKS; ++j) stage_block(stage, j, lane >> 4, lane & 15, y[j]);
+  stage_done();
+  const int n = 4 * (lane % kLanes);
+#pragma unroll
+  for (int q = 0; q < 16 / kRows; ++q) {
+    const int m = kRows * q + lane / kLanes;
+    if (row0 + m >= tile.rows) continue;
+    const int slot = plan.order[tile.row0 + row0 + m];
+    float4v x = *reinterpret_cast<const float4v *>(stage + staged(m, n));
+    if (weights) x *= weights[slot];
+    *reinterpret_cast<float4v *>(part + (size_t)slot * N + n0 + n) = x;
+  }
+  stage_done();
 }
 
 // ---- few rows per expert: streaming -----------------------------------------------------------
@@ -206,9 +271,10 @@ __global__ __launch_bounds__(64 * KS) void expert_stream_kernel(ExpertArgs P) {
   constexpr int DEPTH = TN == 2 ? 4 : 2;
   constexpr int STEP = EPI == kGatedOut ? 2 : 1;
   __shared__ float4v red[KS][TN][64];
-  int tile_i, column;
-  if (!place(P.plan, P.columns, blockIdx.x, tile_i, column)) return;
-  const ExpertTile tile = tile_at(P.plan, tile_i);
+  __shared__ __attribute__((aligned(16))) float stage[TN / (2 * STEP)][1024];
+  ExpertTile tile;
+  int column;
+  if (!place(P.plan, P.columns, blockIdx.x, tile, column)) return;
   const int lane = threadIdx.x & 63, wave = uniform_int(threadIdx.x >> 6), c = lane >> 4, r = lane & 15;
   const int K = P.K, N = P.N, G = K / kGroup, NB = N / kTileRows;
   const int vb0 = column * TN;  // first row block (gated: of the alternating ones)
@@ -280,21 +346,22 @@ __global__ __launch_bounds__(64 * KS) void expert_stream_kernel(ExpertArgs P) {
 #pragma unroll
   for (int j = 0; j < TN; ++j) red[wave][j][lane] = acc[j];
   __syncthreads();
-  for (int p = wave; p < TN / STEP; p += KS) {
-    float4v y[STEP];
+  // waves 0 .. finish 32 columns each (gated: of H, from 64 sums)
+  constexpr int OUT = 2 * STEP;
+  if (wave >= TN / OUT) return;
+  float4v y[OUT];
 #pragma unroll
-    for (int i = 0; i < STEP; ++i) {
-      y[i] = red[0][STEP * p + i][lane];
+  for (int i = 0; i < OUT; ++i) {
+    y[i] = red[0][OUT * wave + i][lane];
 #pragma unroll
-      for (int w = 1; w < KS; ++w) y[i] += red[w][STEP * p + i][lane];
-    }
-    const int n = (vb0 / STEP + p) * kTileRows + r;
-    if (n >= N) continue;
-    if constexpr (EPI == kGatedOut)
-      store_gated<BF>(P, tile, 4 * c, n, y[0], y[STEP - 1]);
-    else
-      store_rows(P, tile, 4 * c, n, y[0]);
+    for (int w = 1; w < KS; ++w) y[i] += red[w][OUT * wave + i][lane];
   }
+  const int n0 = (vb0 + OUT * wave) / STEP * kTileRows;
+  if (n0 >= N) return;  // (N is a multiple of 128: all 32 columns are there)
+  if constexpr (EPI == kGatedOut)
+    store_gated<BF>(P, tile, stage[wave], lane, 0, n0, {y[0], y[2]}, {y[1], y[3]});
+  else
+    store_rows<2>(P.plan, P.weights, P.part, N, tile, stage[wave], lane, 0, n0, {y[0], y[1]});
 }
 
 // ---- many rows per expert: LDS tiles -----------------------------------------------------------
@@ -314,11 +381,14 @@ template <int TM, int EPI, bool GATHER, bool BF>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void expert_tile_kernel(ExpertArgs P) {
   constexpr int TN = 4, BM = 16 * TM, STEP = EPI == kGatedOut ? 2 : 1;
   constexpr int kRowChunks = kGroup / 8, kDma = BM * kRowChunks / 256;  // DMA loads per wave and stage (TM)
-  __shared__ __attribute__((aligned(16))) _Float16 As[2][BM * kGroup];
-  __shared__ float4v Xs[2][BM / 4];
-  int tile_i, column;
-  if (!place(P.plan, P.columns, blockIdx.x, tile_i, column)) return;
-  const ExpertTile tile = tile_at(P.plan, tile_i);
+  // (an array for each buffer: from one array the compiler cannot tell the buffer that is
+  // read from the one that a DMA load in flight writes, and waits for the load)
+  __shared__ __attribute__((aligned(16))) _Float16 As0[BM * kGroup], As1[BM * kGroup];
+  __shared__ float4v Xs0[BM / 4], Xs1[BM / 4];
+  __shared__ __attribute__((aligned(16))) float stage[4][1024];
+  ExpertTile tile;
+  int column;
+  if (!place(P.plan, P.columns, blockIdx.x, tile, column)) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform_int(tid >> 6), c = lane >> 4, r = lane & 15;
   const int K = P.K, N = P.N, G = K / kGroup, NB = N / kTileRows;
 
@@ -344,7 +414,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     for (int u = 0; u < kDma; ++u) {
       const int vo = GATHER ? aoff[GATHER ? u : 0] : aoff[0] + 32 * u * K;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          ars, (__attribute__((address_space(3))) void *)(&As[buf][(u * 4 + wave) * 64 * 8]), 16, vo,
+          ars, (__attribute__((address_space(3))) void *)((buf ? As1 : As0) + (u * 4 + wave) * 64 * 8), 16, vo,
           g * kGroup * 2, 0, 0);
     }
   };
@@ -358,109 +428,162 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   }
   const int vb0 = (column * 4 + wave) * TN;
   const int tile_stride = NB * kTileBytes, meta_stride = NB * kTileRows * kMetaQuad * 2;
-  struct BStage {
-    u32x4 code[TN];
-    uint32_t sc[TN], zp[TN];
+  struct Codes {
+    u32x4 w[TN];
   };
-  auto load_b = [&](int g, BStage &b) {
+  uint32_t sc[TN], zp[TN];  // raw fp16 scale and zero point of the latest group
+  auto load_codes = [&](int g, Codes &b) {
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
       const int rb = min(vb0 + j, STEP * NB - 1) / STEP;
-      b.code[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                wrs[j % STEP], lane * 16, g * tile_stride + rb * kTileBytes, 0));
+      b.w[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                             wrs[j % STEP], lane * 16, g * tile_stride + rb * kTileBytes, 0));
+    }
+  };
+  auto load_meta = [&](int g) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      const int rb = min(vb0 + j, STEP * NB - 1) / STEP;
       const int qo = (g / kMetaQuad) * meta_stride + (rb * kTileRows * kMetaQuad + g % kMetaQuad) * 2;
-      b.sc[j] = __builtin_amdgcn_raw_buffer_load_b16(srs[j % STEP], r * kMetaQuad * 2, qo, 0);
-      b.zp[j] = __builtin_amdgcn_raw_buffer_load_b16(zrs[j % STEP], r * kMetaQuad * 2, qo, 0);
+      sc[j] = __builtin_amdgcn_raw_buffer_load_b16(srs[j % STEP], r * kMetaQuad * 2, qo, 0);
+      zp[j] = __builtin_amdgcn_raw_buffer_load_b16(zrs[j % STEP], r * kMetaQuad * 2, qo, 0);
     }
   };
 
-  float4v acc[TM][TN];
+  constexpr int kTiles = TM * TN;
+  float4v acc[kTiles], p[kTiles];  // 16 x 16 block TN i + j: the sum, and the latest group's product
 #pragma unroll
-  for (int j = 0; j < TN; ++j)
-#pragma unroll
-    for (int i = 0; i < TM; ++i) acc[i][j] = float4v{0.f, 0.f, 0.f, 0.f};
-  // a group's zero points, from its stage b and the row sums in LDS
-  auto take_zero_points = [&](const BStage &b, int buf) {
-    float zs[TN];
-#pragma unroll
-    for (int j = 0; j < TN; ++j)
-      zs[j] = (float)__builtin_bit_cast(_Float16, (uint16_t)b.sc[j]) *
-              (kCodeBase<BF> + (float)__builtin_bit_cast(_Float16, (uint16_t)b.zp[j]));
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      const float4v xs = Xs[buf][4 * i + c];
-#pragma unroll
-      for (int j = 0; j < TN; ++j)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(-zs[j], xs[v], acc[i][j][v]);
-    }
-  };
-  auto compute = [&](const BStage &b, int buf) {
-    float4v p[TM][TN], xs = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int tt = 0; tt < 4; ++tt) {
-      const int pc = (4 * tt + c) ^ r;
-      u32x4 bop[TN];
-#pragma unroll
-      for (int j = 0; j < TN; ++j) bop[j] = code_operand<BF>(b.code[j][tt]);
-#pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        const u32x4 a = *reinterpret_cast<const u32x4 *>(&As[buf][(16 * i + r) * kGroup + 8 * pc]);
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-          p[i][j] = mfma<BF>(a, bop[j], tt ? p[i][j] : float4v{0.f, 0.f, 0.f, 0.f});
-      }
-      if (TM == 4 || wave < TM) {
-        const u32x4 a = *reinterpret_cast<const u32x4 *>(&As[buf][(16 * wave + r) * kGroup + 8 * pc]);
-        xs = mfma<BF>(a, ones_operand<BF>(), xs);
-      }
-    }
+  for (int t = 0; t < kTiles; ++t) acc[t] = p[t] = float4v{0.f, 0.f, 0.f, 0.f};
+  u32x4 bop[2][TN];  // operands of this k step and the next
+  float scale[TN], zs[TN];  // of the group before: scale, scale * (base + zero point)
+  auto take_meta = [&]() {
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
-      const float sc = (float)__builtin_bit_cast(_Float16, (uint16_t)b.sc[j]);
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(sc, p[i][j][v], acc[i][j][v]);
+      scale[j] = (float)__builtin_bit_cast(_Float16, (uint16_t)sc[j]);
+      zs[j] = scale[j] * (kCodeBase<BF> + (float)__builtin_bit_cast(_Float16, (uint16_t)zp[j]));
     }
-    if ((TM == 4 || wave < TM) && r == 0) Xs[buf][4 * wave + c] = xs;
   };
-  // One group per step: wait until this group's loads (issued a step ago) and the sums of
-  // the group before are in LDS and every wave is past the previous step, issue the
-  // next group's loads, compute.  Past the range they re-read the last group.
-  BStage b0, b1;
-  auto step = [&](int g, BStage &cur, BStage &nxt, int buf) {
+  // element n (of 4 kTiles) of the zero points' share, row blocks in order
+  auto take_zero = [&](int n, const float4v &xs) {
+    const int i = n / (4 * TN), j = n / 4 % TN, v = n % 4;
+    acc[TN * i + j][v] = __builtin_fmaf(-zs[j], xs[v], acc[TN * i + j][v]);
+  };
+
+  // One group per step: wait until this group's loads (issued a step ago) and the row sums
+  // of the group before are in LDS and every wave is past the previous step, issue the next
+  // group's loads, multiply.  Past the range they re-read the last group.
+  //
+  // An MFMA runs for 16 cycles and takes 4 to issue; only vector instructions that stand right
+  // behind it run meanwhile (16 MFMAs and 48 FMAs take 141 ns in turn by threes, 124 ns without the
+  // FMAs, and 226 ns one after the other, with one to four waves on the SIMD).  So each MFMA
+  // comes with its share of the rest, held in place by scheduling barriers: in the first k
+  // step the block's sum takes the product of the group before (4 FMAs), just before that
+  // product's registers are written again; in the others, the zero points' share of that
+  // group (2, 1 and 1 FMAs); in all, part of the next k step's operands (7 instructions for 4).
+  auto step = [&](int g, Codes &cur, Codes &nxt, int buf) {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    take_meta();
     const int gn = min(g + 1, G - 1);
+    load_codes(gn, nxt);
     load_a(gn, buf ^ 1);
-    if (g > 0) take_zero_points(nxt, buf ^ 1);  // (nxt still holds the group before)
-    load_b(gn, nxt);
-    compute(cur, buf);
+    // (LDS addresses are formed again in every step: kept, they would take the registers
+    // that the operands need)
+    int ln = lane;
+    asm volatile("" : "+v"(ln));
+    const int sc_ = ln >> 4, sr = ln & 15, first = (sr * kGroup + 8 * (sc_ ^ sr)) * 2;
+    const char *as = reinterpret_cast<const char *>(buf ? As1 : As0);
+    auto read_a = [&](int n) {  // k step n / TM, row block n % TM: chunk (4 tt + c) ^ r of row r
+      return *reinterpret_cast<const u32x4 *>(as + ((first ^ (64 * (n / TM))) + 32 * kGroup * (n % TM)));
+    };
+    u32x4 a[3], own;  // two row blocks ahead; the row block whose sums this wave takes
+    a[0] = read_a(0);
+    a[1] = read_a(1);
+    float4v xs_prev, xs_next, xs = {0.f, 0.f, 0.f, 0.f};
+    auto xs_of = [&](int i, int b) { return (b ? Xs1 : Xs0)[4 * i + sc_]; };
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int tt = 0; tt < 4; ++tt) {
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+        const int i = t / TN, j = t % TN, n = TM * tt + i;
+        if (tt == 0) {
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[t][v] = __builtin_fmaf(scale[j], p[t][v], acc[t][v]);
+        }
+        if (j == 0 && n + 2 < 4 * TM) a[(n + 2) % 3] = read_a(n + 2);
+        if (t == kTiles / 2)
+          own = *reinterpret_cast<const u32x4 *>(as + ((first ^ (64 * tt)) + 32 * kGroup * (wave % TM)));
+        if (tt == 1 && t == 0) load_meta(g);
+        if (tt == 0 && t == kTiles - TN) xs_prev = xs_of(0, buf ^ 1);
+        p[t] = mfma<BF>(a[n % 3], bop[tt & 1][j], tt ? p[t] : float4v{0.f, 0.f, 0.f, 0.f});
+        // the next k step's operands, 16 words of them over the step's MFMAs
+#pragma unroll
+        for (int q = 0; q < 16 / kTiles; ++q) {
+          const int m = t * (16 / kTiles) + q;
+          bop[(tt + 1) & 1][m / 4][m % 4] =
+              code_part<BF>(tt < 3 ? cur.w[m / 4][tt < 3 ? tt + 1 : 0] : nxt.w[m / 4][0], m % 4);
+        }
+        // the zero points' share: half of it, then a quarter each
+        if (tt > 0) {
+          constexpr int kPer = 4 * TN;
+          const int n0 = tt == 1 ? 2 * t : kTiles * tt + t, nn = tt == 1 ? 2 : 1;
+#pragma unroll
+          for (int q = 0; q < nn; ++q) {
+            const int e = n0 + q;
+            if (e % kPer == 0 && e > 0) xs_prev = xs_next;
+            if (e % kPer == kPer / 2 && e / kPer + 1 < TM) xs_next = xs_of(e / kPer + 1, buf ^ 1);
+            take_zero(e, xs_prev);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      xs = mfma<BF>(own, ones_operand<BF>(), xs);
+    }
+    (buf ? Xs1 : Xs0)[4 * (wave % TM) + sc_] = xs;  // (the same from all 16 lanes of a row, and every TM-th wave)
   };
+  Codes c0, c1;
+#pragma unroll
+  for (int j = 0; j < TN; ++j) sc[j] = zp[j] = 0;
+  if (tid < BM / 4) Xs1[tid] = float4v{0.f, 0.f, 0.f, 0.f};  // (before the first group: 0 times 0)
+  load_codes(0, c0);
   load_a(0, 0);
-  load_b(0, b0);
-  for (int g = 0; g < G; g += 2) {
-    step(g, b0, b1, 0);
-    if (g + 1 < G) step(g + 1, b1, b0, 1);
+#pragma unroll
+  for (int m = 0; m < 16; ++m) bop[0][m / 4][m % 4] = code_part<BF>(c0.w[m / 4][0], m % 4);
+  // (no branch between the two steps, or what the second alone uses is moved out of the first)
+  int g = 0;
+  for (; g + 1 < G; g += 2) {
+    step(g, c0, c1, 0);
+    step(g + 1, c1, c0, 1);
   }
+  if (g < G) step(g, c0, c1, 0);
   // (the last step's DMA must land before the workgroup's LDS is released)
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  take_zero_points(b0, (G - 1) & 1);  // (both stages hold the last group)
+  take_meta();
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const float4v xs = ((G - 1) & 1 ? Xs1 : Xs0)[4 * i + c];
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        acc[TN * i + j][v] = __builtin_fmaf(scale[j], p[TN * i + j][v], acc[TN * i + j][v]);
+        take_zero(4 * (TN * i + j) + v, xs);
+      }
+  }
 
   // (the lane's place again, rather than in registers through the loop)
   const int at = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+  const int n0 = vb0 / STEP * kTileRows;
+  if (n0 >= N) return;  // (N is a multiple of 128: a wave's columns are all there or none)
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
     if (16 * i >= tile.rows) break;
-#pragma unroll
-    for (int j = 0; j < TN; j += STEP) {
-      const int n = (vb0 + j) / STEP * kTileRows + (at & 15);
-      if (n >= N) continue;
-      if constexpr (EPI == kGatedOut)
-        store_gated<BF>(P, tile, 16 * i + 4 * (at >> 4), n, acc[i][j], acc[i][j + STEP - 1]);
-      else
-        store_rows(P, tile, 16 * i + 4 * (at >> 4), n, acc[i][j]);
-    }
+    if constexpr (EPI == kGatedOut)
+      store_gated<BF>(P, tile, stage[wave], at, 16 * i, n0, {acc[TN * i], acc[TN * i + 2]},
+                      {acc[TN * i + 1], acc[TN * i + 3]});
+    else
+      store_rows<4>(P.plan, P.weights, P.part, N, tile, stage[wave], at, 16 * i, n0,
+                    {acc[TN * i], acc[TN * i + 1], acc[TN * i + 2], acc[TN * i + 3]});
   }
 }
 
@@ -494,11 +617,12 @@ struct ExpertGradArgs {
 template <int TM, int EPI, bool GATHER, bool BF>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void expert_grad_kernel(ExpertGradArgs P) {
   constexpr int TN = 4, BM = 16 * TM, TERMS = EPI == kActGradOut ? 1 : 2;
-  __shared__ __attribute__((aligned(16))) _Float16 As[2][BM * kGroup];
-  __shared__ __attribute__((aligned(16))) unsigned char Ms[2][1024];
-  int tile_i, column;
-  if (!place(P.plan, P.columns, blockIdx.x, tile_i, column)) return;
-  const ExpertTile tile = tile_at(P.plan, tile_i);
+  __shared__ __attribute__((aligned(16))) _Float16 As0[BM * kGroup], As1[BM * kGroup];
+  __shared__ __attribute__((aligned(16))) unsigned char Ms0[1024], Ms1[1024];
+  __shared__ __attribute__((aligned(16))) float Cs[TM >= 4 ? 1 : 4][TM >= 4 ? 4 : 1024];  // (else in As0)
+  ExpertTile tile;
+  int column;
+  if (!place(P.plan, P.columns, blockIdx.x, tile, column)) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform_int(tid >> 6), c = lane >> 4, r = lane & 15;
   const int R = P.R, C = P.C, KB = C / kTileRows, CG = C / kGroup, NG = R / kGroup;
 
@@ -531,13 +655,13 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     for (int u = 0; u < TM; ++u) {
       const int vo = GATHER ? aoff[GATHER ? u : 0] : aoff[0] + 32 * u * R;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rs, (__attribute__((address_space(3))) void *)(&As[buf][(u * 4 + wave) * 64 * 8]), 16, vo,
+          rs, (__attribute__((address_space(3))) void *)((buf ? As1 : As0) + (u * 4 + wave) * 64 * 8), 16, vo,
           g * kGroup * 2, 0, 0);
     }
     // scales and zero points of the block's two quantization groups (or its one, twice): 256 bytes a wave
     const int mo = ((column * 2 + 1 < CG ? wave : wave & 1) * 64 + lane) * 4;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        ms, (__attribute__((address_space(3))) void *)(&Ms[buf][wave * 256]), 4, mo,
+        ms, (__attribute__((address_space(3))) void *)((buf ? Ms1 : Ms0) + wave * 256), 4, mo,
         (g * CG + column * 2) * kMetaBytes, 0, 0);
   };
   const int kb0 = (column * 4 + wave) * TN, tile_stride = KB * kTileBytes;
@@ -562,7 +686,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     for (int j = 0; j < TN; ++j) acc[i][j] = float4v{0.f, 0.f, 0.f, 0.f};
 
   auto compute = [&](const BStage &b, int buf) {
-    const _Float16 *ms = reinterpret_cast<const _Float16 *>(&Ms[buf][ul * kMetaBytes]) + 8 * c;
+    const _Float16 *as = (buf ? As1 : As0) + r * kGroup;
+    const _Float16 *ms = reinterpret_cast<const _Float16 *>((buf ? Ms1 : Ms0) + ul * kMetaBytes) + 8 * c;
     struct Meta {
       half8 scale, bias;
     };
@@ -605,7 +730,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       const int pc = (4 * tt + c) ^ r;
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
-        const u32x4 a = *reinterpret_cast<const u32x4 *>(&As[buf][(16 * i + r) * kGroup + 8 * pc]);
+        const u32x4 a = *reinterpret_cast<const u32x4 *>(as + 16 * i * kGroup + 8 * pc);
 #pragma unroll
         for (int j = 0; j < TN; ++j) acc[i][j] = mfma<BF>(a, bop[j], acc[i][j]);
       }
@@ -622,6 +747,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     const int next = min(i + 1, stages - 1);  // (past the range: the last again, into what nobody reads)
     load_a(next, buf ^ 1);
     load_b(next, nxt);
+    __builtin_amdgcn_sched_barrier(0);  // the loads stay ahead of the MFMAs (the scheduler would sink them)
     compute(cur, buf);
   };
   load_a(0, 0);
@@ -630,51 +756,68 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     step(i, b0, b1, 0);
     if (i + 1 < stages) step(i + 1, b1, b0, 1);
   }
-  // the last step's DMA must land before the workgroup's LDS is released
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  // the last step's DMA must land, and every wave be past its reads, before the rows' LDS is
+  // used for the outputs
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 
-  const int at = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
-  const int ec = at >> 4, er = at & 15;
   if (kb0 >= KB) return;  // (C is a multiple of 128: a wave's 64 outputs are all there or none)
-  float sd[TN];
-  if constexpr (EPI == kActGradOut) {
+  const int at = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+  float *stage = TM >= 4 ? reinterpret_cast<float *>(As0) + wave * 1024 : Cs[TM >= 4 ? 0 : wave];
+  const int n0 = kb0 * kTileRows;
+  if constexpr (EPI == kGradRowsOut) {
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
-      sd[j] = P.s_down ? (float)P.s_down[(size_t)tile.expert * C + (kb0 + j) * kTileRows + er] : 1.f;
-  }
+    for (int i = 0; i < TM; ++i)
+      if (16 * i < tile.rows) store_rows<4>(P.plan, nullptr, P.part, C, tile, stage, at, 16 * i, n0, acc[i]);
+  } else {
+    // (a loop, with one copy of the activations' code: only the sums are picked by number)
+#pragma unroll 1
+    for (int i = 0; 16 * i < tile.rows; ++i) {
 #pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    if (16 * i >= tile.rows) break;
+      for (int k = 0; k < TM; ++k) {
+        if (k != i) continue;
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int row = 16 * i + 4 * ec + v;
-      const bool in = row < tile.rows;
-      const size_t sorted = (size_t)(tile.row0 + (in ? row : 0));
-      const int slot = P.plan.order[sorted];
-      const size_t from = (size_t)slot * C + kb0 * kTileRows + er;
-      if constexpr (EPI == kGradRowsOut) {
-        if (!in) continue;
+        for (int j = 0; j < TN; ++j) stage_block(stage, j, at >> 4, at & 15, acc[k][j]);
+      }
+      stage_done();
+      const int n = 8 * (at & 7);  // eight columns per lane, eight rows at a time
 #pragma unroll
-        for (int j = 0; j < TN; ++j) P.part[from + j * kTileRows] = acc[i][j][v];
-      } else {
+      for (int q = 0; q < 2; ++q) {
+        const int m = 8 * q + (at >> 3), row = 16 * i + m;
+        const bool in = row < tile.rows;
+        const size_t sorted = (size_t)(tile.row0 + (in ? row : 0));
+        const int slot = P.plan.order[sorted];
         const float w = P.weights[slot];
-        const size_t to = sorted * C + kb0 * kTileRows + er;
+        const size_t from = (size_t)slot * C + n0 + n;
+        const u32x4 g8 = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(P.G) + from);
+        const u32x4 u8 = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(P.U) + from);
+        half8 sd;
+        if (P.s_down) sd = load_half8(P.s_down + (size_t)tile.expert * C + n0 + n);
+        float4v dg[2], du[2];
         float dw = 0.f;
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
-          const float g = act_to_f32<BF>(static_cast<const uint16_t *>(P.G)[from + j * kTileRows]);
-          const float u = act_to_f32<BF>(static_cast<const uint16_t *>(P.U)[from + j * kTileRows]);
-          const float dh = acc[i][j][v] * sd[j], a = act_value(g, P.act);
-          dw = __builtin_fmaf(dh, a * u, dw);
-          if (in) {
-            static_cast<uint16_t *>(P.dG)[to + j * kTileRows] = f32_to_act<BF>(w * dh * u * act_grad(g, P.act));
-            static_cast<uint16_t *>(P.dU)[to + j * kTileRows] = f32_to_act<BF>(w * dh * a);
+        for (int h = 0; h < 2; ++h) {
+          const float4v x = *reinterpret_cast<const float4v *>(stage + staged(m, n + 4 * h));
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const int k = 4 * h + v;
+            const float g = act_to_f32<BF>((uint16_t)(g8[k / 2] >> (16 * (k & 1))));
+            const float u = act_to_f32<BF>((uint16_t)(u8[k / 2] >> (16 * (k & 1))));
+            const float dh = P.s_down ? x[v] * (float)sd[k] : x[v], a = act_value(g, P.act);
+            dw = __builtin_fmaf(dh, a * u, dw);
+            dg[h][v] = w * dh * u * act_grad(g, P.act);
+            du[h][v] = w * dh * a;
           }
         }
 #pragma unroll
-        for (int o = 1; o < 16; o *= 2) dw += __shfl_xor(dw, o);
-        if (in && er == 0) P.dw_part[(size_t)slot * (4 * P.columns) + column * 4 + wave] = dw;
+        for (int o = 1; o < 8; o *= 2) dw += __shfl_xor(dw, o);
+        if (in) {
+          const size_t to = sorted * C + n0 + n;
+          *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(P.dG) + to) = pack8<BF>(dg[0], dg[1]);
+          *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(P.dU) + to) = pack8<BF>(du[0], du[1]);
+          if ((at & 7) == 0) P.dw_part[(size_t)slot * (4 * P.columns) + column * 4 + wave] = dw;
+        }
       }
+      stage_done();
     }
   }
 }
