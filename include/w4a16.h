@@ -578,8 +578,8 @@ int w4a16_norm_block_backward(const w4a16_norm_backward_call *call, void *worksp
  *           score + bias; ties go to the lower index
  *   weight  scale * score, divided by the sum of the k chosen scores if renormalize
  * ids int32 [T][k], in the order of the choice, and weights fp32 [T][k].  Choices are made
- * as exact arithmetic would make them (to 2^-50 of a score where a bias or groups
- * are given).  An expert whose logit is -inf or NaN is never chosen, whatever its bias
+ * as exact arithmetic would make them: without a bias experts are compared by their
+ * logits, and with one, as groups always are, by scores to 2^-50.  An expert whose logit is -inf or NaN is never chosen, whatever its bias
  * (finite); where fewer than k are left to choose, the last slots have id -1 and weight 0.
  * +inf counts as the largest finite fp32 value.
  * 0 <= T <= 2^22, 1 <= E <= 1024, 1 <= k <= 64, 1 <= groups <= 64 dividing E,

@@ -99,8 +99,9 @@ def route(logits, k, score="softmax", bias=None, groups=1, topk_groups=1, renorm
     ids, weights = np.full((T, k), -1, np.int32), np.zeros((T, k))
     for t in range(T):
         may = [e for e in range(E) if l[t, e] != -np.inf]
-        # without bias or groups the logits order the scores, also where scores round together
-        value = l[t] if bias is None and groups == 1 else s[t] + (0.0 if bias is None else bias.astype(np.float64))
+        value = s[t] if bias is None else s[t] + bias.astype(np.float64)
+        # without a bias the logits order the scores, also where scores round together
+        order = l[t] if bias is None else value
         if topk_groups < groups:
             size = E // groups
             best = []
@@ -110,7 +111,7 @@ def route(logits, k, score="softmax", bias=None, groups=1, topk_groups=1, renorm
                     best.append((-sum(inside), g))
             kept = {g for _, g in sorted(best)[:topk_groups]}
             may = [e for e in may if e // size in kept]
-        chosen = sorted(may, key=lambda e: (-value[e], e))[:k]
+        chosen = sorted(may, key=lambda e: (-order[e], e))[:k]
         if not chosen:
             continue
         w = s[t, chosen]

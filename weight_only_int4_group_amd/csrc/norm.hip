@@ -29,9 +29,19 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kNormNone = 0, kNormLayer = 2;
 
+// v of the lane that the DPP control names, 0 where there is none
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xf, false));
+}
+// The wave's sum, in lane 63: prefix sums within rows of 16 lanes, then across the rows.
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  v += dpp<0x111, 0xf>(v);
+  v += dpp<0x112, 0xf>(v);
+  v += dpp<0x114, 0xf>(v);
+  v += dpp<0x118, 0xf>(v);
+  v += dpp<0x142, 0xa>(v);
+  v += dpp<0x143, 0xc>(v);
   return v;
 }
 
@@ -44,7 +54,7 @@ __device__ __forceinline__ void row_sum(float &a, float &b, float2 *red) {
   if constexpr (TPR > 64) {
     constexpr int kWaves = TPR / 64;
     const int wave = (threadIdx.x % TPR) >> 6;
-    if ((threadIdx.x & 63) == 0) red[wave] = make_float2(a, b);
+    if ((threadIdx.x & 63) == 63) red[wave] = make_float2(a, b);
     __syncthreads();
     a = b = 0.f;
 #pragma unroll
@@ -52,6 +62,9 @@ __device__ __forceinline__ void row_sum(float &a, float &b, float2 *red) {
       a += red[w].x;
       b += red[w].y;
     }
+  } else {
+    a = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, a), 63));
+    b = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, b), 63));
   }
 }
 
@@ -109,15 +122,16 @@ struct Row {
   }
 };
 
-template <int TPR, int CPT, bool VEC>
+// Which of them there are; FULL: all (D = TPR * CPT), known when compiling.
+template <int TPR, int CPT, bool VEC, bool FULL = false>
 struct Columns {
   bool in[VEC ? CPT / 8 : CPT];
   __device__ __forceinline__ Columns(int t, int D) {
 #pragma unroll
     for (int i = 0; i < (VEC ? CPT / 8 : CPT); ++i)
-      in[i] = Row<TPR, CPT, VEC>::column(t, VEC ? 8 * i : i) < D;
+      in[i] = FULL || Row<TPR, CPT, VEC>::column(t, VEC ? 8 * i : i) < D;
   }
-  __device__ __forceinline__ bool operator[](int i) const { return in[VEC ? i / 8 : i]; }
+  __device__ __forceinline__ bool operator[](int i) const { return FULL || in[VEC ? i / 8 : i]; }
 };
 
 // v becomes its normalised row
@@ -250,14 +264,14 @@ __device__ __forceinline__ const NormGradArgs &args_again() {
 // flight.  A thread keeps its columns' sums over the strip, so the sums cost one
 // fp32 row per strip; norm_sum_kernel adds the strips in order.
 // Without: one row per workgroup (strips of one row), which leaves its statistics.
-template <int TPR, int CPT, bool BF, bool VEC, bool SUMS>
+template <int TPR, int CPT, bool BF, bool VEC, bool SUMS, bool FULL = false>
 __global__ __launch_bounds__(TPR) void norm_grad_kernel(NormGradArgs A0) {
   typedef Row<TPR, CPT, VEC> R16;
   constexpr int kW = TPR / 64;
   __shared__ float2 red[4 * kW];
-  const int t = threadIdx.x, D = A0.d.D;
+  const int t = threadIdx.x, D = FULL ? TPR * CPT : A0.d.D;
   const float rD = 1.0f / D;
-  const Columns<TPR, CPT, VEC> in(t, D);
+  const Columns<TPR, CPT, VEC, FULL> in(t, D);
   const bool pre = A0.d.pre.kind != kNormNone, post = A0.d.post.kind != kNormNone;
   const bool pre_layer = A0.d.pre.kind == kNormLayer, post_layer = A0.d.post.kind == kNormLayer;
   int m0 = blockIdx.x, m1 = blockIdx.x + 1;
@@ -520,8 +534,10 @@ __global__ __launch_bounds__(256) void norm_sum_kernel(NormSumArgs A) {
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Strips of a backward call: about 2^17 threads of them (two waves per SIMD), of at
-// least 8 rows; within one gate vector's rows each, or of whole ones.
+// Strips of a backward call: about 2^18 threads of them (four waves per SIMD), of at
+// least 8 rows; within one gate vector's rows each, or of whole ones.  The backward of
+// 4092 x 4096 (layer norms and four gates, bf16) takes 57 + 8 us so, and with half as
+// many strips 75 + 5.
 struct NormPlan {
   bool fused;  // the sums are taken where the rows are
   int tpr, cpt;
@@ -534,7 +550,7 @@ NormPlan plan_norm_grad(const NormGradDesc &d) {
   while (p.tpr * 8 < d.D && p.tpr < 512) p.tpr *= 2;
   p.cpt = d.D <= 4096 ? 8 : 16;
   const long long T = d.T, gr = d.gate ? d.gate_rows : T;
-  const long long want = std::max(1, (1 << 17) / p.tpr);
+  const long long want = std::max(1, (1 << 18) / p.tpr);
   const long long rows = std::max<long long>(8, (T + want - 1) / want);
   p.segments = (int)((T + gr - 1) / gr);
   if (gr > rows) {
@@ -575,14 +591,19 @@ void launch_norm_typed(const NormDesc &d, hipStream_t stream) {
 template <bool BF>
 void launch_norm_grad_fused(const NormPlan &p, const NormGradArgs &a, hipStream_t stream) {
 #define W4_NORM(TPR, CPT)                                                                        \
-  if (p.tpr == TPR && p.cpt == CPT)                                                              \
-  hipLaunchKernelGGL((norm_grad_kernel<TPR, CPT, BF, true, true>), dim3((unsigned)p.strips),     \
-                     dim3(TPR), 0, stream, a)
-  W4_NORM(64, 8);
-  W4_NORM(128, 8);
-  W4_NORM(256, 8);
-  W4_NORM(512, 8);
-  W4_NORM(512, 16);
+  if (p.tpr == TPR && p.cpt == CPT) {                                                            \
+    if (a.d.D == TPR * CPT)                                                                      \
+      hipLaunchKernelGGL((norm_grad_kernel<TPR, CPT, BF, true, true, true>),                     \
+                         dim3((unsigned)p.strips), dim3(TPR), 0, stream, a);                     \
+    else                                                                                         \
+      hipLaunchKernelGGL((norm_grad_kernel<TPR, CPT, BF, true, true>), dim3((unsigned)p.strips), \
+                         dim3(TPR), 0, stream, a);                                               \
+  }
+  W4_NORM(64, 8)
+  W4_NORM(128, 8)
+  W4_NORM(256, 8)
+  W4_NORM(512, 8)
+  W4_NORM(512, 16)
 #undef W4_NORM
 }
 

@@ -119,6 +119,40 @@ __device__ __forceinline__ double share(const RouteDesc &P, float l, float m) {
   return P.sigmoid ? sigmoid_from(l, m) : exp_from(l, m);
 }
 
+// The k largest keys in order, slot n's expert in lane n (-1: none); ties to the lowest
+// expert.
+template <int VPL, typename Key>
+__device__ __forceinline__ int choose(Key (&key)[VPL], int k, int lane) {
+  int id = -1;
+  for (int n = 0; n < k; ++n) {
+    Key mine = key[0];
+    int at = 0;
+#pragma unroll
+    for (int i = 1; i < VPL; ++i)
+      if (key[i] > mine) {
+        mine = key[i];
+        at = i;
+      }
+    const Key best = wave_max_key(mine);
+    if (best == 0) break;
+    // ties: the lowest expert, that is the lowest i, then the lowest lane
+    uint64_t hit = __ballot(mine == best);
+    if (VPL > 1 && (hit & (hit - 1))) {
+      const uint32_t low = ~wave_max(mine == best ? ~(uint32_t)at : 0u);
+      hit = __ballot(mine == best && at == (int)low);
+    }
+    const int owner = __builtin_ctzll(hit);
+    const int e = __builtin_amdgcn_readlane(lane + 64 * at, owner);
+    if (lane == n) id = e;
+    if (lane == owner) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (at == i) key[i] = 0;
+    }
+  }
+  return id;
+}
+
 // WIDE: choice by 64-bit values (bias or groups), else by the logits.
 template <int TYPE, int VPL, bool WIDE>
 __global__ __launch_bounds__(64 * kTokens) void route_kernel(RouteDesc P) {
@@ -199,43 +233,17 @@ __global__ __launch_bounds__(64 * kTokens) void route_kernel(RouteDesc P) {
     }
   }
 
-  // slot n's expert and logit, in lane n
-  int id = -1;
-  float lid = -INFINITY;
-  for (int n = 0; n < P.k; ++n) {
-    Key mine = key[0];
-    int at = 0;
+  // slot n's expert, in lane n: without a bias by the logits, which order the scores
+  int id;
+  if (WIDE && P.bias) {
+    id = choose(key, P.k, lane);
+  } else {
+    uint32_t by_logit[VPL];
 #pragma unroll
-    for (int i = 1; i < VPL; ++i)
-      if (key[i] > mine) {
-        mine = key[i];
-        at = i;
-      }
-    const Key best = wave_max_key(mine);
-    if (best == 0) break;
-    // ties: the lowest expert, that is the lowest i, then the lowest lane
-    uint64_t hit = __ballot(mine == best);
-    if (VPL > 1 && (hit & (hit - 1))) {
-      const uint32_t low = ~wave_max(mine == best ? ~(uint32_t)at : 0u);
-      hit = __ballot(mine == best && at == (int)low);
-    }
-    const int owner = __builtin_ctzll(hit);
-    float lv = l[0];
-#pragma unroll
-    for (int i = 1; i < VPL; ++i)
-      if (at == i) lv = l[i];
-    const int e = __builtin_amdgcn_readlane(lane + 64 * at, owner);
-    const float le = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, lv), owner));
-    if (lane == n) {
-      id = e;
-      lid = le;
-    }
-    if (lane == owner) {
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (at == i) key[i] = 0;
-    }
+    for (int i = 0; i < VPL; ++i) by_logit[i] = key[i] ? key_of(l[i]) : 0u;
+    id = choose(by_logit, P.k, lane);
   }
+  const float lid = id < 0 ? -INFINITY : fminf(load_logit<TYPE>(P.logits, (size_t)token * P.E + id), 3.402823466e38f);
 
   double w;
   if (P.renormalize) {
