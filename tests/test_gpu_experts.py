@@ -235,7 +235,8 @@ def test_more_slots_than_a_round_holds():
 
 
 def test_weights_past_32_bit_offsets():
-    """The last of 80 experts, 4.7 GB into each weight, gives the bits of the same expert alone."""
+    """The last of 80 experts, 4.7 GB into each weight, gives the bits of the same expert as the last of two
+    (two tiles at most in both calls, so the contraction is split alike)."""
     torch = torch_cuda()
     E, D, N = 80, 4096, 28672
     g = torch.Generator("cuda").manual_seed(4)
@@ -247,15 +248,15 @@ def test_weights_past_32_bit_offsets():
         return w4.PackedExperts(codes, sc, torch.full((E * meta,), 8.0, dtype=torch.float16, device="cuda"), E, n, c)
 
     def last(w):
-        part = [v.view(E, -1)[E - 1].clone() for v in (w.wq, w.scales, w.zeros)]
-        return w4.PackedExperts(*part, 1, w.N, w.K)
+        part = [v.view(E, -1)[E - 2:].reshape(-1).clone() for v in (w.wq, w.scales, w.zeros)]
+        return w4.PackedExperts(*part, 2, w.N, w.K)
     three = [packed(N, D), packed(N, D), packed(D, N)]
     X, _ = tensor("fp16", 7, 2, D)
     w = torch.ones(2, 1, device="cuda")
     note("experts past 32 bits")
     Y = w4.w4a16_experts(X, torch.full((2, 1), E - 1, dtype=torch.int32, device="cuda"), w, *three)
-    one = w4.w4a16_experts(X, torch.zeros(2, 1, dtype=torch.int32, device="cuda"), w, *(last(x) for x in three))
-    assert torch.equal(Y, one) and bool(torch.isfinite(Y).all()) and bool((Y != 0).any())
+    two = w4.w4a16_experts(X, torch.ones(2, 1, dtype=torch.int32, device="cuda"), w, *(last(x) for x in three))
+    assert torch.equal(Y, two) and bool(torch.isfinite(Y).all()) and bool((Y != 0).any())
 
 
 # ---- backward --------------------------------------------------------------------------------

@@ -87,6 +87,9 @@ struct Plan {
   const int32_t *order;      // [S] slots, sorted by expert (those that name one)
   const ExpertTile *tiles;
   const int32_t *count;      // tiles there are
+  // without a plan (order null): the call's ids, at most 64 of them (small_tile)
+  const int32_t *ids;
+  int S, E;
 };
 
 constexpr int kPlanThreads = 1024;  // and the most experts
@@ -174,6 +177,31 @@ __device__ __forceinline__ bool place(const Plan &plan, int columns, int block, 
   return true;
 }
 
+// The same without a plan, for at most 64 slots, whose ids are the lanes of a wave: a slot's
+// rank is how many before it name its expert, and a tile is an expert's slots of 16
+// consecutive ranks, numbered by the first of them.  `slots` gets the slot of each row.  (A
+// launch less: decode of one token over 2 of 8 experts, 56 and 51 us.)
+__device__ __forceinline__ bool small_tile(const Plan &plan, int columns, int block, ExpertTile &tile, int &column, int *slots) {
+  const int lane = threadIdx.x & 63;
+  const int e = lane < plan.S ? plan.ids[lane] : -1;
+  const bool named = e >= 0 && e < plan.E;
+  int rank = 0;
+  for (int i = 0; i < plan.S; ++i) rank += __builtin_amdgcn_readlane(e, i) == e && i < lane ? 1 : 0;
+  uint64_t first = __ballot(named && rank % 16 == 0);
+  const int total = (int)__builtin_popcountll(first) * columns, run = (total + 7) >> 3;
+  const int local = (block & 7) * run + (block >> 3);
+  if ((block >> 3) >= run || local >= total) return false;
+  const int t = local / columns;
+  column = local - t * columns;
+  for (int i = 0; i < t; ++i) first &= first - 1;
+  const int lead = __builtin_ctzll(first);
+  const int te = __builtin_amdgcn_readlane(e, lead), at = __builtin_amdgcn_readlane(rank, lead) / 16;
+  const bool in = named && e == te && rank / 16 == at;
+  tile = {te, 0, (int)__builtin_popcountll(__ballot(in)), 0, 1, {}};
+  if (in && threadIdx.x < 64) slots[rank % 16] = lane;
+  return true;
+}
+
 // A wave's 16 x 64 fp32 sums go through 4 KB of its own LDS on their way out, so that a
 // lane has neighbouring columns of one row and stores 16 bytes of them: straight from
 // the MFMA's layout, 16 columns of 4 bytes at a time, the down product of 32768 slots of
@@ -214,10 +242,11 @@ __device__ __forceinline__ void store_16x32(float *stage, int lane, int row0, in
 }
 
 // 16 rows of G and U (and H from them), 32 columns from n0: g and u hold two 16-column
-// blocks each.
-template <bool BF>
+// blocks each.  SLOT(row) is a tile's row's slot, HROW(row) its row of H.
+template <bool BF, typename SLOT, typename HROW>
 __device__ __forceinline__ void store_gated(const ExpertArgs &P, const ExpertTile &tile, float *stage, int lane, int row0,
-                                            int n0, const float4v (&g)[2], const float4v (&u)[2]) {
+                                            int n0, const float4v (&g)[2], const float4v (&u)[2], SLOT &&slot_of,
+                                            HROW &&h_row) {
   const int r = lane & 15;
   float4v h[2];
 #pragma unroll
@@ -227,20 +256,21 @@ __device__ __forceinline__ void store_gated(const ExpertArgs &P, const ExpertTil
     for (int v = 0; v < 4; ++v) h[j][v] = act_value(g[j][v], P.act) * u[j][v] * sd;
   }
   store_16x32<BF>(stage, lane, row0, tile.rows, h, [&](int m) {
-    return static_cast<uint16_t *>(P.H) + (size_t)(tile.row0 + m) * P.N + n0;
+    return static_cast<uint16_t *>(P.H) + (size_t)h_row(m) * P.N + n0;
   });
   if (!P.G) return;
-  auto slot = [&](void *p) {
-    return [=, &P](int m) { return static_cast<uint16_t *>(p) + (size_t)P.plan.order[tile.row0 + m] * P.N + n0; };
-  };
-  store_16x32<BF>(stage, lane, row0, tile.rows, g, slot(P.G));
-  store_16x32<BF>(stage, lane, row0, tile.rows, u, slot(P.U));
+  store_16x32<BF>(stage, lane, row0, tile.rows, g, [&](int m) {
+    return static_cast<uint16_t *>(P.G) + (size_t)slot_of(m) * P.N + n0;
+  });
+  store_16x32<BF>(stage, lane, row0, tile.rows, u, [&](int m) {
+    return static_cast<uint16_t *>(P.U) + (size_t)slot_of(m) * P.N + n0;
+  });
 }
 
 // 16 rows of a slot's contribution, 16 BLOCKS columns from n0, times the slot's weight (or as
 // they are: weights null), in fp32.
-template <int BLOCKS>
-__device__ __forceinline__ void store_rows(const Plan &plan, const float *weights, float *part, int N, const ExpertTile &tile,
+template <int BLOCKS, typename SLOT>
+__device__ __forceinline__ void store_rows(SLOT &&slot_of, const float *weights, float *part, int N, const ExpertTile &tile,
                                            float *stage, int lane, int row0, int n0, const float4v (&y)[BLOCKS]) {
   constexpr int kLanes = 4 * BLOCKS, kRows = 64 / kLanes;  // lanes along a row, rows at a time
 #pragma unroll
@@ -251,7 +281,7 @@ __device__ __forceinline__ void store_rows(const Plan &plan, const float *weight
   for (int q = 0; q < 16 / kRows; ++q) {
     const int m = kRows * q + lane / kLanes;
     if (row0 + m >= tile.rows) continue;
-    const int slot = plan.order[tile.row0 + row0 + m];
+    const int slot = slot_of(row0 + m);
     float4v x = *reinterpret_cast<const float4v *>(stage + staged(m, n));
     if (weights) x *= weights[slot];
     *reinterpret_cast<float4v *>(part + (size_t)slot * N + n0 + n) = x;
@@ -267,23 +297,34 @@ __device__ __forceinline__ void store_rows(const Plan &plan, const float *weight
 // come straight into registers, DEPTH groups of 128 ahead, with no barrier until the end;
 // rows past the tile's are not loaded (their offset lies past the resource).
 template <int TN, int KS, int EPI, bool GATHER, bool BF>
-__global__ __launch_bounds__(64 * KS) void expert_stream_kernel(ExpertArgs P) {
-  constexpr int DEPTH = TN == 2 ? 4 : 2;
+__global__ __launch_bounds__(64 * KS) __attribute__((amdgpu_waves_per_eu(TN == 2 ? 4 : 3))) void expert_stream_kernel(ExpertArgs P) {
+  constexpr int DEPTH = 2;
   constexpr int STEP = EPI == kGatedOut ? 2 : 1;
   __shared__ float4v red[KS][TN][64];
   __shared__ __attribute__((aligned(16))) float stage[TN / (2 * STEP)][1024];
+  __shared__ int slots[16];
+  const bool small = P.plan.order == nullptr;
   ExpertTile tile;
   int column;
-  if (!place(P.plan, P.columns, blockIdx.x, tile, column)) return;
+  if (small) {
+    if (!small_tile(P.plan, P.columns, blockIdx.x, tile, column, slots)) return;
+  } else {
+    if (!place(P.plan, P.columns, blockIdx.x, tile, column)) return;
+    if ((int)threadIdx.x < tile.rows) slots[threadIdx.x] = P.plan.order[tile.row0 + threadIdx.x];
+  }
+  __syncthreads();
   const int lane = threadIdx.x & 63, wave = uniform_int(threadIdx.x >> 6), c = lane >> 4, r = lane & 15;
   const int K = P.K, N = P.N, G = K / kGroup, NB = N / kTileRows;
   const int vb0 = column * TN;  // first row block (gated: of the alternating ones)
 
+  // rows of A: gathered, of the tokens; else of H, which has the tile's rows in a run, or (without
+  // a plan) every slot's row
   const __amdgpu_buffer_rsrc_t ars =
       GATHER ? resource(P.A, (size_t)P.tokens * K * 2)
-             : resource(static_cast<const uint16_t *>(P.A) + (size_t)tile.row0 * K, (size_t)tile.rows * K * 2);
+             : small ? resource(P.A, (size_t)P.plan.S * K * 2)
+                     : resource(static_cast<const uint16_t *>(P.A) + (size_t)tile.row0 * K, (size_t)tile.rows * K * 2);
   int aoff = kOutOfRange;
-  if (r < tile.rows) aoff = ((GATHER ? P.plan.order[tile.row0 + r] / P.k : r) * K + 8 * c) * 2;
+  if (r < tile.rows) aoff = ((GATHER ? slots[r] / P.k : small ? slots[r] : r) * K + 8 * c) * 2;
   __amdgpu_buffer_rsrc_t wrs[STEP], srs[STEP], zrs[STEP];
   const size_t code0 = tile.expert * P.code_bytes, meta0 = tile.expert * P.meta_count;
 #pragma unroll
@@ -358,10 +399,12 @@ __global__ __launch_bounds__(64 * KS) void expert_stream_kernel(ExpertArgs P) {
   }
   const int n0 = (vb0 + OUT * wave) / STEP * kTileRows;
   if (n0 >= N) return;  // (N is a multiple of 128: all 32 columns are there)
+  auto slot_of = [&](int m) { return slots[m]; };
   if constexpr (EPI == kGatedOut)
-    store_gated<BF>(P, tile, stage[wave], lane, 0, n0, {y[0], y[2]}, {y[1], y[3]});
+    store_gated<BF>(P, tile, stage[wave], lane, 0, n0, {y[0], y[2]}, {y[1], y[3]}, slot_of,
+                    [&](int m) { return small ? slots[m] : tile.row0 + m; });
   else
-    store_rows<2>(P.plan, P.weights, P.part, N, tile, stage[wave], lane, 0, n0, {y[0], y[1]});
+    store_rows<2>(slot_of, P.weights, P.part, N, tile, stage[wave], lane, 0, n0, {y[0], y[1]});
 }
 
 // ---- many rows per expert: LDS tiles -----------------------------------------------------------
@@ -575,14 +618,15 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   const int at = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
   const int n0 = vb0 / STEP * kTileRows;
   if (n0 >= N) return;  // (N is a multiple of 128: a wave's columns are all there or none)
+  auto slot_of = [&](int m) { return P.plan.order[tile.row0 + m]; };
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
     if (16 * i >= tile.rows) break;
     if constexpr (EPI == kGatedOut)
       store_gated<BF>(P, tile, stage[wave], at, 16 * i, n0, {acc[TN * i], acc[TN * i + 2]},
-                      {acc[TN * i + 1], acc[TN * i + 3]});
+                      {acc[TN * i + 1], acc[TN * i + 3]}, slot_of, [&](int m) { return tile.row0 + m; });
     else
-      store_rows<4>(P.plan, P.weights, P.part, N, tile, stage[wave], at, 16 * i, n0,
+      store_rows<4>(slot_of, P.weights, P.part, N, tile, stage[wave], at, 16 * i, n0,
                     {acc[TN * i], acc[TN * i + 1], acc[TN * i + 2], acc[TN * i + 3]});
   }
 }
@@ -767,7 +811,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   if constexpr (EPI == kGradRowsOut) {
 #pragma unroll
     for (int i = 0; i < TM; ++i)
-      if (16 * i < tile.rows) store_rows<4>(P.plan, nullptr, P.part, C, tile, stage, at, 16 * i, n0, acc[i]);
+      if (16 * i < tile.rows) store_rows<4>([&](int m) { return P.plan.order[tile.row0 + m]; }, nullptr, P.part, C, tile, stage, at, 16 * i, n0, acc[i]);
   } else {
     // (a loop, with one copy of the activations' code: only the sums are picked by number)
 #pragma unroll 1
@@ -955,14 +999,35 @@ Layout layout(const ExpertsDesc &d) {
   return l;
 }
 
+// Streaming: row blocks per workgroup and waves that share a contraction, the most waves with
+// at least four groups each while they are under 16 a CU, as few as two where there are
+// enough without.
+struct StreamShape {
+  int tn, ks;
+};
+StreamShape stream_shape(bool gated, int blocks, int groups, int tiles) {
+  const long long wave_tiles = (long long)tiles * blocks;
+  if (gated) return {4, 4};
+  if (wave_tiles / 4 * 2 >= 4096 && groups < 32) return {4, 2};
+  return wave_tiles / 4 * 4 >= 4096 ? StreamShape{4, 4} : StreamShape{2, 8};
+}
+
 template <int EPI, bool GATHER, bool BF>
 hipError_t launch_product(ExpertArgs a, int rows, int tiles, hipStream_t stream) {
   const int blocks = (EPI == kGatedOut ? 2 : 1) * (a.N / kTileRows);
   if (rows == 16) {
-    constexpr int TN = EPI == kGatedOut ? 4 : 2, KS = EPI == kGatedOut ? 4 : 8;
-    a.columns = (blocks + TN - 1) / TN;
-    hipLaunchKernelGGL((expert_stream_kernel<TN, KS, EPI, GATHER, BF>), dim3((unsigned)((tiles * a.columns + 7) / 8 * 8)),
-                       dim3(64 * KS), 0, stream, a);
+    const StreamShape s = stream_shape(EPI == kGatedOut, blocks, a.K / kGroup, tiles);
+    a.columns = (blocks + s.tn - 1) / s.tn;
+    const dim3 grid((unsigned)((tiles * a.columns + 7) / 8 * 8)), threads(64 * s.ks);
+#define W4_STREAM(TN, KS)                                                                        \
+  if (s.tn == TN && s.ks == KS)                                                                  \
+  hipLaunchKernelGGL((expert_stream_kernel<TN, KS, EPI, GATHER, BF>), grid, threads, 0, stream, a)
+    W4_STREAM(4, 4);
+    if constexpr (EPI == kRowsOut) {
+      W4_STREAM(4, 2);
+      W4_STREAM(2, 8);
+    }
+#undef W4_STREAM
   } else {
     a.columns = (blocks + 15) / 16;
     const dim3 grid((unsigned)((tiles * a.columns + 7) / 8 * 8));
@@ -983,7 +1048,9 @@ hipError_t launch_experts_typed(const ExpertsDesc &d, char *ws, hipStream_t stre
     const int32_t *ids = d.ids + (size_t)t0 * d.k;
     int32_t *order = reinterpret_cast<int32_t *>(ws + l.order), *count = reinterpret_cast<int32_t *>(ws + l.count);
     ExpertTile *list = reinterpret_cast<ExpertTile *>(ws + l.list);
-    hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, ids, S, d.E, l.rows, order, list, count);
+    const bool small = S <= 64 && l.rows == 16;
+    if (!small)
+      hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, ids, S, d.E, l.rows, order, list, count);
     const char *X = static_cast<const char *>(d.X) + (size_t)t0 * d.D * 2;
     if (d.s) {
       const long long octets = (long long)T * d.D / 8;
@@ -996,7 +1063,7 @@ hipError_t launch_experts_typed(const ExpertsDesc &d, char *ws, hipStream_t stre
     if (e != hipSuccess) return e;
     const int tiles = max_tiles(S, d.E, l.rows);
     ExpertArgs a = {};
-    a.plan = {order, list, count};
+    a.plan = {small ? nullptr : order, list, count, ids, S, d.E};
     a.k = d.k;
     a.tokens = T;
     a.weights = d.weights + (size_t)t0 * d.k;
@@ -1100,7 +1167,7 @@ hipError_t launch_experts_grad_typed(const ExpertsGradDesc &d, char *ws, hipStre
     const int tiles = max_tiles(S, d.E, l.rows);
     const size_t row = (size_t)t0 * d.D * 2, slot_n = (size_t)t0 * d.k * d.N * 2;
     ExpertGradArgs a = {};
-    a.plan = {order, list, count};
+    a.plan = {order, list, count, ids, S, d.E};
     a.k = d.k;
     a.tokens = T;
     a.weights = d.weights + (size_t)t0 * d.k;
