@@ -172,7 +172,9 @@ def run_forward(T, E, k, D, N, dtype="bf16", act="silu", kind="even", s=False, r
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("T,E,k,D,N", [(1, 1, 1, 128, 128), (1, 4, 2, 256, 384), (3, 8, 3, 640, 128), (16, 4, 2, 384, 640),
                                        (33, 2, 1, 256, 256), (40, 3, 2, 128, 384), (70, 2, 2, 512, 128),
-                                       (200, 3, 2, 384, 256), (130, 1, 1, 256, 640), (64, 16, 8, 256, 128)])
+                                       (200, 3, 2, 384, 256), (130, 1, 1, 256, 640), (64, 16, 8, 256, 128),
+                                       # many experts: tiles of 16, 32 and 64 rows begin at other means
+                                       (56, 512, 8, 128, 128), (448, 512, 8, 128, 128), (1472, 512, 8, 128, 128)])
 def test_shapes(T, E, k, D, N, dtype):
     run_forward(T, E, k, D, N, dtype)
 
@@ -319,7 +321,11 @@ def run_backward(T, E, k, D, N, dtype="bf16", act="silu", kind="even", s=False, 
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("T,E,k,D,N", [(1, 1, 1, 128, 128), (1, 4, 2, 256, 384), (16, 4, 2, 384, 640), (40, 3, 2, 128, 384),
                                        (70, 2, 2, 512, 128), (90, 3, 2, 384, 256), (300, 2, 1, 256, 640),
-                                       (64, 16, 8, 256, 128)])
+                                       (64, 16, 8, 256, 128), (32, 2, 2, 128, 256), (330, 2, 1, 256, 128),
+                                       (200, 1, 1, 128, 384),
+                                       # many experts: tiles of 16 to 128 rows begin at other means
+                                       (448, 512, 8, 128, 128), (960, 512, 8, 128, 128), (400, 512, 32, 128, 128),
+                                       (928, 512, 32, 128, 128)])
 def test_backward_shapes(T, E, k, D, N, dtype):
     run_backward(T, E, k, D, N, dtype)
 

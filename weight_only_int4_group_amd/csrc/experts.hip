@@ -87,7 +87,7 @@ struct Plan {
   const int32_t *order;      // [S] slots, sorted by expert (those that name one)
   const ExpertTile *tiles;
   const int32_t *count;      // tiles there are
-  // without a plan (order null): the call's ids, at most 64 of them (small_tile)
+  // without a plan (order null): the call's ids, at most kSmallSlots of them (small_tile)
   const int32_t *ids;
   int S, E;
 };
@@ -104,9 +104,16 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int32_t *ids, 
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   count[t] = 0;
   __syncthreads();
-  for (int i = t; i < S; i += kPlanThreads) {
-    const int e = ids[i];
-    if (e >= 0 && e < E) atomicAdd(&count[e], 1);
+  // (eight ids per thread and turn, loaded together: one at a time, 32768 slots over 64 experts
+  // took 30 us)
+  constexpr int kAhead = 8;
+  for (int i0 = t; i0 < S; i0 += kAhead * kPlanThreads) {
+    int e[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) e[u] = i0 + u * kPlanThreads < S ? ids[i0 + u * kPlanThreads] : -1;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (e[u] >= 0 && e[u] < E) atomicAdd(&count[e[u]], 1);
   }
   __syncthreads();
   const int rows = count[t], mine = (rows + tile_rows - 1) / tile_rows;
@@ -131,9 +138,16 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int32_t *ids, 
     tiles[b - mine + i] = {t, first + i * tile_rows, min(tile_rows, rows - i * tile_rows), b - mine, mine, {}};
   if (t == kPlanThreads - 1) *tile_count = b;
   __syncthreads();
-  for (int i = t; i < S; i += kPlanThreads) {
-    const int e = ids[i];
-    if (e >= 0 && e < E) order[atomicAdd(&at[e], 1)] = i;
+  for (int i0 = t; i0 < S; i0 += kAhead * kPlanThreads) {
+    int e[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) e[u] = i0 + u * kPlanThreads < S ? ids[i0 + u * kPlanThreads] : -1;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (e[u] >= 0 && e[u] < E) e[u] = atomicAdd(&at[e[u]], 1); else e[u] = -1;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (e[u] >= 0) order[e[u]] = i0 + u * kPlanThreads;
   }
 }
 
@@ -177,35 +191,38 @@ __device__ __forceinline__ bool place(const Plan &plan, int columns, int block, 
   return true;
 }
 
-// The same without a plan, for at most 64 slots, whose ids are the lanes of a wave: a slot's
-// rank is how many before it name its expert, and a tile is an expert's slots of 16
-// consecutive ranks, numbered by the first of them.  `slots` gets the slot of each row.  (A
-// launch less: decode of one token over 2 of 8 experts, 56 and 51 us.)
+// The same without a plan, for at most 16 slots, whose ids are the first lanes of a wave: a
+// tile is all of an expert's slots, numbered by the first of them.  `slots` gets the slot of
+// each row.  A launch less, for a search in every workgroup: 25.8 us for the call rather than
+// 29.2 with a plan at 8 slots (64 experts of 1024 x 4096), 160 and 162 at 16 (8 experts of
+// 14336 x 4096), but with the search over 64 slots 89 and 82.
+constexpr int kSmallSlots = 16;
+
 __device__ __forceinline__ bool small_tile(const Plan &plan, int columns, int block, ExpertTile &tile, int &column, int *slots) {
   const int lane = threadIdx.x & 63;
   const int e = lane < plan.S ? plan.ids[lane] : -1;
   const bool named = e >= 0 && e < plan.E;
-  int rank = 0;
-  for (int i = 0; i < plan.S; ++i) rank += __builtin_amdgcn_readlane(e, i) == e && i < lane ? 1 : 0;
-  uint64_t first = __ballot(named && rank % 16 == 0);
+  int rank = 0;  // how many slots before the lane's name its expert
+#pragma unroll
+  for (int i = 0; i < kSmallSlots - 1; ++i) rank += __builtin_amdgcn_readlane(e, i) == e && i < lane ? 1 : 0;
+  uint64_t first = __ballot(named && rank == 0);
   const int total = (int)__builtin_popcountll(first) * columns, run = (total + 7) >> 3;
   const int local = (block & 7) * run + (block >> 3);
   if ((block >> 3) >= run || local >= total) return false;
   const int t = local / columns;
   column = local - t * columns;
   for (int i = 0; i < t; ++i) first &= first - 1;
-  const int lead = __builtin_ctzll(first);
-  const int te = __builtin_amdgcn_readlane(e, lead), at = __builtin_amdgcn_readlane(rank, lead) / 16;
-  const bool in = named && e == te && rank / 16 == at;
+  const int te = __builtin_amdgcn_readlane(e, __builtin_ctzll(first));
+  const bool in = named && e == te;
   tile = {te, 0, (int)__builtin_popcountll(__ballot(in)), 0, 1, {}};
-  if (in && threadIdx.x < 64) slots[rank % 16] = lane;
+  if (in && threadIdx.x < 64) slots[rank] = lane;
   return true;
 }
 
 // A wave's 16 x 64 fp32 sums go through 4 KB of its own LDS on their way out, so that a
 // lane has neighbouring columns of one row and stores 16 bytes of them: straight from
 // the MFMA's layout, 16 columns of 4 bytes at a time, the down product of 32768 slots of
-// 4096 (1024 deep) took 700 us, and 390 us this way.  Column blocks of 16 are swapped by row
+// 4096 (1024 deep) took 700 us, and 455 us this way.  Column blocks of 16 are swapped by row
 // (XOR with row / 4 % 4), so that the four rows that a write touches lie in different banks.
 __device__ __forceinline__ int staged(int row, int col) { return row * 64 + (col ^ ((row >> 2 & 3) * 16)); }
 __device__ __forceinline__ void stage_block(float *stage, int j, int c, int r, float4v x) {
@@ -791,7 +808,6 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     const int next = min(i + 1, stages - 1);  // (past the range: the last again, into what nobody reads)
     load_a(next, buf ^ 1);
     load_b(next, nxt);
-    __builtin_amdgcn_sched_barrier(0);  // the loads stay ahead of the MFMAs (the scheduler would sink them)
     compute(cur, buf);
   };
   load_a(0, 0);
@@ -965,12 +981,36 @@ int round_tokens(int T, int k, int D) {
 
 int max_tiles(int S, int E, int rows) { return std::min(S, S / rows + std::min(E, S)); }
 
-// Rows per tile: 16 where an expert that is chosen at all gets that many or fewer on
-// average (streaming), else 32 or 64.
-int tile_rows(const ExpertsDesc &d, int S) {
-  const double mean = (double)S / std::min(d.E, S);
-  return mean <= 16 ? 16 : mean <= 32 ? 32 : 64;
+// Rows per tile, from the rows that an expert that is chosen at all gets on average, and from
+// whether one tile of each alone gives every CU a workgroup (tiles are 256 outputs wide).
+// Fewer rows than a tile has are loads and MFMAs of nothing; more are another reading of
+// the weights, from the L2.  Times in us:
+//   forward, 64 experts of 1024 x 4096 (256 workgroups or more)
+//     rows  2: 108 by 16 (streaming), 111 by 32         rows  8: 116, 108
+//     rows 20: 120 by 32, 135 by 64                     rows 24: 151, 136
+//   forward, 8 of 14336 x 4096 (128)
+//     rows 12: 220 by 16, 239 by 32                     rows 20: 310, 242
+//     rows 32: 273 by 32, 295 by 64                     rows 40: 310, 299
+//   backward, 64 of 1024 x 4096
+//     rows  8: 130 by 16, 149 by 32                     rows 12: 159, 153
+//     rows 20: 158 by 32, 172 by 64                     rows 24: 188, 176
+//     rows 40: 188 by 64, 223 by 128                    rows 64: 251, 242
+//   backward, 8 of 14336 x 4096
+//     rows 24: 432 by 16, 464 by 32                     rows 32: 558, 514
+//     rows 32: 514 by 32, 521 by 64                     rows 40: 531, 522
+//     rows 128: 778 by 64, 809 by 128                   rows 256: 1242, 1068
+struct RowsRule {
+  int most[3];  // the largest mean for 16, 32 and 64 rows
+};
+int tile_rows(int S, int E, int D, int N, const RowsRule &filled, const RowsRule &few, int largest) {
+  const int chosen = std::min(E, S);
+  const RowsRule &rule = (long long)chosen * (std::min(D, N) / 128) >= 512 ? filled : few;
+  int rows = 16;
+  for (int i = 0; i < 3 && rows < largest && (long long)rule.most[i] * chosen < S; ++i) rows *= 2;
+  return rows;
 }
+int forward_rows(int S, int E, int D, int N) { return tile_rows(S, E, D, N, {{6, 22}}, {{16, 36}}, 64); }
+int backward_rows(int S, int E, int D, int N) { return tile_rows(S, E, D, N, {{10, 22, 56}}, {{28, 36, 160}}, 128); }
 
 // The workspace of one round.
 struct Layout {
@@ -981,7 +1021,7 @@ Layout layout(const ExpertsDesc &d) {
   Layout l = {};
   l.tokens = round_tokens(d.T, d.k, d.D);
   l.slots = l.tokens * d.k;
-  l.rows = tile_rows(d, l.slots);
+  l.rows = forward_rows(l.slots, d.E, d.D, d.N);
   l.tiles = max_tiles(l.slots, d.E, l.rows);
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -999,17 +1039,24 @@ Layout layout(const ExpertsDesc &d) {
   return l;
 }
 
-// Streaming: row blocks per workgroup and waves that share a contraction, the most waves with
-// at least four groups each while they are under 16 a CU, as few as two where there are
-// enough without.
+// Streaming: 16-row blocks of the weights per workgroup, and waves that share a contraction.
+// The more of both, the fewer times the activations are read and the fewer loads a
+// wave waits for, but the fewer workgroups there are and the more the waves have to join.
+// Times in us:
+//   gate and up of 8 experts, 14336 x 4096, 2 slots: 46.7 by (4, 4), 52.0 by (4, 8), 44.8 by (4, 2);
+//   of 64, 1024 x 4096, 8 slots 25.8, 25.3, 32.7; 128 slots 96, 110, 101
+//   down of 8 experts, 4096 x 14336 (112 groups): 512 blocks over all tiles 46.5 by (2, 8), 63 by
+//   (4, 4); 2048: 133 and 138; 2560: 181 and 172
+//   down of 64, 4096 x 1024 (8 groups): 2048 blocks 24.6 by (4, 4), 25.7 by (4, 2), 25.8 by
+//   (2, 8); 8192: 46, 44 and 64
 struct StreamShape {
   int tn, ks;
 };
 StreamShape stream_shape(bool gated, int blocks, int groups, int tiles) {
-  const long long wave_tiles = (long long)tiles * blocks;
   if (gated) return {4, 4};
-  if (wave_tiles / 4 * 2 >= 4096 && groups < 32) return {4, 2};
-  return wave_tiles / 4 * 4 >= 4096 ? StreamShape{4, 4} : StreamShape{2, 8};
+  const bool many = (long long)tiles * blocks > 2048, deep = groups >= 32;
+  if (many) return deep ? StreamShape{4, 4} : StreamShape{4, 2};
+  return deep ? StreamShape{2, 8} : StreamShape{4, 4};
 }
 
 template <int EPI, bool GATHER, bool BF>
@@ -1048,7 +1095,7 @@ hipError_t launch_experts_typed(const ExpertsDesc &d, char *ws, hipStream_t stre
     const int32_t *ids = d.ids + (size_t)t0 * d.k;
     int32_t *order = reinterpret_cast<int32_t *>(ws + l.order), *count = reinterpret_cast<int32_t *>(ws + l.count);
     ExpertTile *list = reinterpret_cast<ExpertTile *>(ws + l.list);
-    const bool small = S <= 64 && l.rows == 16;
+    const bool small = S <= kSmallSlots && l.rows == 16;
     if (!small)
       hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, ids, S, d.E, l.rows, order, list, count);
     const char *X = static_cast<const char *>(d.X) + (size_t)t0 * d.D * 2;
@@ -1119,8 +1166,7 @@ GradLayout grad_layout(const ExpertsGradDesc &d) {
   GradLayout l = {};
   l.tokens = round_tokens(d.T, d.k, d.D);
   l.slots = l.tokens * d.k;
-  const double mean = (double)l.slots / std::min(d.E, l.slots);
-  l.rows = mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : 128;
+  l.rows = backward_rows(l.slots, d.E, d.D, d.N);
   l.tiles = max_tiles(l.slots, d.E, l.rows);
   l.columns = (d.N + 255) / 256;
   size_t at = 0;
