@@ -5,6 +5,8 @@ the smallest fp16.  Errors are carried to first order, with a factor 1.05 for th
   * A forward product multiplies exact codes: per group of 128 the MFMA's fp32 sum of x (c + q), c = 64 (fp16) or
     128 (bf16), and that of x, at most 40 additions deep each, then two FMAs per group.  Its error is
     (40 + groups + 4) e times B = sum |x| scale 2 (c + 16); X * s adds u times sum |x s| |w|.
+  * With more than 176 slots per expert a product may round each weight (u, or TINY where it is below fp16's
+    normal numbers) and sum in fp32 instead, K additions deep: (u + (K + 8) e) sum |x| |w| + TINY sum |x|.
   * act: slopes within 1.2, fp32 evaluation within 2^-19 (1 + |z|); H = act(G) U s_down, rounded (u).
   * The token's sum: (k + 2) e of the magnitudes; Y is rounded (u).
   * A backward product rounds each weight (u) and sums in fp32: (u + (R + 8) e) times sum |x| |w|.
@@ -82,12 +84,16 @@ def routing(T, E, k, kind="even", seed=0):
     return ids.astype(np.int32), w
 
 
-def product(x, W, scale, e_x, dtype):
-    """(x . W^T, its fp32 error with e_x on x)."""
+def product(x, W, scale, e_x, dtype, rounded=False):
+    """(x . W^T, its fp32 error with e_x on x; rounded: or that of rounded weights)."""
     c = 64 if dtype == "fp16" else 128
     K = x.shape[1]
     B = np.abs(x) @ (scale * 2 * (c + 16)).T
-    return x @ W.T, (44 + K // 128) * E32 * B + e_x @ np.abs(W).T
+    own = (44 + K // 128) * E32 * B
+    if rounded:
+        own = np.maximum(own, (unit(dtype) + (K + 8) * E32) * (np.abs(x) @ np.abs(W).T) +
+                         TINY * np.abs(x).sum(1, keepdims=True))
+    return x @ W.T, own + e_x @ np.abs(W).T
 
 
 def forward_bounds(Xv, ids, w, st, dtype, act, s, s_down, residual):
@@ -97,20 +103,21 @@ def forward_bounds(Xv, ids, w, st, dtype, act, s, s_down, residual):
     Y, G, U = block.experts(Xv, ids, w.astype(np.float64), gate.W, up.W, down.W, act, s, s_down, residual)
     bY, bG, bU = np.zeros_like(Y), np.zeros_like(G), np.zeros_like(U)
     mag = np.zeros_like(Y) if residual is None else np.abs(residual)
+    rounded = ids.size > 176 * min(gate.W.shape[0], ids.size)
     xs = Xv if s is None else Xv * s
     e_x = np.zeros_like(xs) if s is None else u * np.abs(xs) + TINY
     for e in range(gate.W.shape[0]):
         t, j = np.nonzero(ids == e)
         if not len(t):
             continue
-        g, eg = product(xs[t], gate.W[e], gate.scale[e], e_x[t], dtype)
-        uu, eu = product(xs[t], up.W[e], up.scale[e], e_x[t], dtype)
+        g, eg = product(xs[t], gate.W[e], gate.scale[e], e_x[t], dtype, rounded)
+        uu, eu = product(xs[t], up.W[e], up.scale[e], e_x[t], dtype, rounded)
         sd = 1.0 if s_down is None else s_down[e]
         a = of.act(g, act)
         ea = 1.2 * eg + 2.0 ** -19 * (1 + np.abs(g))
         h = a * uu * sd
         eh = sd * (ea * (np.abs(uu) + eu) + np.abs(a) * eu) + (u + 4 * E32) * np.abs(h) + TINY
-        p, ep = product(h, down.W[e], down.scale[e], eh, dtype)
+        p, ep = product(h, down.W[e], down.scale[e], eh, dtype, rounded)
         bG[t, j], bU[t, j] = 1.05 * eg + u * np.abs(g) + TINY, 1.05 * eu + u * np.abs(uu) + TINY
         wt = w[t, j][:, None].astype(np.float64)
         np.add.at(bY, t, wt * ep)
@@ -174,7 +181,9 @@ def run_forward(T, E, k, D, N, dtype="bf16", act="silu", kind="even", s=False, r
                                        (33, 2, 1, 256, 256), (40, 3, 2, 128, 384), (70, 2, 2, 512, 128),
                                        (200, 3, 2, 384, 256), (130, 1, 1, 256, 640), (64, 16, 8, 256, 128),
                                        # many experts: tiles of 16, 32 and 64 rows begin at other means
-                                       (56, 512, 8, 128, 128), (448, 512, 8, 128, 128), (1472, 512, 8, 128, 128)])
+                                       (56, 512, 8, 128, 128), (448, 512, 8, 128, 128), (1472, 512, 8, 128, 128),
+                                       # 128 rows a tile
+                                       (230, 1, 1, 256, 384), (700, 3, 2, 640, 256), (2900, 512, 32, 128, 128)])
 def test_shapes(T, E, k, D, N, dtype):
     run_forward(T, E, k, D, N, dtype)
 
@@ -189,6 +198,12 @@ def test_activations(T, act):
 @pytest.mark.parametrize("T", [1, 7, 60, 300])
 def test_routings(T, kind):
     run_forward(T, 5, 2, 256, 128, "fp16", kind=kind, residual=T > 7, train=True)
+
+
+def test_rounded_weights_with_scales_and_kept_products():
+    for dtype in ("fp16", "bf16"):
+        run_forward(611, 2, 1, 256, 384, dtype, "gelu", s=True, residual=True, train=True)
+        run_forward(901, 3, 2, 384, 128, dtype, kind="skip", residual=True, train=True)
 
 
 def test_residual_in_place():

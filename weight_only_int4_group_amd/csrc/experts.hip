@@ -76,6 +76,25 @@ __device__ __forceinline__ u32x4 ones_operand() {
   return (u32x4){one, one, one, one};
 }
 
+// Eight codes of one word as fp16, exact: columns 2p and 2p + 1 in e[p], plus 1024 (p even) or
+// 64 (p odd).
+__device__ __forceinline__ void code_halves(uint32_t w, half2v (&e)[4]) {
+  const uint32_t w8 = w >> 8;
+  const half2v sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
+  e[0] = as_half2(and_or(w, 0x000F000Fu, kMagic2));
+  e[1] = as_half2(and_or(w, 0x00F000F0u, kMagic2)) * sixteenth;
+  e[2] = as_half2(and_or(w8, 0x000F000Fu, kMagic2));
+  e[3] = as_half2(and_or(w8, 0x00F000F0u, kMagic2)) * sixteenth;
+}
+// q * scale (q - z exact in fp16) in the activations' type, rounded once
+template <bool BF>
+__device__ __forceinline__ uint32_t scaled_codes(half2v q, half2v scale) {
+  if constexpr (BF)
+    return pack_bf16x2(__builtin_fmaf((float)q[0], (float)scale[0], 0.f), __builtin_fmaf((float)q[1], (float)scale[1], 0.f));
+  else
+    return __builtin_bit_cast(uint32_t, q * scale);
+}
+
 // ---- the plan -------------------------------------------------------------------------
 
 struct ExpertTile {
@@ -648,6 +667,154 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   }
 }
 
+// ---- many more rows: weights rounded once -------------------------------------------------------
+
+// A tile of 128 rows and 256 outputs, laid out as above with twice the rows.  Their sums
+// alone take half the registers, which leaves no room for a group's product beside
+// them: each weight is rounded to the activations' type, as in the dense layers, and the
+// MFMAs add to the sums at once.  Decoding a weight costs three times as much that way,
+// shared by twice the rows, and no FMAs follow the MFMAs.
+template <int EPI, bool GATHER, bool BF>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void expert_wide_kernel(ExpertArgs P) {
+  constexpr int TM = 8, TN = 4, BM = 16 * TM, STEP = EPI == kGatedOut ? 2 : 1;
+  __shared__ __attribute__((aligned(16))) _Float16 As0[BM * kGroup], As1[BM * kGroup];
+  ExpertTile tile;
+  int column;
+  if (!place(P.plan, P.columns, blockIdx.x, tile, column)) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform_int(tid >> 6), c = lane >> 4, r = lane & 15;
+  const int K = P.K, N = P.N, G = K / kGroup, NB = N / kTileRows;
+
+  // rows of A: as in expert_tile_kernel
+  const __amdgpu_buffer_rsrc_t ars =
+      GATHER ? resource(P.A, (size_t)P.tokens * K * 2)
+             : resource(static_cast<const uint16_t *>(P.A) + (size_t)tile.row0 * K, (size_t)tile.rows * K * 2);
+  const int arow = 4 * wave + c, lc = r ^ arow;
+  int aoff[GATHER ? TM : 1];
+  aoff[0] = (arow * K + 8 * lc) * 2;
+  if constexpr (GATHER) {
+#pragma unroll
+    for (int u = 0; u < TM; ++u) {
+      aoff[u] = kOutOfRange;
+      if (16 * u + arow < tile.rows)
+        aoff[u] = (P.plan.order[tile.row0 + 16 * u + arow] / P.k * K + 8 * lc) * 2;
+    }
+  }
+  auto load_a = [&](int g, int buf) {
+#pragma unroll
+    for (int u = 0; u < TM; ++u) {
+      const int vo = GATHER ? aoff[GATHER ? u : 0] : aoff[0] + 32 * u * K;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          ars, (__attribute__((address_space(3))) void *)((buf ? As1 : As0) + (u * 4 + wave) * 64 * 8), 16, vo,
+          g * kGroup * 2, 0, 0);
+    }
+  };
+  __amdgpu_buffer_rsrc_t wrs[STEP], srs[STEP], zrs[STEP];
+  const size_t code0 = tile.expert * P.code_bytes, meta0 = tile.expert * P.meta_count;
+#pragma unroll
+  for (int i = 0; i < STEP; ++i) {
+    wrs[i] = resource(P.Wq[i] + code0, P.code_bytes);
+    srs[i] = resource(P.scales[i] + meta0, P.meta_count * 2);
+    zrs[i] = resource(P.zeros[i] + meta0, P.meta_count * 2);
+  }
+  const int vb0 = (column * 4 + wave) * TN;
+  const int tile_stride = NB * kTileBytes, meta_stride = NB * kTileRows * kMetaQuad * 2;
+  struct BStage {
+    u32x4 code[TN];
+    uint32_t sc[TN], zp[TN];  // raw fp16 scale and zero point
+  };
+  auto load_b = [&](int g, BStage &b) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {  // (blocks past N: the last again, not stored)
+      const int rb = min(vb0 + j, STEP * NB - 1) / STEP;
+      const int qo = (g / kMetaQuad) * meta_stride + (rb * kTileRows * kMetaQuad + g % kMetaQuad) * 2;
+      b.code[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                wrs[j % STEP], lane * 16, g * tile_stride + rb * kTileBytes, 0));
+      b.sc[j] = __builtin_amdgcn_raw_buffer_load_b16(srs[j % STEP], r * kMetaQuad * 2, qo, 0);
+      b.zp[j] = __builtin_amdgcn_raw_buffer_load_b16(zrs[j % STEP], r * kMetaQuad * 2, qo, 0);
+    }
+  };
+
+  float4v acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = float4v{0.f, 0.f, 0.f, 0.f};
+
+  auto compute = [&](const BStage &b, int buf) {
+    const _Float16 *as = (buf ? As1 : As0) + r * kGroup;
+    half2v lo[TN], hi[TN], scale[TN];  // 1024 + z and 64 + z, twice each
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      const _Float16 z = __builtin_bit_cast(_Float16, (uint16_t)b.zp[j]), s = __builtin_bit_cast(_Float16, (uint16_t)b.sc[j]);
+      const _Float16 zl = (_Float16)1024.f + z, zh = (_Float16)64.f + z;
+      lo[j] = half2v{zl, zl};
+      hi[j] = half2v{zh, zh};
+      scale[j] = half2v{s, s};
+    }
+    auto dequant = [&](int j, int tt) -> u32x4 {
+      half2v e[4];
+      code_halves(b.code[j][tt], e);
+      return (u32x4){scaled_codes<BF>(e[0] - lo[j], scale[j]), scaled_codes<BF>(e[1] - hi[j], scale[j]),
+                     scaled_codes<BF>(e[2] - lo[j], scale[j]), scaled_codes<BF>(e[3] - hi[j], scale[j])};
+    };
+    // k step tt + 1's weights are dequantized while k step tt's MFMAs run
+    u32x4 bop[TN];
+#pragma unroll
+    for (int j = 0; j < TN; ++j) bop[j] = dequant(j, 0);
+#pragma unroll
+    for (int tt = 0; tt < 4; ++tt) {
+      u32x4 bnx[TN];
+      if (tt < 3) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) bnx[j] = dequant(j, tt + 1);
+      }
+      const int pc = (4 * tt + c) ^ r;
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        const u32x4 a = *reinterpret_cast<const u32x4 *>(as + 16 * i * kGroup + 8 * pc);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = mfma<BF>(a, bop[j], acc[i][j]);
+      }
+      if (tt < 3) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) bop[j] = bnx[j];
+      }
+    }
+  };
+  BStage b0, b1;
+  auto step = [&](int g, BStage &cur, BStage &nxt, int buf) {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    const int gn = min(g + 1, G - 1);  // (past the range: the last again, into what nobody reads)
+    load_a(gn, buf ^ 1);
+    load_b(gn, nxt);
+    compute(cur, buf);
+  };
+  load_a(0, 0);
+  load_b(0, b0);
+  for (int g = 0; g < G; g += 2) {
+    step(g, b0, b1, 0);
+    if (g + 1 < G) step(g + 1, b1, b0, 1);
+  }
+  // the last step's DMA must land, and every wave be past its reads, before the rows' LDS is
+  // used for the outputs
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+
+  const int n0 = vb0 / STEP * kTileRows;
+  if (n0 >= N) return;  // (N is a multiple of 128: a wave's columns are all there or none)
+  const int at = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+  float *stage = reinterpret_cast<float *>(As0) + wave * 1024;
+  auto slot_of = [&](int m) { return P.plan.order[tile.row0 + m]; };
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    if (16 * i >= tile.rows) break;
+    if constexpr (EPI == kGatedOut)
+      store_gated<BF>(P, tile, stage, at, 16 * i, n0, {acc[i][0], acc[i][2]}, {acc[i][1], acc[i][3]}, slot_of,
+                      [&](int m) { return tile.row0 + m; });
+    else
+      store_rows<4>(slot_of, P.weights, P.part, N, tile, stage, at, 16 * i, n0, acc[i]);
+  }
+}
+
 // ---- backward products -------------------------------------------------------------------------
 
 enum { kActGradOut = 0, kGradRowsOut = 1 };
@@ -756,22 +923,13 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       return {*reinterpret_cast<const half8 *>(ms + 32 * tt), *reinterpret_cast<const half8 *>(ms + kGroup + 32 * tt)};
     };
     auto dequant = [&](int j, int tt, const Meta &m) -> u32x4 {
-      const uint32_t w = b.code[j][tt], w8 = w >> 8;
-      const half2v sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
-      const half2v e[4] = {as_half2(and_or(w, 0x000F000Fu, kMagic2)),
-                           as_half2(and_or(w, 0x00F000F0u, kMagic2)) * sixteenth,
-                           as_half2(and_or(w8, 0x000F000Fu, kMagic2)),
-                           as_half2(and_or(w8, 0x00F000F0u, kMagic2)) * sixteenth};
+      half2v e[4];
+      code_halves(b.code[j][tt], e);
       u32x4 out;
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
         const half2v bias = {m.bias[2 * p], m.bias[2 * p + 1]}, scale = {m.scale[2 * p], m.scale[2 * p + 1]};
-        const half2v v = e[p] - bias;  // q - z, exact
-        if constexpr (BF)
-          out[p] = pack_bf16x2(__builtin_fmaf((float)v[0], (float)scale[0], 0.f),
-                               __builtin_fmaf((float)v[1], (float)scale[1], 0.f));
-        else
-          out[p] = __builtin_bit_cast(uint32_t, v * scale);
+        out[p] = scaled_codes<BF>(e[p] - bias, scale);
       }
       return out;
     };
@@ -988,9 +1146,11 @@ int max_tiles(int S, int E, int rows) { return std::min(S, S / rows + std::min(E
 //   forward, 64 experts of 1024 x 4096 (256 workgroups or more)
 //     rows  2: 108 by 16 (streaming), 111 by 32         rows  8: 116, 108
 //     rows 20: 120 by 32, 135 by 64                     rows 24: 151, 136
+//     rows 160: 410 by 64, 438 by 128                   rows 192: 481, 462; 512: 1165, 1060
 //   forward, 8 of 14336 x 4096 (128)
 //     rows 12: 220 by 16, 239 by 32                     rows 20: 310, 242
 //     rows 32: 273 by 32, 295 by 64                     rows 40: 310, 299
+//     rows 192: 711 by 64, 725 by 128                   rows 256: 946, 879; 512: 1680, 1607
 //   backward, 64 of 1024 x 4096
 //     rows  8: 130 by 16, 149 by 32                     rows 12: 159, 153
 //     rows 20: 158 by 32, 172 by 64                     rows 24: 188, 176
@@ -1002,15 +1162,15 @@ int max_tiles(int S, int E, int rows) { return std::min(S, S / rows + std::min(E
 struct RowsRule {
   int most[3];  // the largest mean for 16, 32 and 64 rows
 };
-int tile_rows(int S, int E, int D, int N, const RowsRule &filled, const RowsRule &few, int largest) {
+int tile_rows(int S, int E, int D, int N, const RowsRule &filled, const RowsRule &few) {
   const int chosen = std::min(E, S);
   const RowsRule &rule = (long long)chosen * (std::min(D, N) / 128) >= 512 ? filled : few;
   int rows = 16;
-  for (int i = 0; i < 3 && rows < largest && (long long)rule.most[i] * chosen < S; ++i) rows *= 2;
+  for (int i = 0; i < 3 && (long long)rule.most[i] * chosen < S; ++i) rows *= 2;
   return rows;
 }
-int forward_rows(int S, int E, int D, int N) { return tile_rows(S, E, D, N, {{6, 22}}, {{16, 36}}, 64); }
-int backward_rows(int S, int E, int D, int N) { return tile_rows(S, E, D, N, {{10, 22, 56}}, {{28, 36, 160}}, 128); }
+int forward_rows(int S, int E, int D, int N) { return tile_rows(S, E, D, N, {{6, 22, 176}}, {{16, 36, 224}}); }
+int backward_rows(int S, int E, int D, int N) { return tile_rows(S, E, D, N, {{10, 22, 56}}, {{28, 36, 160}}); }
 
 // The workspace of one round.
 struct Layout {
@@ -1080,8 +1240,10 @@ hipError_t launch_product(ExpertArgs a, int rows, int tiles, hipStream_t stream)
     const dim3 grid((unsigned)((tiles * a.columns + 7) / 8 * 8));
     if (rows == 32)
       hipLaunchKernelGGL((expert_tile_kernel<2, EPI, GATHER, BF>), grid, dim3(256), 0, stream, a);
-    else
+    else if (rows == 64)
       hipLaunchKernelGGL((expert_tile_kernel<4, EPI, GATHER, BF>), grid, dim3(256), 0, stream, a);
+    else
+      hipLaunchKernelGGL((expert_wide_kernel<EPI, GATHER, BF>), grid, dim3(256), 0, stream, a);
   }
   return hipGetLastError();
 }
