@@ -5,7 +5,7 @@ the smallest fp16.  Errors are carried to first order, with a factor 1.05 for th
   * A forward product multiplies exact codes: per group of 128 the MFMA's fp32 sum of x (c + q), c = 64 (fp16) or
     128 (bf16), and that of x, at most 40 additions deep each, then two FMAs per group.  Its error is
     (40 + groups + 4) e times B = sum |x| scale 2 (c + 16); X * s adds u times sum |x s| |w|.
-  * With more than 176 slots per expert a product may round each weight (u, or TINY where it is below fp16's
+  * With more than 56 slots per expert a product may round each weight (u, or TINY where it is below fp16's
     normal numbers) and sum in fp32 instead, K additions deep: (u + (K + 8) e) sum |x| |w| + TINY sum |x|.
   * act: slopes within 1.2, fp32 evaluation within 2^-19 (1 + |z|); H = act(G) U s_down, rounded (u).
   * The token's sum: (k + 2) e of the magnitudes; Y is rounded (u).
@@ -96,14 +96,15 @@ def product(x, W, scale, e_x, dtype, rounded=False):
     return x @ W.T, own + e_x @ np.abs(W).T
 
 
-def forward_bounds(Xv, ids, w, st, dtype, act, s, s_down, residual):
+def forward_bounds(Xv, ids, w, st, dtype, act, s, s_down, residual, rounded=None):
     """The oracle's (Y, G, U) and bounds of each."""
     gate, up, down = st
     u = unit(dtype)
     Y, G, U = block.experts(Xv, ids, w.astype(np.float64), gate.W, up.W, down.W, act, s, s_down, residual)
     bY, bG, bU = np.zeros_like(Y), np.zeros_like(G), np.zeros_like(U)
     mag = np.zeros_like(Y) if residual is None else np.abs(residual)
-    rounded = ids.size > 176 * min(gate.W.shape[0], ids.size)
+    if rounded is None:
+        rounded = ids.size > 56 * min(gate.W.shape[0], ids.size)
     xs = Xv if s is None else Xv * s
     e_x = np.zeros_like(xs) if s is None else u * np.abs(xs) + TINY
     for e in range(gate.W.shape[0]):
@@ -180,10 +181,11 @@ def run_forward(T, E, k, D, N, dtype="bf16", act="silu", kind="even", s=False, r
 @pytest.mark.parametrize("T,E,k,D,N", [(1, 1, 1, 128, 128), (1, 4, 2, 256, 384), (3, 8, 3, 640, 128), (16, 4, 2, 384, 640),
                                        (33, 2, 1, 256, 256), (40, 3, 2, 128, 384), (70, 2, 2, 512, 128),
                                        (200, 3, 2, 384, 256), (130, 1, 1, 256, 640), (64, 16, 8, 256, 128),
-                                       # many experts: tiles of 16, 32 and 64 rows begin at other means
-                                       (56, 512, 8, 128, 128), (448, 512, 8, 128, 128), (1472, 512, 8, 128, 128),
-                                       # 128 rows a tile
-                                       (230, 1, 1, 256, 384), (700, 3, 2, 640, 256), (2900, 512, 32, 128, 128)])
+                                       # tiles of 16, 32, 64 and 128 rows
+                                       (56, 512, 8, 128, 128), (448, 512, 8, 128, 128), (2000, 512, 8, 128, 128),
+                                       (2900, 512, 32, 128, 128), (200, 40, 8, 256, 1024), (5500, 4, 4, 640, 384),
+                                       # and the contraction in two parts and in four
+                                       (1900, 2, 2, 128, 2176), (60, 2, 1, 128, 8192)])
 def test_shapes(T, E, k, D, N, dtype):
     run_forward(T, E, k, D, N, dtype)
 
@@ -202,8 +204,8 @@ def test_routings(T, kind):
 
 def test_rounded_weights_with_scales_and_kept_products():
     for dtype in ("fp16", "bf16"):
-        run_forward(611, 2, 1, 256, 384, dtype, "gelu", s=True, residual=True, train=True)
-        run_forward(901, 3, 2, 384, 128, dtype, kind="skip", residual=True, train=True)
+        run_forward(1800, 2, 2, 256, 2176, dtype, "gelu", s=True, residual=True, train=True)
+        run_forward(2600, 3, 2, 128, 2048, dtype, kind="skip", residual=True, train=True)
 
 
 def test_residual_in_place():
@@ -230,24 +232,28 @@ def test_no_tokens():
 
 
 def test_more_slots_than_a_round_holds():
-    """2 x 70000 slots run in two rounds; every row is the one that a small call gives."""
+    """2 x 70000 slots run in two rounds, of 65536 and 4464 tokens."""
     torch = torch_cuda()
     st = stack(1, 4, 128, 128), stack(2, 4, 128, 128), stack(3, 4, 128, 128)
-    dev = [x.dev for x in st]
-    X, _ = tensor("bf16", 5, 70000, 128)
-    ids, w = (to_dev(x) for x in routing(70000, 4, 2, "skip"))
+    X, Xv = tensor("bf16", 5, 70000, 128)
+    ids, w = routing(70000, 4, 2, "skip")
+    on = (ids >= 0) & (ids < 4)
+    idd, wd = to_dev(ids), to_dev(w)
     pre = tuple(torch.zeros(70000, 2, 128, dtype=X.dtype, device="cuda") for _ in range(2))
     note("experts in rounds")
-    Y = w4.w4a16_experts(X, ids, w, *dev, residual=X, preact=pre)
+    Y = w4.w4a16_experts(X, idd, wd, *(x.dev for x in st), residual=X, preact=pre)
     dY, _ = tensor("bf16", 6, 70000, 128)
     back = [x.transposed() for x in st]
-    dX, dw = w4.w4a16_experts_backward(dY, ids, w, *pre, *back, add=dY)
+    dX, dw = w4.w4a16_experts_backward(dY, idd, wd, *pre, *back, add=dY)
     for a in (0, 65000, 69000):
         r = slice(a, a + 1000)
-        sub = tuple(torch.zeros(1000, 2, 128, dtype=X.dtype, device="cuda") for _ in range(2))
-        y = w4.w4a16_experts(X[r], ids[r], w[r], *dev, residual=X[r], preact=sub)
-        assert torch.equal(Y[r], y) and torch.equal(pre[0][r], sub[0]) and torch.equal(pre[1][r], sub[1])
-        dx, d = w4.w4a16_experts_backward(dY[r], ids[r], w[r], *sub, *back, add=dY[r])
+        refs, bounds = forward_bounds(Xv[r], ids[r], w[r], st, "bf16", "silu", None, None, Xv[r], rounded=True)
+        check(Y[r], refs[0], bounds[0], "Y")
+        for p, ref, b, tag in zip(pre, refs[1:], bounds[1:], "GU"):
+            assert bool((p[r][to_dev(~on[r])] == 0).all()), f"{tag}: a skipped slot was written"
+            check(p[r][to_dev(on[r])], ref[on[r]], b[on[r]], tag)
+        # (two stages of contraction: never split, and of one order in every tile)
+        dx, d = w4.w4a16_experts_backward(dY[r], idd[r], wd[r], *(p[r] for p in pre), *back, add=dY[r])
         assert torch.equal(dX[r], dx) and torch.equal(dw[r], d)
 
 
@@ -338,9 +344,11 @@ def run_backward(T, E, k, D, N, dtype="bf16", act="silu", kind="even", s=False, 
                                        (70, 2, 2, 512, 128), (90, 3, 2, 384, 256), (300, 2, 1, 256, 640),
                                        (64, 16, 8, 256, 128), (32, 2, 2, 128, 256), (330, 2, 1, 256, 128),
                                        (200, 1, 1, 128, 384),
-                                       # many experts: tiles of 16 to 128 rows begin at other means
-                                       (448, 512, 8, 128, 128), (960, 512, 8, 128, 128), (400, 512, 32, 128, 128),
-                                       (928, 512, 32, 128, 128)])
+                                       # tiles of 16, 32, 64 and 128 rows
+                                       (448, 512, 8, 128, 128), (960, 512, 8, 128, 128), (448, 512, 32, 128, 128),
+                                       (928, 512, 32, 128, 128),
+                                       # and the contraction in two parts and in four
+                                       (90, 3, 2, 384, 768), (8, 3, 2, 128, 4096), (1900, 2, 2, 256, 4352)])
 def test_backward_shapes(T, E, k, D, N, dtype):
     run_backward(T, E, k, D, N, dtype)
 

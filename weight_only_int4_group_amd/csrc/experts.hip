@@ -186,8 +186,9 @@ struct ExpertArgs {
   const _Float16 *s_down; // [E][N] or null (gated)
   void *G, *U;            // [slots][N] or null (gated)
   void *H;                // gated: [sorted rows][N]
-  float *part;            // rows: [slots][N], weighted
+  float *part;            // rows: [slabs][slots][N], weighted
   int act, columns;       // columns: workgroups along the outputs
+  int slabs;              // parts of the contraction (tiles of 32 rows and more)
 };
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void *p, size_t bytes) {
@@ -208,6 +209,17 @@ __device__ __forceinline__ bool place(const Plan &plan, int columns, int block, 
   const ExpertTile &t = plan.tiles[first + at - column * count];
   tile = {uniform_int(t.expert), uniform_int(t.row0), uniform_int(t.rows), first, count, {}};
   return true;
+}
+
+// One part of the contraction where it is split: stages begin .. end - 1 of `stages`, and
+// `column` without the part.
+struct Part {
+  int slab, begin, end;
+};
+__device__ __forceinline__ Part part_of(int &column, int columns, int slabs, int stages) {
+  const int slab = column / columns;
+  column -= slab * columns;
+  return {slab, (int)((long long)stages * slab / slabs), (int)((long long)stages * (slab + 1) / slabs)};
 }
 
 // The same without a plan, for at most 16 slots, whose ids are the first lanes of a wave: a
@@ -467,9 +479,11 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   __shared__ __attribute__((aligned(16))) float stage[4][1024];
   ExpertTile tile;
   int column;
-  if (!place(P.plan, P.columns, blockIdx.x, tile, column)) return;
+  if (!place(P.plan, P.columns * P.slabs, blockIdx.x, tile, column)) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform_int(tid >> 6), c = lane >> 4, r = lane & 15;
-  const int K = P.K, N = P.N, G = K / kGroup, NB = N / kTileRows;
+  const int K = P.K, N = P.N, NB = N / kTileRows;
+  const Part part = part_of(column, P.columns, P.slabs, K / kGroup);
+  const int G0 = part.begin, G = part.end - G0;  // the part's first group, and how many
 
   // wave load u fills LDS chunks p = (u * 4 + wave) * 64 + lane: row p / 16 = 16 u + 4 wave +
   // lane / 16, physical chunk p % 16, holding logical chunk lc = (p % 16) ^ (row % 16), the same
@@ -494,7 +508,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       const int vo = GATHER ? aoff[GATHER ? u : 0] : aoff[0] + 32 * u * K;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           ars, (__attribute__((address_space(3))) void *)((buf ? As1 : As0) + (u * 4 + wave) * 64 * 8), 16, vo,
-          g * kGroup * 2, 0, 0);
+          (G0 + g) * kGroup * 2, 0, 0);
     }
   };
   __amdgpu_buffer_rsrc_t wrs[STEP], srs[STEP], zrs[STEP];
@@ -516,10 +530,11 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     for (int j = 0; j < TN; ++j) {
       const int rb = min(vb0 + j, STEP * NB - 1) / STEP;
       b.w[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                             wrs[j % STEP], lane * 16, g * tile_stride + rb * kTileBytes, 0));
+                                             wrs[j % STEP], lane * 16, (G0 + g) * tile_stride + rb * kTileBytes, 0));
     }
   };
-  auto load_meta = [&](int g) {
+  auto load_meta = [&](int step) {
+    const int g = G0 + step;
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
       const int rb = min(vb0 + j, STEP * NB - 1) / STEP;
@@ -662,7 +677,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       store_gated<BF>(P, tile, stage[wave], at, 16 * i, n0, {acc[TN * i], acc[TN * i + 2]},
                       {acc[TN * i + 1], acc[TN * i + 3]}, slot_of, [&](int m) { return tile.row0 + m; });
     else
-      store_rows<4>(slot_of, P.weights, P.part, N, tile, stage[wave], at, 16 * i, n0,
+      store_rows<4>(slot_of, P.weights, P.part + (size_t)part.slab * P.plan.S * N, N, tile, stage[wave], at, 16 * i, n0,
                     {acc[TN * i], acc[TN * i + 1], acc[TN * i + 2], acc[TN * i + 3]});
   }
 }
@@ -680,9 +695,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   __shared__ __attribute__((aligned(16))) _Float16 As0[BM * kGroup], As1[BM * kGroup];
   ExpertTile tile;
   int column;
-  if (!place(P.plan, P.columns, blockIdx.x, tile, column)) return;
+  if (!place(P.plan, P.columns * P.slabs, blockIdx.x, tile, column)) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform_int(tid >> 6), c = lane >> 4, r = lane & 15;
-  const int K = P.K, N = P.N, G = K / kGroup, NB = N / kTileRows;
+  const int K = P.K, N = P.N, NB = N / kTileRows;
+  const Part part = part_of(column, P.columns, P.slabs, K / kGroup);
 
   // rows of A: as in expert_tile_kernel
   const __amdgpu_buffer_rsrc_t ars =
@@ -784,16 +800,16 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   BStage b0, b1;
   auto step = [&](int g, BStage &cur, BStage &nxt, int buf) {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    const int gn = min(g + 1, G - 1);  // (past the range: the last again, into what nobody reads)
+    const int gn = min(g + 1, part.end - 1);  // (past the range: the last again, into what nobody reads)
     load_a(gn, buf ^ 1);
     load_b(gn, nxt);
     compute(cur, buf);
   };
-  load_a(0, 0);
-  load_b(0, b0);
-  for (int g = 0; g < G; g += 2) {
+  load_a(part.begin, 0);
+  load_b(part.begin, b0);
+  for (int g = part.begin; g < part.end; g += 2) {
     step(g, b0, b1, 0);
-    if (g + 1 < G) step(g + 1, b1, b0, 1);
+    if (g + 1 < part.end) step(g + 1, b1, b0, 1);
   }
   // the last step's DMA must land, and every wave be past its reads, before the rows' LDS is
   // used for the outputs
@@ -811,7 +827,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       store_gated<BF>(P, tile, stage, at, 16 * i, n0, {acc[i][0], acc[i][2]}, {acc[i][1], acc[i][3]}, slot_of,
                       [&](int m) { return tile.row0 + m; });
     else
-      store_rows<4>(slot_of, P.weights, P.part, N, tile, stage, at, 16 * i, n0, acc[i]);
+      store_rows<4>(slot_of, P.weights, P.part + (size_t)part.slab * P.plan.S * N, N, tile, stage, at, 16 * i, n0, acc[i]);
   }
 }
 
@@ -831,8 +847,8 @@ struct ExpertGradArgs {
   const void *G, *U;             // [slots][C]
   void *dG, *dU;                 // [sorted rows][C]
   float *dw_part;                // [slots][4 columns]
-  float *part;                   // [slots][C]
-  int act, columns;
+  float *part;                   // rows: [slabs][slots][C]
+  int act, columns, slabs;
 };
 
 // A tile of 16 TM rows and 256 outputs of the sum over the terms of A . D, D [R][C] the
@@ -850,9 +866,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   __shared__ __attribute__((aligned(16))) float Cs[TM >= 4 ? 1 : 4][TM >= 4 ? 4 : 1024];  // (else in As0)
   ExpertTile tile;
   int column;
-  if (!place(P.plan, P.columns, blockIdx.x, tile, column)) return;
+  if (!place(P.plan, P.columns * P.slabs, blockIdx.x, tile, column)) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform_int(tid >> 6), c = lane >> 4, r = lane & 15;
   const int R = P.R, C = P.C, KB = C / kTileRows, CG = C / kGroup, NG = R / kGroup;
+  const Part part = part_of(column, P.columns, P.slabs, TERMS * NG);
 
   __amdgpu_buffer_rsrc_t ars[TERMS], wrs[TERMS], mrs[TERMS];
 #pragma unroll
@@ -960,19 +977,18 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     }
   };
   BStage b0, b1;
-  const int stages = TERMS * NG;
   auto step = [&](int i, BStage &cur, BStage &nxt, int buf) {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    const int next = min(i + 1, stages - 1);  // (past the range: the last again, into what nobody reads)
+    const int next = min(i + 1, part.end - 1);  // (past the range: the last again, into what nobody reads)
     load_a(next, buf ^ 1);
     load_b(next, nxt);
     compute(cur, buf);
   };
-  load_a(0, 0);
-  load_b(0, b0);
-  for (int i = 0; i < stages; i += 2) {
+  load_a(part.begin, 0);
+  load_b(part.begin, b0);
+  for (int i = part.begin; i < part.end; i += 2) {
     step(i, b0, b1, 0);
-    if (i + 1 < stages) step(i + 1, b1, b0, 1);
+    if (i + 1 < part.end) step(i + 1, b1, b0, 1);
   }
   // the last step's DMA must land, and every wave be past its reads, before the rows' LDS is
   // used for the outputs
@@ -985,7 +1001,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   if constexpr (EPI == kGradRowsOut) {
 #pragma unroll
     for (int i = 0; i < TM; ++i)
-      if (16 * i < tile.rows) store_rows<4>([&](int m) { return P.plan.order[tile.row0 + m]; }, nullptr, P.part, C, tile, stage, at, 16 * i, n0, acc[i]);
+      if (16 * i < tile.rows) store_rows<4>([&](int m) { return P.plan.order[tile.row0 + m]; }, nullptr,
+                      P.part + (size_t)part.slab * P.plan.S * C, C, tile, stage, at, 16 * i, n0, acc[i]);
   } else {
     // (a loop, with one copy of the activations' code: only the sums are picked by number)
 #pragma unroll 1
@@ -1060,14 +1077,15 @@ __global__ __launch_bounds__(256) void weight_grad_kernel(const int32_t *ids, co
 
 struct CombineArgs {
   const int32_t *ids;
-  const float *part;         // [slots][D]
+  const float *part;         // [slabs][slots][D]
   const void *add;           // [T][D] or null
   const _Float16 *s;         // [D] or null (backward)
   void *out;                 // [T][D]
-  int T, D, k, E;
+  int T, D, k, E, slabs;
 };
 
-// out[t] = add[t] + s * sum of the token's rows, in the order of its slots; four columns
+// out[t] = add[t] + s * sum of the token's rows, in the order of its slots (and for a slot of its
+// slabs); four columns
 // per thread.
 template <bool BF>
 __global__ __launch_bounds__(256) void combine_kernel(CombineArgs P) {
@@ -1087,6 +1105,12 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs P) {
       in[j] = e >= 0 && e < P.E;
       x[j] = float4v{0.f, 0.f, 0.f, 0.f};
       if (in[j]) x[j] = *reinterpret_cast<const float4v *>(rows + (size_t)(j0 + j) * P.D);
+    }
+    for (int i = 1; i < P.slabs; ++i) {
+      const float *slab = rows + (size_t)i * P.T * P.k * P.D;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (in[j]) x[j] += *reinterpret_cast<const float4v *>(slab + (size_t)(j0 + j) * P.D);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) y += x[j];
@@ -1131,58 +1155,72 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 // so that its workspace stays bounded.
 constexpr long long kMaxSlots = 1 << 17;
 
+// the most tiles that S slots can make
+int max_tiles(int S, int E, int rows) { return std::min(S, S / rows + std::min(E, S)); }
+
 int round_tokens(int T, int k, int D) {
   const long long by_slots = std::max<long long>(1, kMaxSlots / k);
   const long long by_bytes = std::max<long long>(1, ((1ll << 31) - 1) / (2ll * D));
   return (int)std::min<long long>(T, std::min(by_slots, by_bytes));
 }
 
-int max_tiles(int S, int E, int rows) { return std::min(S, S / rows + std::min(E, S)); }
 
-// Rows per tile, from the rows that an expert that is chosen at all gets on average, and from
-// whether one tile of each alone gives every CU a workgroup (tiles are 256 outputs wide).
-// Fewer rows than a tile has are loads and MFMAs of nothing; more are another reading of
-// the weights, from the L2.  Times in us:
-//   forward, 64 experts of 1024 x 4096 (256 workgroups or more)
-//     rows  2: 108 by 16 (streaming), 111 by 32         rows  8: 116, 108
-//     rows 20: 120 by 32, 135 by 64                     rows 24: 151, 136
-//     rows 160: 410 by 64, 438 by 128                   rows 192: 481, 462; 512: 1165, 1060
-//   forward, 8 of 14336 x 4096 (128)
-//     rows 12: 220 by 16, 239 by 32                     rows 20: 310, 242
-//     rows 32: 273 by 32, 295 by 64                     rows 40: 310, 299
-//     rows 192: 711 by 64, 725 by 128                   rows 256: 946, 879; 512: 1680, 1607
-//   backward, 64 of 1024 x 4096
-//     rows  8: 130 by 16, 149 by 32                     rows 12: 159, 153
-//     rows 20: 158 by 32, 172 by 64                     rows 24: 188, 176
-//     rows 40: 188 by 64, 223 by 128                    rows 64: 251, 242
-//   backward, 8 of 14336 x 4096
-//     rows 24: 432 by 16, 464 by 32                     rows 32: 558, 514
-//     rows 32: 514 by 32, 521 by 64                     rows 40: 531, 522
-//     rows 128: 778 by 64, 809 by 128                   rows 256: 1242, 1068
-struct RowsRule {
-  int most[3];  // the largest mean for 16, 32 and 64 rows
-};
-int tile_rows(int S, int E, int D, int N, const RowsRule &filled, const RowsRule &few) {
-  const int chosen = std::min(E, S);
-  const RowsRule &rule = (long long)chosen * (std::min(D, N) / 128) >= 512 ? filled : few;
-  int rows = 16;
-  for (int i = 0; i < 3 && (long long)rule.most[i] * chosen < S; ++i) rows *= 2;
+// Rows per tile, from the rows that an expert that is chosen at all gets on average.  Fewer
+// rows than a tile has are loads and MFMAs of nothing; more are another reading of the
+// weights, from the L2, and another decoding.  From 64 on a tile must also leave the
+// first product (`columns` tiles wide) enough workgroups.  Times in us (bf16):
+//   forward                          rows  8: 115 by 16, 109 by 32        rows 24: 152 by 32, 140 by 64
+//   64 experts of 1024 x 4096        rows 48: 171 by 64, 202 by 128       rows 64: 229, 220; 512: 1222, 1061
+//   8 of 14336 x 4096                rows  8: 209 by 16, 180 by 32        rows 24: 193 by 32, 245 by 64; 32: 252, 247
+//                                    rows 48: 264 by 64, 332 by 128       rows 96: 429, 367; 512: 1698, 1494
+//   16 of 1536 x 2048                rows 64: 59 by 32, 71 by 64          rows 192: 108 by 64, 117 by 128; 256: 141, 134
+//   backward
+//   64 experts of 1024 x 4096        rows  8: 131 by 16, 149 by 32        rows 12: 160, 156
+//                                    rows 24: 190 by 32, 179 by 64        rows 48: 204 by 64, 229 by 128; 64: 260, 243
+//   8 of 14336 x 4096                rows  8: 195 by 16, 217 by 32        rows 12: 248, 226
+//                                    rows 24: 227 by 32, 265 by 64; 32: 348, 265
+//                                    rows 48: 290 by 64, 343 by 128; 64: 426, 350
+//   16 of 1536 x 2048                rows 64: 87 by 32, 90 by 64          rows 256: 156 by 64, 162 by 128; 512: 282, 259
+
+int tile_rows(int S, int E, int columns, int most16, int enough) {
+  const long long chosen = std::min(E, S);
+  if (S <= most16 * chosen) return 16;
+  int rows = 32;
+  if (S > 26 * chosen && (long long)max_tiles(S, E, 64) * columns >= enough) rows = 64;
+  if (S > 56 * chosen && (long long)max_tiles(S, E, 128) * columns >= enough) rows = 128;
   return rows;
 }
-int forward_rows(int S, int E, int D, int N) { return tile_rows(S, E, D, N, {{6, 22, 176}}, {{16, 36, 224}}); }
-int backward_rows(int S, int E, int D, int N) { return tile_rows(S, E, D, N, {{10, 22, 56}}, {{28, 36, 160}}); }
+int forward_rows(int S, int E, int N) { return tile_rows(S, E, (N + 127) / 128, 6, 512); }
+int backward_rows(int S, int E, int N) { return tile_rows(S, E, (N + 255) / 256, 10, 384); }
+
+// Parts of the contraction of the product that makes the tokens' rows (D wide), each with its
+// own workgroups and its own slab of sums, which combine_kernel adds.  The GPU holds 512
+// workgroups at once.  Times of the whole call in us, with one, two and four parts:
+//   forward, 8 experts of 14336 x 4096 (112 stages): 160 workgroups 237, 203, 180; 384: 583, 546, 533;
+//   512: 758, 762, 777; 640: 1613, 1494, 1508
+//   forward, 16 of 1536 x 2048 (12): 176: 43, 39, 41; 320: 55, 54, 61
+//   backward, 8 of 14336 x 4096 (224): 160: 459, 286, 217; 384: 780, 701, 636; 512: 878, 880, 886;
+//   640: 1835, 1600, 1577
+//   backward, 16 of 1536 x 2048 (24): 224: 80, 72, 73; 384: 115, 111, 111; 640: 259, 261, 304
+//   backward, 64 of 1024 x 4096 (16): 1152: 158, 165, 186
+int row_slabs(int tiles, int D, int stages) {
+  const long long units = (long long)tiles * ((D + 255) / 256);
+  if (units < 512) return stages >= 64 ? 4 : stages >= 12 ? 2 : 1;
+  return units > 512 && units <= 1280 && stages >= 64 ? 2 : 1;  // (a part's share of the last turn is smaller)
+}
 
 // The workspace of one round.
 struct Layout {
-  int tokens, slots, rows, tiles;  // rows: per tile
+  int tokens, slots, rows, tiles, slabs;  // rows: per tile
   size_t order, list, count, xs, h, part, total;
 };
 Layout layout(const ExpertsDesc &d) {
   Layout l = {};
   l.tokens = round_tokens(d.T, d.k, d.D);
   l.slots = l.tokens * d.k;
-  l.rows = forward_rows(l.slots, d.E, d.D, d.N);
+  l.rows = forward_rows(l.slots, d.E, d.N);
   l.tiles = max_tiles(l.slots, d.E, l.rows);
+  l.slabs = l.rows == 16 ? 1 : row_slabs(l.tiles, d.D, d.N / kGroup);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -1194,7 +1232,7 @@ Layout layout(const ExpertsDesc &d) {
   l.count = take(4);
   l.xs = take(d.s ? (size_t)l.tokens * d.D * 2 : 0);
   l.h = take((size_t)l.slots * d.N * 2);
-  l.part = take((size_t)l.slots * d.D * 4);
+  l.part = take((size_t)l.slabs * l.slots * d.D * 4);
   l.total = at;
   return l;
 }
@@ -1220,7 +1258,7 @@ StreamShape stream_shape(bool gated, int blocks, int groups, int tiles) {
 }
 
 template <int EPI, bool GATHER, bool BF>
-hipError_t launch_product(ExpertArgs a, int rows, int tiles, hipStream_t stream) {
+hipError_t launch_product(ExpertArgs a, int rows, int tiles, int slabs, hipStream_t stream) {
   const int blocks = (EPI == kGatedOut ? 2 : 1) * (a.N / kTileRows);
   if (rows == 16) {
     const StreamShape s = stream_shape(EPI == kGatedOut, blocks, a.K / kGroup, tiles);
@@ -1237,7 +1275,8 @@ hipError_t launch_product(ExpertArgs a, int rows, int tiles, hipStream_t stream)
 #undef W4_STREAM
   } else {
     a.columns = (blocks + 15) / 16;
-    const dim3 grid((unsigned)((tiles * a.columns + 7) / 8 * 8));
+    a.slabs = slabs;
+    const dim3 grid((unsigned)((tiles * a.columns * slabs + 7) / 8 * 8));
     if (rows == 32)
       hipLaunchKernelGGL((expert_tile_kernel<2, EPI, GATHER, BF>), grid, dim3(256), 0, stream, a);
     else if (rows == 64)
@@ -1296,12 +1335,12 @@ hipError_t launch_experts_typed(const ExpertsDesc &d, char *ws, hipStream_t stre
     a.G = d.G ? static_cast<char *>(d.G) + t0 * slot_n : nullptr;
     a.U = d.U ? static_cast<char *>(d.U) + t0 * slot_n : nullptr;
     a.H = ws + l.h;
-    if ((e = launch_product<kGatedOut, true, BF>(a, l.rows, tiles, stream)) != hipSuccess) return e;
+    if ((e = launch_product<kGatedOut, true, BF>(a, l.rows, tiles, 1, stream)) != hipSuccess) return e;
     weight(0, d.down);
     shape(d.D, d.N);
     a.A = ws + l.h;
     a.part = reinterpret_cast<float *>(ws + l.part);
-    if ((e = launch_product<kRowsOut, false, BF>(a, l.rows, tiles, stream)) != hipSuccess) return e;
+    if ((e = launch_product<kRowsOut, false, BF>(a, l.rows, tiles, l.slabs, stream)) != hipSuccess) return e;
     const size_t row = (size_t)t0 * d.D * 2;
     CombineArgs c = {};
     c.ids = ids;
@@ -1312,6 +1351,7 @@ hipError_t launch_experts_typed(const ExpertsDesc &d, char *ws, hipStream_t stre
     c.D = d.D;
     c.k = d.k;
     c.E = d.E;
+    c.slabs = l.slabs;
     hipLaunchKernelGGL(combine_kernel<BF>, dim3((unsigned)(((long long)T * d.D / 4 + 255) / 256)), dim3(256), 0, stream, c);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
@@ -1321,16 +1361,17 @@ hipError_t launch_experts_typed(const ExpertsDesc &d, char *ws, hipStream_t stre
 // ---- backward launches
 
 struct GradLayout {
-  int tokens, slots, rows, tiles, columns;
+  int tokens, slots, rows, tiles, columns, slabs;
   size_t order, list, count, dg, du, dw, part, total;
 };
 GradLayout grad_layout(const ExpertsGradDesc &d) {
   GradLayout l = {};
   l.tokens = round_tokens(d.T, d.k, d.D);
   l.slots = l.tokens * d.k;
-  l.rows = backward_rows(l.slots, d.E, d.D, d.N);
+  l.rows = backward_rows(l.slots, d.E, d.N);
   l.tiles = max_tiles(l.slots, d.E, l.rows);
   l.columns = (d.N + 255) / 256;
+  l.slabs = row_slabs(l.tiles, d.D, 2 * (d.N / kGroup));
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -1343,15 +1384,16 @@ GradLayout grad_layout(const ExpertsGradDesc &d) {
   l.dg = take((size_t)l.slots * d.N * 2);
   l.du = take((size_t)l.slots * d.N * 2);
   l.dw = take((size_t)l.slots * l.columns * 16);
-  l.part = take((size_t)l.slots * d.D * 4);
+  l.part = take((size_t)l.slabs * l.slots * d.D * 4);
   l.total = at;
   return l;
 }
 
 template <int EPI, bool GATHER, bool BF>
-hipError_t launch_grad_product(ExpertGradArgs a, int rows, int tiles, hipStream_t stream) {
+hipError_t launch_grad_product(ExpertGradArgs a, int rows, int tiles, int slabs, hipStream_t stream) {
   a.columns = (a.C + 255) / 256;
-  const dim3 grid((unsigned)((tiles * a.columns + 7) / 8 * 8));
+  a.slabs = slabs;
+  const dim3 grid((unsigned)((tiles * a.columns * slabs + 7) / 8 * 8));
 #define W4_GRAD(TM)                                                                              \
   if (rows == 16 * TM)                                                                           \
   hipLaunchKernelGGL((expert_grad_kernel<TM, EPI, GATHER, BF>), grid, dim3(256), 0, stream, a)
@@ -1393,7 +1435,7 @@ hipError_t launch_experts_grad_typed(const ExpertsGradDesc &d, char *ws, hipStre
     a.dG = ws + l.dg;
     a.dU = ws + l.du;
     a.dw_part = reinterpret_cast<float *>(ws + l.dw);
-    hipError_t e = launch_grad_product<kActGradOut, true, BF>(a, l.rows, tiles, stream);
+    hipError_t e = launch_grad_product<kActGradOut, true, BF>(a, l.rows, tiles, 1, stream);
     if (e != hipSuccess) return e;
     if (d.dweights)
       hipLaunchKernelGGL(weight_grad_kernel<BF>, dim3((unsigned)((S + 3) / 4)), dim3(256), 0, stream, ids, a.dw_part,
@@ -1408,7 +1450,7 @@ hipError_t launch_experts_grad_typed(const ExpertsGradDesc &d, char *ws, hipStre
       a.R = d.N;
       a.C = d.D;
       a.part = reinterpret_cast<float *>(ws + l.part);
-      if ((e = launch_grad_product<kGradRowsOut, false, BF>(a, l.rows, tiles, stream)) != hipSuccess) return e;
+      if ((e = launch_grad_product<kGradRowsOut, false, BF>(a, l.rows, tiles, l.slabs, stream)) != hipSuccess) return e;
       CombineArgs c = {};
       c.ids = ids;
       c.part = a.part;
@@ -1419,6 +1461,7 @@ hipError_t launch_experts_grad_typed(const ExpertsGradDesc &d, char *ws, hipStre
       c.D = d.D;
       c.k = d.k;
       c.E = d.E;
+      c.slabs = l.slabs;
       hipLaunchKernelGGL(combine_kernel<BF>, dim3((unsigned)(((long long)T * d.D / 4 + 255) / 256)), dim3(256), 0, stream, c);
     }
     if ((e = hipGetLastError()) != hipSuccess) return e;
