@@ -663,7 +663,8 @@ int w4a16_experts(const w4a16_experts_call *call, void *workspace, size_t worksp
  *   dX[t] = add[t] + s * sum over j of (dG . Wg_e + dU . Wu_e).
  * gate, up and down are the transposed copies (w4a16_transpose) of the E weights, one after
  * the other in each buffer.  dX and add (or NULL; may be dX) [T][D] and dweights [T][k] are
- * of the activations' type: the products round each weight, and dG and dU, to it once, as
+ * of the activations' type, dweights fp32 (as w4a16_route_backward takes them) where
+ * dweights_f32 is not 0; the products round each weight, and dG and dU, to that type once, as
  * w4a16_gated_backward's do.  dX or dweights may be NULL; add needs dX.  A slot that names
  * no expert has dweights 0, and its G and U are not read.  Limits, errors and workspace
  * (w4a16_experts_backward_workspace_size() bytes) as for w4a16_experts. */
@@ -687,6 +688,7 @@ typedef struct w4a16_experts_backward_call {
   int64_t T, E, k, D, N;
   int32_t act;
   int32_t dtype;
+  int32_t dweights_f32;
 } w4a16_experts_backward_call;
 
 int w4a16_experts_backward_workspace_size(const w4a16_experts_backward_call *call, size_t *bytes);

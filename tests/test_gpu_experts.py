@@ -284,7 +284,8 @@ def test_weights_past_32_bit_offsets():
 
 # ---- backward --------------------------------------------------------------------------------
 
-def run_backward(T, E, k, D, N, dtype="bf16", act="silu", kind="even", s=False, add=False, want_dx=True, want_dw=True):
+def run_backward(T, E, k, D, N, dtype="bf16", act="silu", kind="even", s=False, add=False, want_dx=True, want_dw=True,
+                 f32=False):
     torch = torch_cuda()
     note(f"experts backward T={T} E={E} k={k} D={D} N={N} {dtype} {act} {kind} s={s} add={add}")
     st = stack(1, E, N, D), stack(2, E, N, D), stack(3, E, D, N)
@@ -298,7 +299,7 @@ def run_backward(T, E, k, D, N, dtype="bf16", act="silu", kind="even", s=False, 
     G[off], U[off] = float("nan"), float("inf")       # a skipped slot's are not read
     buf = torch.full((T + 2, D), 777.0, dtype=dY.dtype, device="cuda")
     dX = buf[:T] if want_dx else None
-    dw = torch.full((T, k), float("nan"), dtype=dY.dtype, device="cuda") if want_dw else None
+    dw = torch.full((T, k), float("nan"), dtype=torch.float32 if f32 else dY.dtype, device="cuda") if want_dw else None
     call = w4.ExpertsBackwardCall(dY, to_dev(ids), to_dev(w), G, U, *(x.transposed() for x in st), dX, dw, s=sd, s_down=sdd,
                                   act=ACT[act], add=A)
     call.ws.fill_(0x7f)
@@ -332,7 +333,7 @@ def run_backward(T, E, k, D, N, dtype="bf16", act="silu", kind="even", s=False, 
         check(dX, rX, 1.05 * sq * (bX + (k + 4) * E32 * mag) + extra + u * np.abs(rX) + TINY, "dX")
         assert bool((buf[T:] == 777.0).all()), "rows behind the output were written"
     if want_dw:
-        check(dw, rw, 1.05 * bw + u * np.abs(rw) + TINY, "dweights")
+        check(dw, rw, 1.05 * bw + (E32 if f32 else u) * np.abs(rw) + TINY, "dweights")
     first = [None if x is None else x.clone() for x in (dX, dw)]
     call()
     for x, y in zip(first, (dX, dw)):
@@ -367,6 +368,8 @@ def test_backward_routings(T, kind):
 def test_backward_parts():
     run_backward(20, 4, 2, 128, 256, want_dx=False)
     run_backward(20, 4, 2, 128, 256, want_dw=False, s=True)
+    run_backward(20, 4, 2, 128, 256, want_dx=False, f32=True)
+    run_backward(70, 3, 2, 256, 384, "fp16", kind="skip", s=True, add=True, f32=True)
 
 
 def test_graphs_streams_and_workspaces():

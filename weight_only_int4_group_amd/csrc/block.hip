@@ -184,6 +184,7 @@ w4a16::ExpertsGradDesc experts_grad_desc(const w4a16_experts_backward_call &c) {
   d.add = c.add;
   d.dX = c.dX;
   d.dweights = c.dweights;
+  d.dweights_f32 = c.dweights_f32 != 0;
   d.T = (int)c.T;
   d.E = (int)c.E;
   d.k = (int)c.k;
@@ -344,11 +345,12 @@ int w4a16_experts_backward(const w4a16_experts_backward_call *c, void *workspace
   const size_t rows = (size_t)(c->T * c->D) * 2, slots = (size_t)(c->T * c->k), kept = slots * c->N * 2;
   const size_t codes = (size_t)(c->E * (c->N * c->D / 2)), E = (size_t)c->E;
   const size_t meta = (size_t)(c->E * (c->N / W4A16_GROUP) * (c->D / W4A16_GROUP) * 512);
-  if (overlaps({{c->dX, rows}, {c->dweights, slots * 2}, {workspace, need}},
+  const size_t grads = slots * (c->dweights_f32 ? 4 : 2);
+  if (overlaps({{c->dX, rows}, {c->dweights, grads}, {workspace, need}},
                {{c->dY, rows}, {c->ids, slots * 4}, {c->weights, slots * 4}, {c->G, kept}, {c->U, kept},
                 {c->gate.Wt, codes}, {c->up.Wt, codes}, {c->down.Wt, codes}, {c->gate.meta, meta}, {c->up.meta, meta},
                 {c->down.meta, meta}, {c->s, (size_t)c->D * 2}, {c->s_down, E * c->N * 2}}, 0) ||
-      overlaps({{c->dweights, slots * 2}, {workspace, need}}, {{c->add, rows}}, 0) ||
+      overlaps({{c->dweights, grads}, {workspace, need}}, {{c->add, rows}}, 0) ||
       overlaps({{c->dX, rows}}, {{c->add, rows}}, 1))
     return W4A16_EINVAL;
   return status(w4a16::launch_experts_grad(d, workspace, static_cast<hipStream_t>(stream)));

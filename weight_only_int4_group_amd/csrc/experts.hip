@@ -1061,7 +1061,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 // fixed order; 0 for a slot that names no expert.
 template <bool BF>
 __global__ __launch_bounds__(256) void weight_grad_kernel(const int32_t *ids, const float *part, int stride, int parts,
-                                                          int S, int E, uint16_t *dw) {
+                                                          int S, int E, void *dw, bool f32) {
   const int slot = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
   if (slot >= S) return;
   const int e = ids[slot];
@@ -1070,7 +1070,11 @@ __global__ __launch_bounds__(256) void weight_grad_kernel(const int32_t *ids, co
     for (int i = lane; i < parts; i += 64) s += part[(size_t)slot * stride + i];
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
-  if (lane == 0) dw[slot] = f32_to_act<BF>(s);
+  if (lane != 0) return;
+  if (f32)
+    static_cast<float *>(dw)[slot] = s;
+  else
+    static_cast<uint16_t *>(dw)[slot] = f32_to_act<BF>(s);
 }
 
 // ---- joining a token's slots ---------------------------------------------------------------------
@@ -1439,7 +1443,8 @@ hipError_t launch_experts_grad_typed(const ExpertsGradDesc &d, char *ws, hipStre
     if (e != hipSuccess) return e;
     if (d.dweights)
       hipLaunchKernelGGL(weight_grad_kernel<BF>, dim3((unsigned)((S + 3) / 4)), dim3(256), 0, stream, ids, a.dw_part,
-                         4 * l.columns, d.N / 64, S, d.E, static_cast<uint16_t *>(d.dweights) + (size_t)t0 * d.k);
+                         4 * l.columns, d.N / 64, S, d.E,
+                         static_cast<char *>(d.dweights) + (size_t)t0 * d.k * (d.dweights_f32 ? 4 : 2), d.dweights_f32);
     if (d.dX) {
       a.A[0] = a.dG;
       a.A[1] = a.dU;

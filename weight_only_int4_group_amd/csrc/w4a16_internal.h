@@ -206,6 +206,7 @@ struct ExpertsGradDesc {
   ExpertTransposed gate, up, down;
   const void *s, *s_down, *add;
   void *dX, *dweights;
+  bool dweights_f32;
   int T, E, k, D, N, act;
   bool bf16;
 };

@@ -82,7 +82,7 @@ class ExpertsBackwardStruct(ctypes.Structure):
                 ("gate", ExpertTransposedStruct), ("up", ExpertTransposedStruct),
                 ("down", ExpertTransposedStruct), ("s", _VP), ("s_down", _VP), ("add", _VP), ("dX", _VP),
                 ("dweights", _VP), ("T", _I64), ("E", _I64), ("k", _I64), ("D", _I64), ("N", _I64),
-                ("act", _I32), ("dtype", _I32)]
+                ("act", _I32), ("dtype", _I32), ("dweights_f32", _I32)]
 
 
 def _declare(L):
@@ -469,9 +469,10 @@ def _transposed_struct(w, name, shape, device):
 
 
 class ExpertsBackwardCall(_PreparedCall):
-    """A prepared w4a16_experts_backward call: dX [T][D] (or None) and dweights [T][k] (or None), of
-    the activations' type, from dY, the routing and the G and U of the forward; gate, up and
-    down TransposedExperts; add [T][D] (or None; may be dX) is added to dX."""
+    """A prepared w4a16_experts_backward call: dX [T][D] (or None), of the activations' type, and
+    dweights [T][k] (or None), fp32 (as w4a16_route_backward takes them) or of that type, from dY,
+    the routing and the G and U of the forward; gate, up and down TransposedExperts; add [T][D]
+    (or None; may be dX) is added to dX."""
 
     def __init__(self, dY, ids, weights, G, U, gate, up, down, dX, dweights, s=None, s_down=None, act=ACT_SILU,
                  add=None, stream=None, workspace=None):
@@ -482,6 +483,7 @@ class ExpertsBackwardCall(_PreparedCall):
         (T, D), E, N = dY.shape, gate.E, gate.N
         k, slots = _slots_ptrs(ids, weights, T, device)
         self.keep = (dY, ids, weights, G, U, gate, up, down, dX, dweights, s, s_down, add)
+        f32 = dweights is not None and dweights.dtype == torch.float32
         self.call = ExpertsBackwardStruct(
             _dev_ptr(dY, "dY", dt), *slots, _shaped_ptr(G, "G", dt, (T, k, N), device),
             _shaped_ptr(U, "U", dt, (T, k, N), device), _transposed_struct(gate, "gate", (E, N, D), device),
@@ -489,16 +491,17 @@ class ExpertsBackwardCall(_PreparedCall):
             _shaped_ptr(s, "s", torch.float16, (D,), device),
             _shaped_ptr(s_down, "s_down", torch.float16, (E, N), device),
             _shaped_ptr(add, "add", dt, (T, D), device), _shaped_ptr(dX, "dX", dt, (T, D), device),
-            _shaped_ptr(dweights, "dweights", dt, (T, k), device), T, E, k, D, N, act, _dtype_code(dt))
+            _shaped_ptr(dweights, "dweights", torch.float32 if f32 else dt, (T, k), device), T, E, k, D, N, act,
+            _dtype_code(dt), int(f32))
         nbytes = self._size("w4a16_experts_backward_workspace_size", ctypes.byref(self.call))
         self._prepare(device, nbytes, workspace, stream)
         self._bind("w4a16_experts_backward", ctypes.byref(self.call))
 
 
 def w4a16_experts_backward(dY, ids, weights, G, U, gate, up, down, s=None, s_down=None, act=ACT_SILU, add=None):
-    """Backward of w4a16_experts on the current stream: (dX, dweights).  Arguments as for
-    ExpertsBackwardCall."""
+    """Backward of w4a16_experts on the current stream: (dX, dweights), dweights fp32.  Arguments
+    as for ExpertsBackwardCall."""
     torch = _torch()
-    dX, dw = torch.empty_like(dY), torch.empty(ids.shape, dtype=dY.dtype, device=dY.device)
+    dX, dw = torch.empty_like(dY), torch.empty(ids.shape, dtype=torch.float32, device=dY.device)
     ExpertsBackwardCall(dY, ids, weights, G, U, gate, up, down, dX, dw, s, s_down, act, add)()
     return dX, dw
