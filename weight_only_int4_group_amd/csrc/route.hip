@@ -22,7 +22,11 @@
 //   otherwise     softmax  dl = score (g - sum score g) on all (g = 0 on those not chosen)
 //                 sigmoid  dl = g score (1 - score)
 //
-// Bound by HBM for many tokens (a read of the logits; the backward writes as much).
+// Bound by vector instructions: a choice is a maximum over the wave for each of the k, a score an
+// fp64 exponential.  One token of 64 experts takes 2.8 us (a launch); 8192 tokens, 8 of 256
+// experts each, fp32: 8.3 us by the logits, 13.9 with a bias (64-bit keys), 18.5 with groups
+// too, for a read of 8 MB; their backward 8.0.  (32-bit keys where all of a token's values
+// differ in them, with the rest as before, and sorted lists per lane: 17.5 to 18.9 with groups.)
 #include "epilogue.h"
 #include "w4a16_device.h"
 #include "w4a16_internal.h"
