@@ -579,9 +579,10 @@ int w4a16_norm_block_backward(const w4a16_norm_backward_call *call, void *worksp
  *   weight  scale * score, divided by the sum of the k chosen scores if renormalize
  * ids int32 [T][k], in the order of the choice, and weights fp32 [T][k].  Choices are made
  * as exact arithmetic would make them: without a bias experts are compared by their
- * logits, and with one, as groups always are, by scores to 2^-50.  An expert whose logit is -inf or NaN is never chosen, whatever its bias
- * (finite); where fewer than k are left to choose, the last slots have id -1 and weight 0.
- * +inf counts as the largest finite fp32 value.
+ * logits, and with one, as groups always are, by scores to 2^-50.  An expert whose logit is
+ * -inf or NaN is never chosen, whatever its bias (finite); where fewer than k are left to
+ * choose, the last slots have id -1 and weight 0.  +inf counts as the largest finite fp32
+ * value.
  * 0 <= T <= 2^22, 1 <= E <= 1024, 1 <= k <= 64, 1 <= groups <= 64 dividing E,
  * 1 <= topk_groups <= groups, k <= topk_groups * (E / groups), scale finite (EINVAL).
  * Outputs must not overlap each other or an input.  Asynchronous on `stream`. */
@@ -623,7 +624,7 @@ int w4a16_route_backward(const w4a16_routing *routing, const void *dweights, con
  * Y; sums are held in fp32.  Weights are not rounded: codes are multiplied exactly, scales
  * and zero points applied to the fp32 sums of their group.  (Only where an expert
  * gets more than 56 slots on average may each weight be rounded once to the activations'
- * type instead, as in the dense products.)
+ * type instead, as in the dense products.)  An infinite activation may give NaN.
  * 0 <= T <= 2^22, 1 <= E <= 1024, 1 <= k <= 64, D and N multiples of 128 up to 2^20 with
  * N * D / 2 < 2^31 - 2^20 (EINVAL).  workspace: w4a16_experts_workspace_size() bytes
  * (it depends on T, E, k, D, N and whether s is set), 256-byte aligned; EINVAL if smaller.

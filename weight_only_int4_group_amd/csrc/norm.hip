@@ -652,12 +652,17 @@ void launch_norm_grad_rows(const NormGradArgs &a, hipStream_t stream) {
 #define W4_NORM(TPR, CPT)                                                                        \
   hipLaunchKernelGGL((norm_grad_kernel<TPR, CPT, BF, VEC, false>), dim3((unsigned)a.d.T),        \
                      dim3(TPR), 0, stream, a)
-  if (D <= 64 * 8)
-    W4_NORM(64, 8);
-  else if (D <= 512 * 8)
-    W4_NORM(512, 8);
-  else
-    W4_NORM(1024, 16);
+  if constexpr (!VEC) {  // (shorter rows of 16-byte pieces take the sums along)
+    if (D <= 64 * 8) {
+      W4_NORM(64, 8);
+      return;
+    }
+    if (D <= 512 * 8) {
+      W4_NORM(512, 8);
+      return;
+    }
+  }
+  W4_NORM(1024, 16);
 #undef W4_NORM
 }
 
