@@ -469,7 +469,7 @@ __global__ __launch_bounds__(64 * KS) __attribute__((amdgpu_waves_per_eu(TN == 2
 // half of what their four MFMAs take.  The sums of a group's activations, which the zero
 // points multiply, are MFMAs with ones: wave i takes those of row block i, and they reach
 // the other waves through LDS a stage later.  64 tokens, 8 of 64 experts of 1024 x 4096 (fp16, 32
-// rows): gate and up 60 us (4.7 TB/s of weights), down 39 (3.7, and 8 MB written); 48 rows
+// rows): gate and up 58 us (4.9 TB/s of weights), down 36.6 (3.9, and 8 MB written); 48 rows
 // per expert and more are bound by the issue of vector instructions (4.35 to an MFMA).
 template <int TM, int EPI, bool GATHER, bool BF>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void expert_tile_kernel(ExpertArgs P) {
@@ -528,12 +528,16 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     u32x4 w[TN];
   };
   uint32_t sc[TN], zp[TN];  // raw fp16 scale and zero point of the latest group
+  // (32 rows: an expert has a tile or two, and streaming loads leave the L2 to the rest: gate and up
+  // of 64 experts as above 60 -> 58 us, down 38.5 -> 36.6; weights that all fit in the caches and
+  // are there already, 76 MB, 40 -> 42)
+  constexpr int kStreaming = TM == 2 ? 2 : 0;
   auto load_codes = [&](int g, Codes &b) {
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
       const int rb = min(vb0 + j, STEP * NB - 1) / STEP;
       b.w[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                             wrs[j % STEP], lane * 16, (G0 + g) * tile_stride + rb * kTileBytes, 0));
+                                             wrs[j % STEP], lane * 16, (G0 + g) * tile_stride + rb * kTileBytes, kStreaming));
     }
   };
   auto load_meta = [&](int step) {
