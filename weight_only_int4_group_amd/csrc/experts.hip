@@ -699,7 +699,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 // them: each weight is rounded to the activations' type, as in the dense layers, and the
 // MFMAs add to the sums at once.  Decoding a weight costs three times as much that way,
 // shared by twice the rows, and no FMAs follow the MFMAs.  4096 tokens, 8 of 64 experts of
-// 1024 x 4096 (bf16): gate and up 560-600 us (550 GFLOP), down 396-410 (275 GFLOP, 537 MB written); by
+// 1024 x 4096 (bf16): gate and up 560-600 us (550 GFLOP), down 395-410 (275 GFLOP, 537 MB written); by
 // 64 rows with exact codes 663 and 453.  MFMAs and vector instructions take turns (41% and 31%
 // of the time).
 template <int EPI, bool GATHER, bool BF>
