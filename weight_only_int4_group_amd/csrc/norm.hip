@@ -576,7 +576,7 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 // Strips of a backward call: about 2^18 threads of them (four waves per SIMD), of at
 // least 8 rows; within one gate vector's rows each, or of whole ones.  The backward of
 // 4092 x 4096 (layer norms and four gates, bf16) takes 57 + 8 us so, and with half as
-// many strips 75 + 5.
+// many strips 75 + 5 (two rows at a time there, for 176 registers: 73 + 5).
 struct NormPlan {
   bool fused;  // the sums are taken where the rows are
   int tpr, cpt;
