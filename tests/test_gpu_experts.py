@@ -220,6 +220,41 @@ def test_long_contraction_and_many_experts():
     run_forward(50, 130, 8, 128, 128, "fp16", kind="skip")
 
 
+@pytest.mark.parametrize("T,E,k,D,N", [(5, 4, 2, 256, 128), (40, 3, 2, 256, 384), (200, 40, 8, 256, 1024),
+                                       (1900, 2, 2, 128, 2176)])
+def test_nothing_of_padded_tokens_is_read(T, E, k, D, N):
+    """Tokens without an expert hold NaN, their weights and kept products too; the others give the bits that they
+    give beside finite ones, and a padded token's row is the residual."""
+    torch = torch_cuda()
+    note(f"experts padded T={T} E={E} k={k} D={D} N={N}")
+    st = stack(1, E, N, D), stack(2, E, N, D), stack(3, E, D, N)
+    ids, w = routing(T, E, k)
+    pad = np.arange(T) % 3 == 1
+    ids[pad] = -1
+    X, _ = tensor("bf16", 41, T, D)
+    R, _ = tensor("bf16", 42, T, D)
+    dY, _ = tensor("bf16", 43, T, D)
+    idd, wd, off = to_dev(ids), to_dev(w), to_dev(pad)
+    G, U = (torch.zeros(T, k, N, dtype=X.dtype, device="cuda") for _ in range(2))
+    back = [x.transposed() for x in st]
+
+    def run():
+        Y = w4.w4a16_experts(X, idd, wd, *(x.dev for x in st), residual=R, preact=(G, U))
+        return (Y, *w4.w4a16_experts_backward(dY, idd, wd, G, U, *back, add=R))
+    want = [t.clone() for t in run()]
+    for t in (X, dY, G, U, wd):
+        t[off] = float("nan")
+    got = run()
+    assert all(bool(torch.isfinite(t).all()) for t in got)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert torch.equal(got[0][off], R[off]) and torch.equal(got[1][off], R[off]) and bool((got[2][off] == 0).all())
+
+
+def test_most_experts_and_slots():
+    run_forward(3, 1024, 64, 128, 128, "bf16", s=True, train=True)
+    run_backward(3, 1024, 64, 128, 128, "fp16", f32=True)
+
+
 def test_no_tokens():
     torch = torch_cuda()
     st = stack(1, 2, 128, 128), stack(2, 2, 128, 128), stack(3, 2, 128, 128)
