@@ -186,6 +186,7 @@ def experts_backward_rc(ws=at(20), nbytes=1 << 25, **kw):
     (dict(dY=ODD), -2), (dict(G=ODD), -2), (dict(add=ODD), -2), (dict(dX=ODD), -2), (dict(dweights=ODD), -2),
     (dict(ws=None), -1), (dict(nbytes=64), -1), (dict(ws=at(20) + 128), -2), (dict(dX=at(0)), -1), (dict(dX=at(3)), -1),
     (dict(dweights=at(8)), -1), (dict(dX=at(7) + 32), -1), (dict(dweights=at(7)), -1), (dict(dX=at(20)), -1),
+    (dict(dweights=at(7) - 16, dweights_f32=1), -1),   # 8 slots: 32 bytes in fp32
     (dict(T=0, dY=None), 0),
 ])
 def test_experts_backward_refusals(kw, code):

@@ -1185,7 +1185,6 @@ int round_tokens(int T, int k, int D) {
   return (int)std::min<long long>(T, std::min(by_slots, by_bytes));
 }
 
-
 // Rows per tile, from the rows that an expert that is chosen at all gets on average.  Fewer
 // rows than a tile has are loads and MFMAs of nothing; more are another reading of the
 // weights, from the L2, and another decoding.  From 64 on a tile must also leave the
@@ -1202,7 +1201,6 @@ int round_tokens(int T, int k, int D) {
 //                                    rows 24: 227 by 32, 265 by 64; 32: 348, 265
 //                                    rows 48: 290 by 64, 343 by 128; 64: 426, 350
 //   16 of 1536 x 2048                rows 64: 87 by 32, 90 by 64          rows 256: 156 by 64, 162 by 128; 512: 282, 259
-
 int tile_rows(int S, int E, int columns, int most16, int enough) {
   const long long chosen = std::min(E, S);
   if (S <= most16 * chosen) return 16;
