@@ -142,7 +142,8 @@ def route_backward(dweights, logits, ids, score="softmax", renormalize=True, sca
             q = shares(l[t, e], score)
             g = q * (g - (q * g).sum())
             if score == "sigmoid":
-                g = g / (1.0 + np.exp(l[t, e]))
+                with np.errstate(over="ignore"):  # (a score of 1: no gradient)
+                    g = g / (1.0 + np.exp(l[t, e]))
             np.add.at(d[t], e, g)
         elif score == "sigmoid":
             np.add.at(d[t], e, g * s[t, e] * (1.0 - s[t, e]))
