@@ -540,7 +540,8 @@ int w4a16_norm_block(const w4a16_norm_call *call, void *stream);
  * both [T][D] of the activations' type, rounded once, or NULL.  Statistics are taken
  * again from y and r, so nothing else is kept by the forward.  The fp32 gradients dgate
  * (the gate's shape) and dpost_weight, dpost_bias, dpre_weight, dpre_bias [D], each or
- * NULL, are sums over rows in a fixed order; one of an absent gate or norm is EINVAL.
+ * NULL, are sums over rows in a fixed order (T = 0: zeros for the norms', while a gate has
+ * no rows and dgate is not written); one of an absent gate or norm is EINVAL.
  * Outputs must not overlap each other or any input.  workspace:
  * w4a16_norm_block_backward_workspace_size() bytes for the same call (it depends on T, D,
  * gate_rows and which gradients are wanted; may be 0), 256-byte aligned; EINVAL if

@@ -195,6 +195,49 @@ def test_no_tokens():
     assert dx.shape == (0, 64) and bool((g.pre_weight == 0).all())
 
 
+@pytest.mark.parametrize("rows", [None, 0])
+@pytest.mark.parametrize("how", ["current", "handle", "graph"])
+def test_no_tokens_with_a_gate(rows, how):
+    """A gate of one vector or of none: its gradient is a sum over no rows, zeros, on the stream
+    of the call."""
+    torch = torch_cuda()
+    D = 64
+    note(f"norm without tokens, gate rows {rows}, {how}")
+    x = torch.empty(0, D, dtype=torch.float16, device="cuda")
+    gate = torch.ones(*([] if rows is None else [rows]), D, device="cuda").half()
+    post, pre = (w4.Norm(w4.NORM_RMS, torch.ones(D, device="cuda").half()) for _ in range(2))
+    r, h = w4.w4a16_norm_block(x, x, post=post, pre=pre, gate=gate)
+    assert r.shape == h.shape == (0, D)
+    sums = w4.NormGrads(torch.empty(gate.shape, device="cuda"), *(torch.empty(D, device="cuda") for _ in range(4)))
+    sums.post_bias = sums.pre_bias = None
+    side = torch.cuda.Stream()
+    call = w4.NormBlockBackwardCall(x, x, x, x, torch.empty_like(x), torch.empty_like(x), sums, post, pre, gate,
+                                    stream=side.cuda_stream if how == "handle" else None)
+    got = [g for g in vars(sums).values() if g is not None]
+
+    def fill():
+        for g in got:
+            g.fill_(float("nan"))
+        torch.cuda.synchronize()
+    fill()
+    if how == "graph":
+        side.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            call()
+        for _ in range(3):
+            fill()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(bool((g == 0).all()) for g in got)
+    else:
+        call()
+        torch.cuda.synchronize()
+        assert all(bool((g == 0).all()) for g in got)
+    grads = w4.w4a16_norm_block_backward(x, x, x, x, post, pre, gate)[2]
+    assert grads.gate.shape == gate.shape and bool((grads.gate == 0).all())
+
+
 # ---- backward --------------------------------------------------------------------------------
 
 def grad_error(d, v, kind, eps, e_d):
