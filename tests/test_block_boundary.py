@@ -241,3 +241,12 @@ def test_block_kernels_keep_everything_in_registers(source, tmp_path):
     assert kernels
     bad = [k for k in kernels if k[1] or k[2] or k[3]]
     assert not bad, f"{source}: (kernel, private bytes, VGPR spills, SGPR spills): {bad}"
+
+
+def test_gate_of_an_empty_batch():
+    """A gate of one row serves all tokens, also where there are none."""
+    import torch
+    for shape, want in (((64,), (64,)), ((1, 64), (1, 64)), ((0, 64), (0, 64))):
+        assert ex._gate_shape(torch.zeros(shape), None, 0, 64)[0] == want
+    assert ex._gate_shape(torch.zeros(1, 64), 5, 0, 64) == ((1, 64), 5)
+    assert ex._gate_shape(torch.zeros(2, 64), 5, 0, 64)[0] == (0, 64)      # refused: two rows for no token

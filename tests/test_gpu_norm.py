@@ -195,10 +195,10 @@ def test_no_tokens():
     assert dx.shape == (0, 64) and bool((g.pre_weight == 0).all())
 
 
-@pytest.mark.parametrize("rows", [None, 0])
+@pytest.mark.parametrize("rows", [None, 1, 0])
 @pytest.mark.parametrize("how", ["current", "handle", "graph"])
 def test_no_tokens_with_a_gate(rows, how):
-    """A gate of one vector or of none: its gradient is a sum over no rows, zeros, on the stream
+    """A gate of one vector ([D] or [1][D]) or of none: its gradient is a sum over no rows, zeros, on the stream
     of the call."""
     torch = torch_cuda()
     D = 64
