@@ -250,3 +250,12 @@ def test_gate_of_an_empty_batch():
         assert ex._gate_shape(torch.zeros(shape), None, 0, 64)[0] == want
     assert ex._gate_shape(torch.zeros(1, 64), 5, 0, 64) == ((1, 64), 5)
     assert ex._gate_shape(torch.zeros(2, 64), 5, 0, 64)[0] == (0, 64)      # refused: two rows for no token
+
+
+@pytest.mark.parametrize("rows", [4, 1 << 40, (1 << 63) - 1])
+def test_one_gate_for_all_is_checked_whatever_its_rows(rows):
+    """An output over the gate is refused, also where T + gate_rows would pass 64 bits."""
+    for kw in (dict(h=at(2)), dict(r=at(2)), dict(h=at(2) + 64)):
+        assert norm_rc(gate_rows=rows, **kw) == -1
+    for kw in (dict(dx=at(4)), dict(dy=at(4) + 64), dict(dgate=at(4)), dict(dgate=at(9) + 256), dict(dgate=at(2))):
+        assert norm_backward_rc(gate_rows=rows, **kw) == -1

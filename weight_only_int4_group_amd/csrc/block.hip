@@ -67,7 +67,12 @@ int tokens_per_gate(const void *gate, int64_t gate_rows, int64_t T) {
   return (int)std::max<int64_t>(1, gate ? std::min(gate_rows, T) : T);
 }
 
-int64_t gates(int64_t T, int64_t gate_rows) { return gate_rows < 1 ? 0 : (T + gate_rows - 1) / gate_rows; }
+// (a gate's tokens are clamped before they are added to T: gate_rows may be any 64-bit number)
+int64_t gates(int64_t T, int64_t gate_rows) {
+  if (gate_rows < 1 || T < 1) return 0;
+  const int64_t rows = std::min(gate_rows, T);
+  return (T + rows - 1) / rows;
+}
 
 w4a16::NormGradDesc norm_grad_desc(const w4a16_norm_backward_call &c) {
   w4a16::NormGradDesc d = {};
