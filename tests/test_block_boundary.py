@@ -248,7 +248,7 @@ def test_gate_of_an_empty_batch():
     import torch
     for shape, want in (((64,), (64,)), ((1, 64), (1, 64)), ((0, 64), (0, 64))):
         assert ex._gate_shape(torch.zeros(shape), None, 0, 64)[0] == want
-    assert ex._gate_shape(torch.zeros(1, 64), 5, 0, 64) == ((1, 64), 5)
+    assert ex._gate_shape(torch.zeros(1, 64), 5, 0, 64)[0] == (1, 64)
     assert ex._gate_shape(torch.zeros(2, 64), 5, 0, 64)[0] == (0, 64)      # refused: two rows for no token
 
 
@@ -259,3 +259,11 @@ def test_one_gate_for_all_is_checked_whatever_its_rows(rows):
         assert norm_rc(gate_rows=rows, **kw) == -1
     for kw in (dict(dx=at(4)), dict(dy=at(4) + 64), dict(dgate=at(4)), dict(dgate=at(9) + 256), dict(dgate=at(2))):
         assert norm_backward_rc(gate_rows=rows, **kw) == -1
+
+
+@pytest.mark.parametrize("rows", [5, 1 << 40, 1 << 63, (1 << 64) + 1])
+def test_gate_rows_reach_the_library_whole(rows):
+    """Rows past 64 bits would wrap on their way (2^64 + 1 to a gate vector per token, of which one is there)."""
+    import torch
+    shape, n = ex._gate_shape(torch.zeros(1, 8), rows, 5, 8)
+    assert shape == (1, 8) and ex.NormCallStruct(gate_rows=n).gate_rows >= 5

@@ -142,6 +142,7 @@ def _gate_shape(gate, gate_rows, T, D):
         gate_rows = max(T, 1) if gate.shape[0] == 1 else 1
     if gate_rows < 1:
         raise ValueError("gate_rows must be at least 1")
+    gate_rows = min(gate_rows, max(T, 1))  # (the same gates, and a number of 64 bits)
     if T == 0 and gate.shape[0] == 1:
         return (1, D), gate_rows
     return (-(-T // gate_rows), D), gate_rows
