@@ -267,3 +267,20 @@ def test_gate_rows_reach_the_library_whole(rows):
     import torch
     shape, n = ex._gate_shape(torch.zeros(1, 8), rows, 5, 8)
     assert shape == (1, 8) and ex.NormCallStruct(gate_rows=n).gate_rows >= 5
+
+
+def test_norm_block_without_work_checks_its_arguments():
+    """Without y, pre and alpha there is nothing to launch; what is refused beside them is refused here too."""
+    import torch
+    x = torch.zeros(4, 8, dtype=torch.float16)
+    for alpha in (1.0, 0.5):
+        for kw in (dict(post=w4.Norm()), dict(gate=x[0]), dict(post=w4.Norm(w4.NORM_LAYER), gate=x)):
+            with pytest.raises(ValueError):
+                w4.w4a16_norm_block(x, alpha=alpha, **kw)
+        for bad in (x, x.float(), None):
+            with pytest.raises(TypeError):
+                w4.w4a16_norm_block(bad, alpha=alpha)
+        with pytest.raises(ValueError):
+            w4.w4a16_norm_block(x.clone().requires_grad_(), alpha=alpha)
+        with pytest.raises(ValueError):
+            w4.w4a16_norm_block(x[0], alpha=alpha)

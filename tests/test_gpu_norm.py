@@ -238,6 +238,17 @@ def test_no_tokens_with_a_gate(rows, how):
     assert grads.gate.shape == gate.shape and bool((grads.gate == 0).all())
 
 
+def test_nothing_to_do_returns_the_input():
+    torch = torch_cuda()
+    x = torch.randn(3, 40, device="cuda").half()
+    r, h = w4.w4a16_norm_block(x)
+    assert r is x and h is None
+    r, h = w4.w4a16_norm_block(x, post=w4.Norm(w4.NORM_NONE))
+    assert r is x and h is None
+    with pytest.raises(ValueError):
+        w4.w4a16_norm_block(x.t())
+
+
 # ---- backward --------------------------------------------------------------------------------
 
 def grad_error(d, v, kind, eps, e_d):

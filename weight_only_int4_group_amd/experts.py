@@ -174,10 +174,14 @@ def w4a16_norm_block(x, y=None, post=None, pre=None, gate=None, gate_rows=None, 
     """(r, h) = (alpha * x + gate * post(y), pre(r)) on the current stream; h is None without
     pre, and r is x itself where y is None and alpha is 1.  Arguments as for NormBlockCall."""
     torch = _torch()
+    _act_dtype(x, "x")
+    if y is None and (gate is not None or (post is not None and post.kind != NORM_NONE)):
+        raise ValueError("post and gate need y")
     r = x if y is None and alpha == 1.0 else torch.empty_like(x)
     h = torch.empty_like(x) if pre is not None else None
+    call = NormBlockCall(x, y, None if r is x else r, h, post, pre, gate, gate_rows, alpha)
     if r is not x or h is not None:
-        NormBlockCall(x, y, None if r is x else r, h, post, pre, gate, gate_rows, alpha)()
+        call()
     return r, h
 
 
