@@ -72,6 +72,16 @@ def test_groups_and_bias(E, groups, topk_groups, k, score):
     check_route(t, v, k, bias, score=score, renormalize=False)
 
 
+@pytest.mark.parametrize("E,groups,topk_groups,k", [(192, 64, 3, 6), (320, 64, 63, 20), (576, 64, 1, 4), (130, 2, 1, 5)])
+def test_lanes_past_the_last_group(E, groups, topk_groups, k):
+    """A wave has more lanes than experts, whose group would be the 64th and more."""
+    t, v = logits_of(5, E, "fp32", 9)
+    bias = (np.random.default_rng(E).standard_normal(E) * 0.2).astype(np.float32)
+    for b in (None, bias):
+        for score in ("softmax", "sigmoid"):
+            check_route(t, v, k, b, score=score, groups=groups, topk_groups=topk_groups)
+
+
 @pytest.mark.parametrize("E", [16, 100, 512])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_ties_go_to_the_lowest_index(E, dtype):

@@ -35,7 +35,6 @@ namespace w4a16 {
 namespace {
 
 constexpr int kTokens = 4;  // waves, and so tokens, per workgroup
-constexpr int kNone = 0x7fffffff;
 
 template <int CTRL, int ROWS>
 __device__ __forceinline__ uint32_t dpp(uint32_t v) {
@@ -232,8 +231,8 @@ __global__ __launch_bounds__(64 * kTokens) void route_kernel(RouteDesc P) {
         if (lane == first) value = 0;
       }
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (!(kept >> ((lane + 64 * i) / size) & 1)) key[i] = 0;
+      for (int i = 0; i < VPL; ++i)  // (past E, where the keys are 0, groups may be numbered 64 and more)
+        if (!(kept >> ((lane + 64 * i) / size & 63) & 1)) key[i] = 0;
     }
   }
 
