@@ -200,8 +200,8 @@ __global__ __launch_bounds__(64 * kTokens) void route_kernel(RouteDesc P) {
       __shared__ uint64_t keys[kTokens][64 * VPL];
 #pragma unroll
       for (int i = 0; i < VPL; ++i) keys[wave][lane + 64 * i] = key[i];
-      // (a wave's own LDS: written and read in order)
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      // (a wave's own LDS: written and read in order, also by the compiler)
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       // `per` lanes a group (a power of two), each over every per-th of its experts
       int per = 64;
       while (per * P.groups > 64) per /= 2;
