@@ -360,6 +360,21 @@ def test_backward_many_rows():
     run_backward(20000, 24, "bf16", "layer", "none", gate_rows=3)
 
 
+@pytest.mark.parametrize("post", block.KINDS)
+@pytest.mark.parametrize("gate_rows", [64, 1000])
+@pytest.mark.parametrize("D", [77, 8200])
+def test_backward_long_gates_of_rows_in_two_passes(D, gate_rows, post):
+    """Widths whose sums have a kernel of their own, gates of several strips of rows, the last one cut short."""
+    run_backward(203, D, "fp16" if D == 77 else "bf16", post, "rms", gate_rows=gate_rows, alpha=0.7)
+
+
+def test_backward_many_rows_in_two_passes():
+    """As above with strips of more than eight rows; and strips of several gates, the last one cut short."""
+    run_backward(40001, 17, "fp16", "rms", "layer", gate_rows=9000)
+    run_backward(40001, 13, "bf16", "layer", "none", gate_rows=3)
+    run_backward(4200, 8200, "bf16", "rms", "none", gate_rows=1000)
+
+
 def test_backward_against_differences():
     """dx and dy of a few elements against differences of the forward's fp64 values through the
     library's own rows (an fp16 step of 1/16 about a smooth point)."""
