@@ -454,3 +454,13 @@ def test_graphs_streams_and_workspaces():
             call()
         side.synchronize()
         assert torch.equal(other, want[0])
+
+
+@pytest.mark.parametrize("T,E,k,kind", [(50, 130, 8, "skip"), (448, 512, 8, "even"), (3, 1024, 64, "even")])
+def test_every_expert_has_weights_of_its_own(monkeypatch, T, E, k, kind):
+    """Stacks whose seeds lie further apart than there are experts: no expert of one has the weights of another
+    expert of another stack."""
+    plain = stack
+    monkeypatch.setitem(globals(), "stack", lambda key, *shape: plain(20 * key, *shape))
+    run_forward(T, E, k, 128, 128, "fp16", kind=kind, s=True, train=True)
+    run_backward(T, E, k, 128, 128, "bf16", kind=kind, f32=True)
