@@ -623,9 +623,11 @@ int w4a16_route_backward(const w4a16_routing *routing, const void *dweights, con
  * slot that names no expert are not written.
  * X * s is rounded to the activations' type once (not without s), and so are H, G, U and
  * Y; sums are held in fp32.  Weights are not rounded: codes are multiplied exactly, scales
- * and zero points applied to the fp32 sums of their group.  (Only where an expert
- * gets more than 56 slots on average may each weight be rounded once to the activations'
- * type instead, as in the dense products.)  An infinite activation may give NaN.
+ * and zero points applied to the fp32 sums of their group.  (Only where T * k > 56 E, slots
+ * that name no expert counted with the others, may each weight be rounded once to the
+ * activations' type instead, as in the dense products.)  In fp16 an H past 65504 becomes
+ * infinite.  An activation that is infinite, or past 2^112 (with scales above 1: past 2^112
+ * over the scale), may give NaN.
  * 0 <= T <= 2^22, 1 <= E <= 1024, 1 <= k <= 64, D and N multiples of 128 up to 2^20 with
  * N * D / 2 < 2^31 - 2^20 (EINVAL).  workspace: w4a16_experts_workspace_size() bytes
  * (it depends on T, E, k, D, N and whether s is set), 256-byte aligned; EINVAL if smaller.

@@ -293,7 +293,9 @@ __device__ __forceinline__ void store_16x32(float *stage, int lane, int row0, in
 }
 
 // 16 rows of G and U (and H from them), 32 columns from n0: g and u hold two 16-column
-// blocks each.  SLOT(row) is a tile's row's slot, HROW(row) its row of H.
+// blocks each.  SLOT(row) is a tile's row's slot, HROW(row) its row of H.  H is rounded because it
+// is the next product's MFMA operand: Y's error 2.9e-4 rather than 2.1e-4 in fp16, 2.35e-3 rather
+// than 1.66e-3 in bf16.
 template <bool BF, typename SLOT, typename HROW>
 __device__ __forceinline__ void store_gated(const ExpertArgs &P, const ExpertTile &tile, float *stage, int lane, int row0,
                                             int n0, const float4v (&g)[2], const float4v (&u)[2], SLOT &&slot_of,
@@ -347,7 +349,7 @@ __device__ __forceinline__ void store_rows(SLOT &&slot_of, const float *weights,
 // order).  Bound by HBM: every weight is read once per tile.  Codes and activations
 // come straight into registers, DEPTH groups of 128 ahead, with no barrier until the end;
 // rows past the tile's are not loaded (their offset lies past the resource).  One token, 2 of 8
-// experts of 14336 x 4096 (bf16): gate and up 29.6 us (4.2 TB/s), down 15.8 (3.9).
+// experts of 14336 x 4096 (bf16): gate and up 29.5-29.9 us (4.2 TB/s), down 16.0 (3.9).
 template <int TN, int KS, int EPI, bool GATHER, bool BF>
 __global__ __launch_bounds__(64 * KS) __attribute__((amdgpu_waves_per_eu(TN == 2 ? 4 : 3))) void expert_stream_kernel(ExpertArgs P) {
   constexpr int DEPTH = 2;
@@ -472,7 +474,7 @@ __global__ __launch_bounds__(64 * KS) __attribute__((amdgpu_waves_per_eu(TN == 2
 // half of what their four MFMAs take.  The sums of a group's activations, which the zero
 // points multiply, are MFMAs with ones: wave i takes those of row block i, and they reach
 // the other waves through LDS a stage later.  64 tokens, 8 of 64 experts of 1024 x 4096 (fp16, 32
-// rows): gate and up 58 us (4.9 TB/s of weights), down 36.6 (3.9, and 8 MB written); 48 rows
+// rows): gate and up 58-60 us (4.7-4.9 TB/s of weights), down 37-38.5 (3.7-3.8, and 8 MB written); 48 rows
 // per expert and more are bound by the issue of vector instructions (4.35 to an MFMA).
 template <int TM, int EPI, bool GATHER, bool BF>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void expert_tile_kernel(ExpertArgs P) {
@@ -699,9 +701,11 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 // them: each weight is rounded to the activations' type, as in the dense layers, and the
 // MFMAs add to the sums at once.  Decoding a weight costs three times as much that way,
 // shared by twice the rows, and no FMAs follow the MFMAs.  4096 tokens, 8 of 64 experts of
-// 1024 x 4096 (bf16): gate and up 560-600 us (550 GFLOP), down 395-410 (275 GFLOP, 537 MB written); by
+// 1024 x 4096 (bf16): gate and up 598-609 us (550 GFLOP), down 411-423 (275 GFLOP, 537 MB written); by
 // 64 rows with exact codes 663 and 453.  MFMAs and vector instructions take turns (41% and 31%
-// of the time).
+// of the time).  What the rounding costs (16 experts of 2560 x 3584, error of Y against 64 bits in
+// the 2-norm): 4.2e-4 in fp16 and 3.7e-3 in bf16, with exact codes 2.9e-4 and 2.35e-3; rounding Y
+// alone is 2.1e-4 and 1.66e-3.
 template <int EPI, bool GATHER, bool BF>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void expert_wide_kernel(ExpertArgs P) {
   constexpr int TM = 8, TN = 4, BM = 16 * TM, STEP = EPI == kGatedOut ? 2 : 1;
@@ -870,8 +874,10 @@ struct ExpertGradArgs {
 // with DMA loads, the wave's code tiles into registers, all one stage ahead.  The scale
 // varies along the contraction here, so it cannot multiply the sums: each weight is
 // rounded once to the activations' type, which the MFMA takes, as in the dense layers'
-// backward.  2048 tokens, 2 of 8 experts of 14336 x 4096 (bf16): dG and dU 583-593 us (481
-// GFLOP), rows 988-1003 (962 GFLOP).  (Scheduling barriers that pin the loads before the
+// backward; dG and dU are rounded because they are MFMA operands too.  Both together take the error of dX
+// from 2.1e-4 to 3.8e-4 (fp16) and from 1.66e-3 to 3.3e-3 (bf16; 16 experts of 2560 x 3584).
+// 2048 tokens, 2 of 8 experts of 14336 x 4096 (bf16): dG and dU 591-605 us (481
+// GFLOP), rows 1001-1017 (962 GFLOP).  (Scheduling barriers that pin the loads before the
 // MFMAs made the bf16 instances of 128 rows spill: 938 and 861 us on equal work without.)
 template <int TM, int EPI, bool GATHER, bool BF>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void expert_grad_kernel(ExpertGradArgs P) {
@@ -1152,7 +1158,9 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs P) {
   *reinterpret_cast<u16x4 *>(static_cast<uint16_t *>(P.out) + at) = out;
 }
 
-// X * s, rounded once, eight columns per thread.
+// X * s, rounded once, eight columns per thread: an MFMA operand has 16 bits, and the product's other half
+// would be a second MFMA for each.  The error of G and U goes from 2.1e-4 to 2.9e-4 (fp16) and from
+// 1.66e-3 to 2.35e-3 (bf16), that of Y from 2.9e-4 to 4.2e-4 and from 2.35e-3 to 3.3e-3.
 template <bool BF>
 __global__ __launch_bounds__(256) void expert_prescale_kernel(const uint16_t *X, const _Float16 *s, uint16_t *out,
                                                               int K, long long octets) {
@@ -1201,6 +1209,8 @@ int round_tokens(int T, int k, int D) {
 //                                    rows 24: 227 by 32, 265 by 64; 32: 348, 265
 //                                    rows 48: 290 by 64, 343 by 128; 64: 426, 350
 //   16 of 1536 x 2048                rows 64: 87 by 32, 90 by 64          rows 256: 156 by 64, 162 by 128; 512: 282, 259
+// Slots that name no expert count in S, since the host cannot tell them: 512 slots of which 71 name one
+// of 8 experts of 14336 x 4096 take 321 us, those 71 alone 168 (and a seventh of the workspace).
 int tile_rows(int S, int E, int columns, int most16, int enough) {
   const long long chosen = std::min(E, S);
   if (S <= most16 * chosen) return 16;

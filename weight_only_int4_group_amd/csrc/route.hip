@@ -24,9 +24,10 @@
 //
 // Bound by vector instructions: a choice is a maximum over the wave for each of the k, a score an
 // fp64 exponential.  One token of 64 experts takes 2.8 us (a launch); 8192 tokens, 8 of 256
-// experts each, fp32: 8.3 us by the logits, 13.9 with a bias (64-bit keys), 18.5 with groups
-// too, for a read of 8 MB; their backward 8.0.  (32-bit keys where all of a token's values
-// differ in them, with the rest as before, and sorted lists per lane: 17.5 to 18.9 with groups.)
+// experts each, fp32: 8.4-8.7 us by the logits, 13.5 (sigmoid) and 15.3 (softmax) with a bias (64-bit
+// keys), 18.2 and 19.9 with groups too, for a read of 8 MB; their backward 7.9-8.9.  (32-bit keys where
+// all of a token's values differ in them, with the rest as before, and sorted lists per lane: sigmoid
+// with groups 17.5 to 18.9.)
 #include "epilogue.h"
 #include "w4a16_device.h"
 #include "w4a16_internal.h"
