@@ -116,7 +116,7 @@ constexpr int kPlanThreads = 1024;  // and the most experts
 // Counts per expert, their prefix sums (and those of their tiles), then each slot to its
 // place.  A workgroup places a share of the slots and counts all of them, those before its
 // share apart, so none waits for another: placing is what takes long, a store to a
-// line of its own for each slot.  32768 slots over 64 experts: 8.1 us, and by
+// line of its own for each slot.  32768 slots over 64 experts: 8.4 us, and by
 // one workgroup 21.
 __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int32_t *ids, int S, int E, int tile_rows,
                                                             int32_t *order, ExpertTile *tiles,
@@ -349,7 +349,7 @@ __device__ __forceinline__ void store_rows(SLOT &&slot_of, const float *weights,
 // order).  Bound by HBM: every weight is read once per tile.  Codes and activations
 // come straight into registers, DEPTH groups of 128 ahead, with no barrier until the end;
 // rows past the tile's are not loaded (their offset lies past the resource).  One token, 2 of 8
-// experts of 14336 x 4096 (bf16): gate and up 29.5-29.9 us (4.2 TB/s), down 16.0 (3.9).
+// experts of 14336 x 4096 (bf16): gate and up 29.5-30.2 us (4.1-4.2 TB/s), down 15.9-16.2 (3.9).
 template <int TN, int KS, int EPI, bool GATHER, bool BF>
 __global__ __launch_bounds__(64 * KS) __attribute__((amdgpu_waves_per_eu(TN == 2 ? 4 : 3))) void expert_stream_kernel(ExpertArgs P) {
   constexpr int DEPTH = 2;
@@ -876,8 +876,8 @@ struct ExpertGradArgs {
 // rounded once to the activations' type, which the MFMA takes, as in the dense layers'
 // backward; dG and dU are rounded because they are MFMA operands too.  Both together take the error of dX
 // from 2.1e-4 to 3.8e-4 (fp16) and from 1.66e-3 to 3.3e-3 (bf16; 16 experts of 2560 x 3584).
-// 2048 tokens, 2 of 8 experts of 14336 x 4096 (bf16): dG and dU 591-605 us (481
-// GFLOP), rows 1001-1017 (962 GFLOP).  (Scheduling barriers that pin the loads before the
+// 2048 tokens, 2 of 8 experts of 14336 x 4096 (bf16): dG and dU 590-605 us (481
+// GFLOP), rows 1000-1017 (962 GFLOP).  (Scheduling barriers that pin the loads before the
 // MFMAs made the bf16 instances of 128 rows spill: 938 and 861 us on equal work without.)
 template <int TM, int EPI, bool GATHER, bool BF>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void expert_grad_kernel(ExpertGradArgs P) {

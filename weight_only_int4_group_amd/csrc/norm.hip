@@ -173,7 +173,7 @@ __device__ __forceinline__ void affine(float (&v)[CPT], const void *weight, cons
 }
 
 // One row per TPR threads.  One row of 4096: 2.9 us, which is a launch and two
-// reductions; 4096 x 8192 with both norms (bf16): 41.6 us, 6.4 TB/s of what it reads and writes.
+// reductions; 4096 x 8192 with both norms (bf16): 41.3-41.7 us, 6.4 TB/s of what it reads and writes.
 template <int TPR, int CPT, bool BF, bool VEC>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormDesc P) {
   constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
@@ -263,7 +263,7 @@ __device__ __forceinline__ const NormGradArgs &args_again() {
 
 // Bound by HBM, and at this occupancy (four waves per SIMD, of 128 registers) by a row's four
 // reductions in turn: 4092 x 4096 with layer norms and gates (bf16), 201 MB and 42 of the
-// strips' sums, takes 59 us (4.1 TB/s).
+// strips' sums, takes 58-63 us (3.9-4.2 TB/s).
 // SUMS: a strip of rows per workgroup, one row at a time with the next one's loads in
 // flight.  A thread keeps its columns' sums over the strip, so the sums cost one
 // fp32 row per strip; norm_sum_kernel adds the strips in order.
@@ -575,7 +575,7 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 // Strips of a backward call: about 2^18 threads of them (four waves per SIMD), of at
 // least 8 rows; within one gate vector's rows each, or of whole ones.  The backward of
-// 4092 x 4096 (layer norms and four gates, bf16) takes 59 + 8 us so, and with half as
+// 4092 x 4096 (layer norms and four gates, bf16) takes 58 to 63 + 8 us so, and with half as
 // many strips 75 + 5 (two rows at a time there, for 176 registers: 73 + 5).
 struct NormPlan {
   bool fused;  // the sums are taken where the rows are
