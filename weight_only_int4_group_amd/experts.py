@@ -234,18 +234,22 @@ class NormBlockBackwardCall(_PreparedCall):
         nbytes = self._size("w4a16_norm_block_backward_workspace_size", ctypes.byref(self.call))
         self._prepare(device, nbytes, workspace, stream)
         self._bind("w4a16_norm_block_backward", ctypes.byref(self.call))
-        # (of no tokens the C call sees a gate of no rows, and writes none)
-        self.unwritten = g.gate if T == 0 else None
+        if T == 0 and g.gate is not None:
+            self.function = self._with_zeros(self.function, g.gate, device)
 
-    def __call__(self):
-        super().__call__()
-        if self.unwritten is None:
-            return
+    @staticmethod
+    def _with_zeros(function, dgate, device):
+        """Of no tokens the C call sees a gate of no rows and writes none: zeros, on the stream it gets."""
         torch = _torch()
-        stream = (torch.cuda.current_stream(self.device) if self.stream is None
-                  else torch.cuda.ExternalStream(self.stream.value or 0, self.device))
-        with torch.cuda.stream(stream):
-            self.unwritten.zero_()
+
+        def call(*args):
+            rc = function(*args)
+            if not rc:
+                handle = getattr(args[-1], "value", args[-1]) or 0
+                with torch.cuda.stream(torch.cuda.ExternalStream(handle, device)):
+                    dgate.zero_()
+            return rc
+        return call
 
 
 def w4a16_norm_block_backward(dr, dh, y=None, r=None, post=None, pre=None, gate=None, gate_rows=None,
